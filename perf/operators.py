@@ -142,7 +142,8 @@ def _make_logits(case, g, n):
 def _undecided(case, logits, bias):
     """Rows whose choice hangs on the last bits of a float32: two different values next to each
     other in the order of the first K + 1 experts (or of the groups) are almost equal."""
-    keys, gk, _ = _choice64(case, logits, bias)
+    keys, gk, scores = _choice64(case, logits, bias)
+    loud = scores.max(-1, keepdim=True).values  # sums of a score and a bias may cancel
     top = torch.sort(keys, -1, descending=True).values[:, :case["K"] + 1]
     sets = [top]
     if gk is not None:
@@ -151,7 +152,8 @@ def _undecided(case, logits, bias):
     for v in sets:
         hi, lo = v[:, :-1], v[:, 1:]
         gap = hi - lo
-        near = (lo > -math.inf) & (gap > 0) & (gap < 4e-6 * torch.maximum(hi.abs(), lo.abs()))
+        near = (lo > -math.inf) & (gap > 0) & \
+            (gap < 4e-6 * torch.maximum(torch.maximum(hi.abs(), lo.abs()), loud))
         bad |= near.any(-1)
     return bad
 
