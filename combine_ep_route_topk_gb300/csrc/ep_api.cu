@@ -395,6 +395,150 @@ ep_status_t ep_route_dispatch(const float* logits, const int32_t* rank_offsets, 
     return cuda_status(launch_dispatch(m, s));
 }
 
+ep_status_t ep_gate_topk(const void* logits, ep_dtype_t logits_dtype, int32_t N, int32_t E,
+                         int32_t K, ep_score_t score, const float* bias, int32_t groups,
+                         int32_t topk_groups, int32_t group_top, int32_t renorm, float scale,
+                         const int32_t* expert_map, int32_t* topk_idx, float* topk_w,
+                         void* stream) {
+    ep_status_t st = check_sizes(N, E, K);
+    if (st != EP_OK) return st;
+    if (logits_dtype != EP_DTYPE_F32 && logits_dtype != EP_DTYPE_BF16) return EP_ERR_INVALID_ARG;
+    if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID) return EP_ERR_INVALID_ARG;
+    if (groups < 1 || E % groups != 0) return EP_ERR_INVALID_ARG;
+    if (groups > kMaxGroups) return EP_ERR_UNSUPPORTED;
+    if (topk_groups < 1 || topk_groups > groups) return EP_ERR_INVALID_ARG;
+    if ((int64_t)topk_groups * (E / groups) < K) return EP_ERR_INVALID_ARG;
+    if (group_top != 1 && group_top != 2) return EP_ERR_INVALID_ARG;
+    if (N > 0 && (!logits || !topk_idx || !topk_w)) return EP_ERR_INVALID_ARG;
+    const bool bf16 = logits_dtype == EP_DTYPE_BF16;
+    if ((reinterpret_cast<uintptr_t>(logits) & (bf16 ? 1u : 3u)) != 0) return EP_ERR_INVALID_ARG;
+    if (!aligned4(bias) || !aligned4(expert_map) || !aligned4(topk_idx) || !aligned4(topk_w))
+        return EP_ERR_INVALID_ARG;
+    GateArgs a;
+    a.logits = logits;
+    a.bias = bias;
+    a.emap = expert_map;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.scale = scale;
+    a.N = N;
+    a.E = E;
+    a.K = K;
+    a.score = (int)score;
+    a.groups = topk_groups == groups ? 1 : groups;  // nothing to choose between
+    a.topk_groups = topk_groups;
+    a.group_top = group_top;
+    a.renorm = renorm != 0;
+    a.bf16 = bf16;
+    a.vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & (bf16 ? 7u : 15u)) == 0;
+    return cuda_status(launch_gate(a, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_gate_topk_backward(const float* d_topk_w, const void* logits,
+                                  ep_dtype_t logits_dtype, const int32_t* topk_idx, int32_t N,
+                                  int32_t E, int32_t K, ep_score_t score, int32_t renorm,
+                                  float scale, const int32_t* expert_map, void* d_logits,
+                                  void* stream) {
+    ep_status_t st = check_sizes(N, E, K);
+    if (st != EP_OK) return st;
+    if (logits_dtype != EP_DTYPE_F32 && logits_dtype != EP_DTYPE_BF16) return EP_ERR_INVALID_ARG;
+    if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID) return EP_ERR_INVALID_ARG;
+    if (N > 0 && (!d_topk_w || !logits || !topk_idx || !d_logits)) return EP_ERR_INVALID_ARG;
+    const bool bf16 = logits_dtype == EP_DTYPE_BF16;
+    const uintptr_t both = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(d_logits);
+    if ((both & (bf16 ? 1u : 3u)) != 0) return EP_ERR_INVALID_ARG;
+    if (!aligned4(d_topk_w) || !aligned4(topk_idx) || !aligned4(expert_map))
+        return EP_ERR_INVALID_ARG;
+    GateGradArgs a;
+    a.d_w = d_topk_w;
+    a.logits = logits;
+    a.topk_idx = topk_idx;
+    a.emap = expert_map;
+    a.d_logits = d_logits;
+    a.scale = scale;
+    a.N = N;
+    a.E = E;
+    a.K = K;
+    a.score = (int)score;
+    a.renorm = renorm != 0;
+    a.bf16 = bf16;
+    a.vec = E % 4 == 0 && (both & (bf16 ? 7u : 15u)) == 0;
+    return cuda_status(launch_gate_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_quantize_rows(const void* x, ep_dtype_t x_dtype, ep_act_t act, int32_t rows,
+                             int32_t cols, const int32_t* expert_offsets, int32_t E,
+                             ep_layout_t layout, int32_t cap, int8_t* q, float* scales,
+                             void* stream) {
+    if (rows < 0 || cols < 16 || cols % 16 != 0) return EP_ERR_INVALID_ARG;
+    if (x_dtype != EP_DTYPE_F32 && x_dtype != EP_DTYPE_BF16) return EP_ERR_INVALID_ARG;
+    if (act != EP_ACT_NONE && act != EP_ACT_SWIGLU) return EP_ERR_INVALID_ARG;
+    if (layout != EP_LAYOUT_CONTIG && layout != EP_LAYOUT_MASKED) return EP_ERR_INVALID_ARG;
+    if (cols > INT32_MAX / 2) return EP_ERR_UNSUPPORTED;
+    if (expert_offsets) {
+        if (E < 1) return EP_ERR_INVALID_ARG;
+        if (E > kMaxE) return EP_ERR_UNSUPPORTED;
+        if (layout == EP_LAYOUT_MASKED && (cap < 1 || (int64_t)E * cap != rows))
+            return EP_ERR_INVALID_ARG;
+    }
+    if (rows > 0 && (!x || !q || !scales)) return EP_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned4(scales) || !aligned4(expert_offsets))
+        return EP_ERR_INVALID_ARG;
+    QuantArgs a;
+    a.x = x;
+    a.expert_offsets = expert_offsets;
+    a.q = q;
+    a.scales = scales;
+    a.rows = rows;
+    a.cols = cols;
+    a.E = E;
+    a.cap = cap;
+    a.layout = (int)layout;
+    a.swiglu = act == EP_ACT_SWIGLU;
+    a.bf16 = x_dtype == EP_DTYPE_BF16;
+    return cuda_status(launch_quantize(a, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_rows,
+                             const int8_t* w, const float* w_scales, int32_t E, int32_t Nc,
+                             int32_t Kd, const int32_t* expert_offsets, ep_layout_t layout,
+                             int32_t cap, int32_t rows, const int32_t* row_src, int32_t n_src,
+                             ep_dtype_t out_dtype, void* out, int32_t* status, void* stream) {
+    if (E < 1 || Nc < 1 || rows < 0 || x_rows < 0 || Kd < 16 || Kd % 16 != 0)
+        return EP_ERR_INVALID_ARG;
+    if (layout != EP_LAYOUT_CONTIG && layout != EP_LAYOUT_MASKED) return EP_ERR_INVALID_ARG;
+    if (out_dtype != EP_DTYPE_BF16 && out_dtype != EP_DTYPE_F32) return EP_ERR_INVALID_ARG;
+    if (E > kMaxE || Kd > kMaxMatmulK || (int64_t)E * Nc > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    if (layout == EP_LAYOUT_MASKED && (cap < 1 || (int64_t)E * cap != rows))
+        return EP_ERR_INVALID_ARG;
+    if (row_src ? n_src < 0 : x_rows != rows) return EP_ERR_INVALID_ARG;
+    if (!expert_offsets || (rows > 0 && (!w || !w_scales || !out))) return EP_ERR_INVALID_ARG;
+    if (rows > 0 && x_rows > 0 && (!x || !x_scales)) return EP_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(out)) return EP_ERR_INVALID_ARG;
+    const void* ptrs[] = {x_scales, w_scales, expert_offsets, row_src, status};
+    for (const void* p : ptrs)
+        if (!aligned4(p)) return EP_ERR_INVALID_ARG;
+    MatmulArgs a;
+    a.x = x;
+    a.x_scales = x_scales;
+    a.w = w;
+    a.w_scales = w_scales;
+    a.expert_offsets = expert_offsets;
+    a.row_src = row_src;
+    a.out = out;
+    a.status = status;
+    a.x_rows = x_rows;
+    a.n_src = n_src;
+    a.rows = rows;
+    a.E = E;
+    a.Nc = Nc;
+    a.Kd = Kd;
+    a.cap = cap;
+    a.layout = (int)layout;
+    a.out_bf16 = out_dtype == EP_DTYPE_BF16;
+    return cuda_status(launch_expert_matmul(a, static_cast<cudaStream_t>(stream)));
+}
+
 ep_status_t ep_selftest_wait_timeout(int32_t* status, void* workspace, size_t ws_bytes,
                                      void* stream) {
     if (!status || !workspace || ws_bytes < sizeof(unsigned)) return EP_ERR_INVALID_ARG;

@@ -166,4 +166,59 @@ bool route_dispatch_fits(int N, int E, int K, int R);
 size_t route_dispatch_hist_bytes(int N, int E);
 cudaError_t launch_route_dispatch(const RouteDispatchArgs& a, cudaStream_t s);
 
+// ---- gate ------------------------------------------------------------------
+constexpr int kScoreSoftmax = 0;
+constexpr int kScoreSigmoid = 1;
+constexpr int kMaxGroups = 32;
+
+struct GateArgs {
+    const void* logits;         // float32, or bf16 when bf16 != 0
+    const float* bias;          // or nullptr
+    const int32_t* emap;        // or nullptr
+    int32_t* topk_idx;
+    float* topk_w;
+    float scale;
+    int N, E, K, score, groups, topk_groups, group_top, renorm;
+    int bf16;
+    int vec;                    // rows start on a boundary of 4 elements
+};
+cudaError_t launch_gate(const GateArgs& a, cudaStream_t s);
+
+struct GateGradArgs {
+    const float* d_w;
+    const void* logits;
+    const int32_t* topk_idx;
+    const int32_t* emap;
+    void* d_logits;             // the logits' type
+    float scale;
+    int N, E, K, score, renorm;
+    int bf16, vec;              // as in GateArgs (logits and d_logits)
+};
+cudaError_t launch_gate_backward(const GateGradArgs& a, cudaStream_t s);
+
+// ---- 8-bit rows and the experts' products -----------------------------------
+constexpr int kMaxMatmulK = 65536;  // 2^16 products of at most 2^14 fit 31 bits
+
+struct QuantArgs {
+    const void* x;
+    const int32_t* expert_offsets;  // or nullptr: every row is quantised
+    int8_t* q;
+    float* scales;
+    int rows, cols, E, cap, layout, swiglu, bf16;
+};
+cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t s);
+
+struct MatmulArgs {
+    const int8_t* x;
+    const float* x_scales;
+    const int8_t* w;
+    const float* w_scales;
+    const int32_t* expert_offsets;
+    const int32_t* row_src;     // or nullptr: x rows lie where the output rows do
+    void* out;
+    int32_t* status;            // or nullptr
+    int x_rows, n_src, rows, E, Nc, Kd, cap, layout, out_bf16;
+};
+cudaError_t launch_expert_matmul(const MatmulArgs& a, cudaStream_t s);
+
 }  // namespace ep

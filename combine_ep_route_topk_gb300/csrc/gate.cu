@@ -1,0 +1,416 @@
+// Gate of an expert layer for sm_103a: scores, balance bias, groups, top-K and
+// weights (ep_gate_topk), and the gradient of the weights with respect to the
+// logits (ep_gate_topk_backward).
+//
+//   s_e   = 1 / (1 + exp(-l_e))                  (sigmoid), or
+//           exp(l_e - m) / sum_a exp(l_a - m)    (softmax over available experts)
+//   key_e = s_e + bias_e, or l_e without a bias (the scores grow with l)
+//   group score = largest key of the group, or the sum of its two largest
+//           s_e + bias_e; only experts of the best topk_groups groups remain
+//   picks = the K largest keys, ties to the lower id
+//   w_k   = scale * s_k [/ sum of the picks' s]
+//
+// One warp per token.  Lane i holds the VPL consecutive experts i*VPL ..
+// i*VPL + VPL-1 as order-preserving 32-bit keys in registers, so that a lower
+// lane always means lower ids: a round of the selection is one redux.sync max
+// over the lanes' best keys, a ballot, and the lowest lane that holds the
+// maximum wins.  Lanes cache their three best slots and rescan after a third
+// win.  Scores are recomputed for the picks alone.
+#include <cuda_bf16.h>
+
+#include <cfloat>
+
+#include "ep_kernels.cuh"
+
+namespace ep {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kGateWarps = 8;  // tokens per block
+
+// Larger float -> larger key; -0 folds onto +0.  Key 0 means "not available".
+__device__ __forceinline__ uint32_t order_key(float v) {
+    uint32_t u = __float_as_uint(v);
+    if (u == 0x80000000u) u = 0u;
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// False for NaN and -inf.
+__device__ __forceinline__ bool available(float v) { return v > -INFINITY; }
+
+// A logit as the formulas use it: +inf counts as the largest finite number, so
+// that no score is inf / inf.
+__device__ __forceinline__ float clamp_logit(float v) { return fminf(v, FLT_MAX); }
+
+__device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
+
+__device__ __forceinline__ float load_one(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load_one(const __nv_bfloat16* p) {
+    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
+}
+
+__device__ __forceinline__ void load_four(const float* p, float* v) {
+    const float4 q = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+}
+__device__ __forceinline__ void load_four(const __nv_bfloat16* p, float* v) {
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+    v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+    return v;
+}
+
+// The share s_k / sum_j s_j of the lane's pick (logit l) among the warp's
+// picks; 0 on lanes without one.  The scores are taken relative to the largest
+// pick's, exp(l - c) with c = max l for the softmax and min(0, max l) for the
+// sigmoid, so that no sum underflows however far below the others' the picks'
+// scores lie.
+__device__ __forceinline__ float pick_share(float l, bool picked, int score) {
+    float c = warp_max(picked ? l : -INFINITY);
+    float s = 0.0f;
+    if (score == kScoreSigmoid) {
+        c = fminf(c, 0.0f);
+        // l <= 0: exp(l) / (1 + exp(l)); l > 0 (then c = 0): 1 / (1 + exp(-l))
+        if (picked) s = l > 0.0f ? sigmoid(l) : __fdiv_rn(expf(l - c), 1.0f + expf(l));
+    } else if (picked) {
+        s = expf(l - c);
+    }
+    const float sum = warp_sum(s);  // at least 1/2 where anything is picked
+    return picked ? __fdiv_rn(s, sum) : 0.0f;
+}
+
+// The lane's VPL logits (NaN past E), four at a time where rows allow it.
+template <int VPL, typename T>
+__device__ __forceinline__ void load_row(const T* row, int E, bool vec, int lane, float (&v)[VPL]) {
+    const int e0 = lane * VPL;
+    if constexpr (VPL >= 4) {
+        if (vec) {
+#pragma unroll
+            for (int j = 0; j < VPL; j += 4) {
+                if (e0 + j < E) {
+                    load_four(row + e0 + j, &v[j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[j + i] = __int_as_float(0x7fffffff);
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+        v[j] = (e0 + j < E) ? load_one(row + e0 + j) : __int_as_float(0x7fffffff);
+}
+
+// Insert slot j into the sorted triple (key descending, slot ascending).
+__device__ __forceinline__ void insert3(int j, uint32_t x, int& s0, uint32_t& b0, int& s1,
+                                        uint32_t& b1, int& s2, uint32_t& b2) {
+    if (x > b0) {
+        s2 = s1; b2 = b1;
+        s1 = s0; b1 = b0;
+        s0 = j;  b0 = x;
+    } else if (x > b1) {
+        s2 = s1; b2 = b1;
+        s1 = j;  b1 = x;
+    } else if (x > b2) {
+        s2 = j;  b2 = x;
+    }
+}
+
+__device__ __forceinline__ void two_best(float x, float& a, float& b) {
+    b = fmaxf(b, fminf(a, x));
+    a = fmaxf(a, x);
+}
+
+template <int VPL, typename T>
+__global__ void __launch_bounds__(kGateWarps * 32)
+gate_kernel(GateArgs a) {
+    extern __shared__ float s_choice[];  // [warps][E], only for groups that cross lanes unevenly
+    pdl_prologue();
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    const int t = blockIdx.x * kGateWarps + warp;
+    if (t >= a.N) return;  // warp-uniform
+    const int E = a.E, K = a.K;
+    const T* row = static_cast<const T*>(a.logits) + (size_t)t * E;
+    const int e0 = lane * VPL;
+
+    float v[VPL];
+    load_row<VPL>(row, E, a.vec != 0, lane, v);
+
+    // softmax: the largest available logit, and the sum where a score is needed
+    const bool groups_sum = a.groups > 1 && a.group_top == 2;
+    const bool all_scores = a.bias != nullptr || groups_sum;
+    float m = 0.0f, total = 1.0f;
+    if (a.score == kScoreSoftmax) {
+        m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (available(v[j])) m = fmaxf(m, clamp_logit(v[j]));
+        m = warp_max(m);
+        if (all_scores || !a.renorm) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (available(v[j])) sum += expf(clamp_logit(v[j]) - m);
+            total = warp_sum(sum);
+        }
+    }
+
+    // keys, and the groups' scores
+    uint32_t key[VPL];
+    float c[VPL];  // s + bias, where groups are scored by sums
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        const float l = clamp_logit(v[j]);
+        float x = l;
+        bool ok = available(v[j]);
+        c[j] = -INFINITY;
+        if (all_scores && ok) {
+            x = a.score == kScoreSigmoid ? sigmoid(l) : __fdiv_rn(expf(l - m), total);
+            if (a.bias != nullptr) x += __ldg(a.bias + e0 + j);
+            ok = available(x);
+            if (ok) c[j] = x;
+            if (a.bias == nullptr) x = l;
+        }
+        key[j] = ok ? order_key(x) : 0u;
+    }
+    if (a.groups > 1) {
+        const int per = E / a.groups;
+        float* mine = s_choice + (size_t)warp * E;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j < E) {
+                float x = c[j];
+                if (!groups_sum) x = key[j] == 0u ? -INFINITY : (all_scores ? c[j] : clamp_logit(v[j]));
+                mine[e0 + j] = x;
+            }
+        __syncwarp();
+        float best = -INFINITY, second = -INFINITY;
+        if (lane < a.groups) {
+            int i = lane % per;  // start apart, so that the lanes' banks differ
+            for (int n = 0; n < per; ++n) {
+                two_best(mine[lane * per + i], best, second);
+                i = i + 1 == per ? 0 : i + 1;
+            }
+            if (groups_sum && second > -INFINITY) best += second;
+        }
+        int before = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const float o = __shfl_sync(kFull, best, g);
+            before += (o > best || (o == best && g < lane)) ? 1 : 0;
+        }
+        const unsigned kept = __ballot_sync(kFull, lane < a.groups && before < a.topk_groups);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j < E && !(kept >> ((e0 + j) / per) & 1u)) key[j] = 0u;
+    }
+
+    int s0 = 0, s1 = 0, s2 = 0;
+    uint32_t b0 = 0u, b1 = 0u, b2 = 0u;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) insert3(j, key[j], s0, b0, s1, b1, s2, b2);
+    int my_id = -1;
+    for (int k = 0; k < K; ++k) {
+        const uint32_t top = __reduce_max_sync(kFull, b0);
+        if (top == 0u) break;  // no expert left
+        const int win = __ffs(__ballot_sync(kFull, b0 == top)) - 1;
+        const int id = __shfl_sync(kFull, e0 + s0, win);
+        if (lane == k) my_id = id;
+        const bool won = lane == win;
+        const uint32_t lk = b0;
+        const int ls = s0;
+        if (won) {
+            s0 = s1; b0 = b1;
+            s1 = s2; b1 = b2;
+            b2 = 0u;
+        }
+        if (VPL > 3 && __any_sync(kFull, won && b0 == 0u)) {
+            if (won && b0 == 0u) {  // the next three after (lk, ls)
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    if (key[j] < lk || (key[j] == lk && j > ls)) insert3(j, key[j], s0, b0, s1, b1, s2, b2);
+            }
+        }
+    }
+
+    float l = -INFINITY, s = 0.0f;
+    if (my_id >= 0) l = clamp_logit(load_one(row + my_id));
+    if (a.renorm) {
+        s = pick_share(l, my_id >= 0, a.score);
+    } else if (my_id >= 0) {
+        s = a.score == kScoreSigmoid ? sigmoid(l) : __fdiv_rn(expf(l - m), total);
+    }
+    if (lane < K) {
+        int id = my_id;
+        if (id >= 0 && a.emap != nullptr) {
+            id = __ldg(a.emap + id);
+            if (id < 0 || id >= E) id = -1;
+        }
+        a.topk_idx[(size_t)t * K + lane] = id;
+        a.topk_w[(size_t)t * K + lane] = s * a.scale;
+    }
+}
+
+template <typename T>
+cudaError_t launch_gate_t(const GateArgs& a, cudaStream_t s) {
+    const dim3 grid((a.N + kGateWarps - 1) / kGateWarps), block(kGateWarps * 32);
+    const size_t smem = a.groups > 1 ? sizeof(float) * kGateWarps * a.E : 0;
+    if (a.E <= 32) return launch(gate_kernel<1, T>, grid, block, smem, s, a);
+    if (a.E <= 64) return launch(gate_kernel<2, T>, grid, block, smem, s, a);
+    if (a.E <= 128) return launch(gate_kernel<4, T>, grid, block, smem, s, a);
+    if (a.E <= 256) return launch(gate_kernel<8, T>, grid, block, smem, s, a);
+    if (a.E <= 512) return launch(gate_kernel<16, T>, grid, block, smem, s, a);
+    return launch(gate_kernel<32, T>, grid, block, smem, s, a);
+}
+
+// ---- gradient ---------------------------------------------------------------
+//
+// With g_k the gradient of weight k, c the scale, q_k = s_k / sum_j s_j and
+// h_k = c g_k - sum_j c g_j q_j:
+//   sigmoid, renormalised   dl_k = h_k q_k (1 - s_k)
+//   softmax, renormalised   dl_k = h_k q_k   (the full sum cancels)
+//   sigmoid                 dl_k = c g_k s_k (1 - s_k)
+//   softmax                 dl_e = s_e (c g_e - sum_j c g_j s_j), every expert
+// and 0 elsewhere.  The choice of the experts and the bias are constants.
+
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_four(float* p, float4 v) {
+    *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void store_four(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    uint2 q;
+    q.x = *reinterpret_cast<const uint32_t*>(&lo);
+    q.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(p) = q;
+}
+
+// One warp per token; the row's gradient is put together in shared memory
+// (zeros, then the picks) and stored once.
+template <typename T>
+__global__ void __launch_bounds__(kGateWarps * 32)
+gate_backward_kernel(GateGradArgs a) {
+    extern __shared__ float4 s_rows4[];
+    float* s_rows = reinterpret_cast<float*>(s_rows4);
+    pdl_prologue();
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    const int E = a.E, K = a.K;
+    const int pitch = (E + 3) & ~3;
+    float* mine = s_rows + (size_t)warp * pitch;
+    int* inv = reinterpret_cast<int*>(s_rows + (size_t)kGateWarps * pitch);
+    if (a.emap != nullptr) {  // new id -> old id; the lowest old id where several map to one
+        for (int e = threadIdx.x; e < E; e += kGateWarps * 32) inv[e] = E;
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += kGateWarps * 32) {
+            const int to = __ldg(a.emap + e);
+            if (to >= 0 && to < E) atomicMin(inv + to, e);
+        }
+        __syncthreads();
+    }
+    const int t = blockIdx.x * kGateWarps + warp;
+    if (t >= a.N) return;  // warp-uniform
+    const T* row = static_cast<const T*>(a.logits) + (size_t)t * E;
+    T* out = static_cast<T*>(a.d_logits) + (size_t)t * E;
+
+    int id = -1;
+    float g = 0.0f, l = -INFINITY;
+    if (lane < K) {
+        id = __ldg(a.topk_idx + (size_t)t * K + lane);
+        if (id < 0 || id >= E) id = -1;
+        if (id >= 0 && a.emap != nullptr) {
+            id = inv[id];
+            if (id >= E) id = -1;
+        }
+        if (id >= 0) {
+            g = a.scale * __ldg(a.d_w + (size_t)t * K + lane);
+            l = load_one(row + id);
+            if (!available(l)) id = -1, g = 0.0f;
+        }
+    }
+    for (int e = lane * 4; e < pitch; e += 128)
+        *reinterpret_cast<float4*>(mine + e) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __syncwarp();
+
+    l = clamp_logit(l);
+    float d = 0.0f;
+    if (a.renorm) {
+        const float q = pick_share(l, id >= 0, a.score);
+        d = (g - warp_sum(g * q)) * q;
+        if (a.score == kScoreSigmoid && id >= 0) d *= sigmoid(-l);  // 1 - s, without cancellation
+    } else if (a.score == kScoreSigmoid) {
+        const float e = expf(-fabsf(l));
+        if (id >= 0) d = g * __fdiv_rn(e, (1.0f + e) * (1.0f + e));  // s (1 - s), likewise
+    } else {
+        d = g;
+    }
+    if (id >= 0) mine[id] = d;
+    __syncwarp();
+
+    if (a.score == kScoreSoftmax && !a.renorm) {
+        float m = -INFINITY;
+        for (int e = lane; e < E; e += 32) {
+            const float x = load_one(row + e);
+            if (available(x)) m = fmaxf(m, clamp_logit(x));
+        }
+        m = warp_max(m);
+        float sum = 0.0f, dot = 0.0f;
+        for (int e = lane; e < E; e += 32) {
+            const float x = load_one(row + e);
+            const float p = available(x) ? expf(clamp_logit(x) - m) : 0.0f;
+            sum += p;
+            dot += p * mine[e];
+        }
+        sum = warp_sum(sum);
+        dot = warp_sum(dot);
+        const float inv_sum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+        dot *= inv_sum;
+        for (int e = lane; e < E; e += 32) {
+            const float x = load_one(row + e);
+            const float p = available(x) ? expf(clamp_logit(x) - m) * inv_sum : 0.0f;
+            mine[e] = p * (mine[e] - dot);
+        }
+        __syncwarp();
+    }
+    if (a.vec) {
+        for (int e = lane * 4; e < E; e += 128)
+            store_four(out + e, *reinterpret_cast<const float4*>(mine + e));
+    } else {
+        for (int e = lane; e < E; e += 32) store_one(out + e, mine[e]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_gate(const GateArgs& a, cudaStream_t s) {
+    if (a.N == 0) return cudaSuccess;
+    const cudaError_t err = a.bf16 ? launch_gate_t<__nv_bfloat16>(a, s) : launch_gate_t<float>(a, s);
+    note_launch();
+    return err;
+}
+
+cudaError_t launch_gate_backward(const GateGradArgs& a, cudaStream_t s) {
+    if (a.N == 0) return cudaSuccess;
+    const dim3 grid((a.N + kGateWarps - 1) / kGateWarps), block(kGateWarps * 32);
+    const size_t smem = sizeof(float) * kGateWarps * ((a.E + 3) & ~3) +
+                        (a.emap != nullptr ? sizeof(int) * a.E : 0);
+    const cudaError_t err = a.bf16
+        ? launch(gate_backward_kernel<__nv_bfloat16>, grid, block, smem, s, a)
+        : launch(gate_backward_kernel<float>, grid, block, smem, s, a);
+    note_launch();
+    return err;
+}
+
+}  // namespace ep

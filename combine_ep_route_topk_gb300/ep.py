@@ -22,6 +22,13 @@ EP_LAYOUT_CONTIG = 0
 EP_LAYOUT_MASKED = 1
 EP_DTYPE_BF16 = 0
 EP_DTYPE_FP8_E4M3_B128 = 1
+EP_DTYPE_F32 = 2
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+EP_ACT_NONE = 0
+EP_ACT_SWIGLU = 1
+
+_FLOATS = {torch.bfloat16: EP_DTYPE_BF16, torch.float32: EP_DTYPE_F32}
 
 _lib = None
 
@@ -78,6 +85,16 @@ def lib():
         L.ep_host_free.restype = ctypes.c_int
         for f in ("ep_route_topk", "ep_expert_balance_map", "ep_dispatch_layout", "ep_dispatch",
                   "ep_combine"):
+            getattr(L, f).restype = ctypes.c_int
+        f32, enum = ctypes.c_float, ctypes.c_int
+        L.ep_gate_topk.argtypes = [P, enum, i32, i32, i32, enum, P, i32, i32, i32, i32, f32, P, P,
+                                   P, P]
+        L.ep_gate_topk_backward.argtypes = [P, P, enum, P, i32, i32, i32, enum, i32, f32, P, P, P]
+        L.ep_quantize_rows.argtypes = [P, enum, enum, i32, i32, P, i32, enum, i32, P, P, P]
+        L.ep_expert_matmul.argtypes = [P, P, i32, P, P, i32, i32, i32, P, enum, i32, i32, P, i32,
+                                       enum, P, P, P]
+        for f in ("ep_gate_topk", "ep_gate_topk_backward", "ep_quantize_rows",
+                  "ep_expert_matmul"):
             getattr(L, f).restype = ctypes.c_int
         L.ep_status_string.argtypes = [ctypes.c_int]
         L.ep_status_string.restype = ctypes.c_char_p
@@ -334,6 +351,104 @@ def ep_combine(y, topk_idx, topk_w, pos, expert_offsets, E, layout=EP_LAYOUT_CON
         _dev(topk_w, torch.float32, "topk_w", (N, K)), _dev(pos, torch.int32, "pos", (N, K)),
         _opt(expert_offsets, torch.int32, "expert_offsets", (E + 1,)), layout, cap,
         _dev(out, torch.bfloat16, "out", (N, H)), _stream(stream)))
+    return out
+
+
+def _float_type(t, name):
+    d = _FLOATS.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if d is None:
+        raise EPError(f"{name} must be a bfloat16 or float32 tensor")
+    return d
+
+
+def ep_gate_topk(logits, K, score=EP_SCORE_SOFTMAX, bias=None, groups=1, topk_groups=None,
+                 group_top=2, renorm=True, scale=1.0, expert_map=None, topk_idx=None,
+                 topk_w=None, stream=None):
+    """logits bf16 or float32 [N, E] -> (topk_idx int32 [N, K], topk_w float32
+    [N, K]): softmax or sigmoid scores, optional balance bias [E] on the choice
+    alone, the best topk_groups of `groups` groups, the K best experts, their
+    scores (renormalised) times scale."""
+    N, E = logits.shape
+    dt = _float_type(logits, "logits")
+    if topk_idx is None:
+        topk_idx = _empty((N, K), torch.int32, logits)
+    if topk_w is None:
+        topk_w = _empty((N, K), torch.float32, logits)
+    _check("ep_gate_topk", lib().ep_gate_topk(
+        _dev(logits, logits.dtype, "logits"), dt, N, E, K, score,
+        _opt(bias, torch.float32, "bias", (E,)), groups,
+        groups if topk_groups is None else topk_groups, group_top, int(renorm), scale,
+        _opt(expert_map, torch.int32, "expert_map", (E,)),
+        _dev(topk_idx, torch.int32, "topk_idx", (N, K)),
+        _dev(topk_w, torch.float32, "topk_w", (N, K)), _stream(stream)))
+    return topk_idx, topk_w
+
+
+def ep_gate_topk_backward(d_topk_w, logits, topk_idx, score=EP_SCORE_SOFTMAX, renorm=True,
+                          scale=1.0, expert_map=None, d_logits=None, stream=None):
+    """Gradient of ep_gate_topk's weights: d_topk_w float32 [N, K] -> d_logits
+    [N, E] of the logits' type."""
+    N, E = logits.shape
+    K = topk_idx.shape[1]
+    dt = _float_type(logits, "logits")
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+    _check("ep_gate_topk_backward", lib().ep_gate_topk_backward(
+        _dev(d_topk_w, torch.float32, "d_topk_w", (N, K)), _dev(logits, logits.dtype, "logits"),
+        dt, _dev(topk_idx, torch.int32, "topk_idx", (N, K)), N, E, K, score, int(renorm), scale,
+        _opt(expert_map, torch.int32, "expert_map", (E,)),
+        _dev(d_logits, logits.dtype, "d_logits", (N, E)), _stream(stream)))
+    return d_logits
+
+
+def ep_quantize_rows(x, act=EP_ACT_NONE, expert_offsets=None, layout=EP_LAYOUT_CONTIG, cap=0,
+                     q=None, scales=None, stream=None):
+    """x bf16 or float32 [rows, cols] (EP_ACT_SWIGLU: [rows, 2*cols]) -> (q int8
+    [rows, cols], scales float32 [rows]).  With expert_offsets, rows that hold
+    no token are skipped."""
+    rows, wide = x.shape
+    cols = wide // 2 if act == EP_ACT_SWIGLU else wide
+    dt = _float_type(x, "x")
+    if act == EP_ACT_SWIGLU and wide % 2:
+        raise EPError("x must have an even number of columns for SwiGLU")
+    if q is None:
+        q = _empty((rows, cols), torch.int8, x)
+    if scales is None:
+        scales = _empty((rows,), torch.float32, x)
+    _check("ep_quantize_rows", lib().ep_quantize_rows(
+        _dev(x, x.dtype, "x"), dt, act, rows, cols,
+        _opt(expert_offsets, torch.int32, "expert_offsets"),
+        0 if expert_offsets is None else expert_offsets.numel() - 1, layout, cap,
+        _dev(q, torch.int8, "q", (rows, cols)), _dev(scales, torch.float32, "scales", (rows,)),
+        _stream(stream)))
+    return q, scales
+
+
+def ep_expert_matmul(x, x_scales, w, w_scales, expert_offsets, layout=EP_LAYOUT_CONTIG, cap=0,
+                     row_src=None, out=None, out_dtype=torch.bfloat16, status=None, stream=None):
+    """Every expert's rows times its weights: x int8 [x_rows, Kd], x_scales
+    float32 [x_rows], w int8 [E, Nc, Kd], w_scales float32 [E, Nc] -> out bf16
+    or float32 [rows, Nc] ([E*cap, Nc] for the masked layout).  With row_src
+    (the layout's), x holds token rows.  Rows that hold no token are not
+    written."""
+    E, Nc, Kd = w.shape
+    x_rows = x.shape[0]
+    if layout == EP_LAYOUT_MASKED:
+        rows = E * cap
+    else:
+        rows = x_rows if row_src is None else row_src.numel()
+    if out is None:
+        out = _empty((rows, Nc), out_dtype, x)
+    elif out.numel() != rows * Nc:
+        raise EPError(f"out must hold {rows} x {Nc} elements")
+    dt = _float_type(out, "out")
+    _check("ep_expert_matmul", lib().ep_expert_matmul(
+        _dev(x, torch.int8, "x", (x_rows, Kd)),
+        _dev(x_scales, torch.float32, "x_scales", (x_rows,)), x_rows, _dev(w, torch.int8, "w"),
+        _dev(w_scales, torch.float32, "w_scales", (E, Nc)), E, Nc, Kd,
+        _dev(expert_offsets, torch.int32, "expert_offsets", (E + 1,)), layout, cap, rows,
+        _opt(row_src, torch.int32, "row_src"), 0 if row_src is None else row_src.numel(), dt,
+        _dev(out, out.dtype, "out"), _opt(status, torch.int32, "status", (1,)), _stream(stream)))
     return out
 
 

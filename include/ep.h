@@ -85,8 +85,19 @@ typedef enum {
 
 typedef enum {
     EP_DTYPE_BF16 = 0,          /* rows copied as bf16 */
-    EP_DTYPE_FP8_E4M3_B128 = 1  /* E4M3 codes + one float scale per 128 columns */
+    EP_DTYPE_FP8_E4M3_B128 = 1, /* E4M3 codes + one float scale per 128 columns */
+    EP_DTYPE_F32 = 2            /* float32 (gate logits, rows, expert outputs) */
 } ep_dtype_t;
+
+typedef enum {
+    EP_SCORE_SOFTMAX = 0,
+    EP_SCORE_SIGMOID = 1
+} ep_score_t;
+
+typedef enum {
+    EP_ACT_NONE = 0,
+    EP_ACT_SWIGLU = 1           /* silu(first half) * second half */
+} ep_act_t;
 
 /*
  * ep_route_topk -- [Anatomy] "What we have to do": each token's router
@@ -321,6 +332,114 @@ ep_status_t ep_route_dispatch(const float* logits, const int32_t* rank_offsets, 
                               int32_t* masked_m, int32_t* overflow_count, void* out,
                               float* out_scales, void* workspace, size_t ws_bytes,
                               void* stream);
+
+/*
+ * ep_gate_topk -- the gate of an expert layer with scores, a bias for balance,
+ * groups, top-K and renormalised weights; an addition of this library next to
+ * ep_route_topk (whose gate is logits order and a softmax over the picks).
+ * Its outputs feed ep_dispatch_layout, ep_dispatch and ep_combine.  Per token:
+ *   s_e    = 1 / (1 + exp(-l_e))  (EP_SCORE_SIGMOID), or the softmax of the
+ *            logits over the available experts  (EP_SCORE_SOFTMAX).
+ *   key_e  = s_e + bias_e; without a bias l_e itself (the scores' order).
+ *   groups: the E experts are `groups` sets of E/groups consecutive ones.  A
+ *            group's score is its largest key (group_top 1) or the sum of its
+ *            two largest s_e + bias_e (group_top 2; of one, where it has but
+ *            one available).  Only the experts of the topk_groups best groups
+ *            (ties: lower group) can be picked.
+ *   picks  = the K largest keys, descending, ties to the lower id (-0.0
+ *            equals +0.0).
+ *   w_k    = scale * s_k / sum_j s_j over the picks (renorm != 0; taken
+ *            relative to the largest, so that scores too small for a float32
+ *            keep their shares), or scale * s_k.  The bias moves the choice,
+ *            never the weights.
+ * An expert whose logit or key is -inf or NaN is not available: it is never
+ * picked and takes no part in the softmax.  Where fewer than K are available,
+ * the remaining picks are -1 with weight 0 ("no pick" for the layout).  A
+ * logit of +inf counts as the largest finite float.
+ *   logits     [N, E] float32 or bf16 (logits_dtype), row-major.
+ *   bias       float32 [E] or NULL.
+ *   expert_map int32 [E] or NULL, as for ep_route_topk.
+ *   topk_idx   int32 [N, K], topk_w float32 [N, K] out.
+ * Scores and sums are float32.  Limits: groups <= 32, E % groups == 0,
+ * topk_groups * (E / groups) >= K, besides those above.
+ */
+ep_status_t ep_gate_topk(const void* logits, ep_dtype_t logits_dtype, int32_t N, int32_t E,
+                         int32_t K, ep_score_t score, const float* bias, int32_t groups,
+                         int32_t topk_groups, int32_t group_top, int32_t renorm, float scale,
+                         const int32_t* expert_map, int32_t* topk_idx, float* topk_w,
+                         void* stream);
+
+/*
+ * ep_gate_topk_backward -- gradient of ep_gate_topk's weights with respect to
+ * the logits, for training.  The choice of the experts (hence the bias and the
+ * groups) is constant; the scores are recomputed from the logits.
+ *   d_topk_w   float32 [N, K]: gradient of each weight.
+ *   logits, logits_dtype, score, renorm, scale   as in the forward call.
+ *   topk_idx   int32 [N, K] as ep_gate_topk wrote it; a token's ids are
+ *              distinct, ids outside [0, E) are "no pick" and get nothing.
+ *   expert_map the forward call's, or NULL: the ids are then mapped back (to
+ *              the lowest expert, should several map to one id).
+ *   d_logits   [N, E] out, of the logits' type, every element written: 0 for
+ *              experts that no weight depends on.  Must not overlap logits.
+ */
+ep_status_t ep_gate_topk_backward(const float* d_topk_w, const void* logits,
+                                  ep_dtype_t logits_dtype, const int32_t* topk_idx, int32_t N,
+                                  int32_t E, int32_t K, ep_score_t score, int32_t renorm,
+                                  float scale, const int32_t* expert_map, void* d_logits,
+                                  void* stream);
+
+/*
+ * ep_quantize_rows -- rows to 8-bit integers with one scale per row, as
+ * ep_expert_matmul reads them; an addition of this library.
+ *   v      = x (EP_ACT_NONE), or silu(x[:cols]) * x[cols:] (EP_ACT_SWIGLU, x
+ *            rows of 2*cols: the experts' first product, gate half first).
+ *   scale  = max|v| / 127 (1 for a row of zeros); q = v * (127 / max|v|)
+ *            rounded to nearest even.  The rows hold finite values.
+ *   x      [rows, cols or 2*cols] float32 or bf16, 16-byte aligned.
+ *   expert_offsets int32 [E+1] of the layout, or NULL for every row.  When
+ *            given, rows that hold no token (CONTIG: from expert_offsets[E]
+ *            on; MASKED, rows == E*cap: slots past the expert's count) are
+ *            neither read nor written.
+ *   q      int8 [rows, cols], 16-byte aligned; scales float32 [rows].
+ * cols is a multiple of 16.
+ */
+ep_status_t ep_quantize_rows(const void* x, ep_dtype_t x_dtype, ep_act_t act, int32_t rows,
+                             int32_t cols, const int32_t* expert_offsets, int32_t E,
+                             ep_layout_t layout, int32_t cap, int8_t* q, float* scales,
+                             void* stream);
+
+/*
+ * ep_expert_matmul -- every expert's product of its rows with its own weights,
+ * in 8-bit integers with a scale for each row and each output channel; an
+ * addition of this library.  For each row r of expert e:
+ *   out[r, n] = x_scales[s] * w_scales[e, n] * sum_k x[s, k] * w[e, n, k]
+ * with the sum kept in 32 bits, the scales applied in float32 and one rounding
+ * to the output's type.  Rows lie as ep_dispatch lays them:
+ *   CONTIG  out is [rows, Nc]; expert e owns rows expert_offsets[e] ..
+ *           expert_offsets[e+1]-1.
+ *   MASKED  out is [E, cap, Nc] (rows == E*cap); expert e owns its first
+ *           min(expert_offsets[e+1] - expert_offsets[e], cap) slots.
+ *   Rows that hold no token are not written.
+ *   x       int8 [x_rows, Kd] with x_scales float32 [x_rows].  Without
+ *           row_src, s = r and x_rows == rows.
+ *   row_src int32 [n_src] or NULL: row r reads x row s = row_src[p], where p
+ *           is its position in expert-major order (CONTIG: r; MASKED:
+ *           expert_offsets[e] + slot), so the layout's row_src reads token
+ *           rows in place and no dispatched copy is needed.  An s outside
+ *           [0, x_rows) gives a row of zeros.
+ *   w       int8 [E, Nc, Kd] with w_scales float32 [E, Nc].
+ *   out     bf16 or float32 (out_dtype).
+ *   status  int32 [1] device or NULL: 0 when the call completed, 1 if one of
+ *           the kernel's bounded waits ran out (results then incomplete; its
+ *           waits are for its own copies and products, so this does not occur).
+ * x, w and out are 16-byte aligned.  Kd is a multiple of 16.  Limits: E <=
+ * 1024, Kd <= 65536, E*Nc <= 2^31 - 1.
+ */
+ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_rows,
+                             const int8_t* w, const float* w_scales, int32_t E, int32_t Nc,
+                             int32_t Kd, const int32_t* expert_offsets, ep_layout_t layout,
+                             int32_t cap, int32_t rows, const int32_t* row_src, int32_t n_src,
+                             ep_dtype_t out_dtype, void* out, int32_t* status, void* stream);
 
 /*
  * ep_host_pipeline_* -- no counterpart in the source pages: the path for
