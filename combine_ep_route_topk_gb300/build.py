@@ -18,9 +18,11 @@ LIB = os.path.join(HERE, "libep_gb300.so")
 SOURCES = ["ep_api.cu", "route_topk.cu", "layout.cu", "layout_cluster.cu", "layout_static.cu", "layout_small.cu",
            "host_pipeline.cu",
            "route_layout.cu", "route_dispatch.cu",
-           "dispatch.cu", "combine.cu", "gate.cu", "quantize.cu", "expert_matmul.cu"]
+           "dispatch.cu", "combine.cu", "gate.cu", "quantize.cu", "expert_matmul.cu",
+           "expert_matmul_tc.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("ep_kernels.cuh", "route_common.cuh",
-                                            "layout_common.cuh", "dispatch_common.cuh")] + [
+                                            "layout_common.cuh", "dispatch_common.cuh",
+                                            "expert_common.cuh")] + [
     os.path.join(ROOT, "include", "ep.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

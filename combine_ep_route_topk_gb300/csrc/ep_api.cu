@@ -508,7 +508,8 @@ ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_r
         return EP_ERR_INVALID_ARG;
     if (layout != EP_LAYOUT_CONTIG && layout != EP_LAYOUT_MASKED) return EP_ERR_INVALID_ARG;
     if (out_dtype != EP_DTYPE_BF16 && out_dtype != EP_DTYPE_F32) return EP_ERR_INVALID_ARG;
-    if (E > kMaxE || Kd > kMaxMatmulK || (int64_t)E * Nc > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    if (E > kMaxE || Kd > kMaxMatmulK || (int64_t)E * Nc > INT32_MAX - 256)
+        return EP_ERR_UNSUPPORTED;
     if (layout == EP_LAYOUT_MASKED && (cap < 1 || (int64_t)E * cap != rows))
         return EP_ERR_INVALID_ARG;
     if (row_src ? n_src < 0 : x_rows != rows) return EP_ERR_INVALID_ARG;

@@ -10,38 +10,17 @@
 // the block's 8 warps owns 4 channels, streams their weights with 16-byte
 // loads and multiplies them with the group's rows, staged in shared memory,
 // by dp4a.  Bound by the weight bytes while the experts have few rows.
-#include <cuda_bf16.h>
-
-#include "ep_kernels.cuh"
+#include "expert_common.cuh"
 
 namespace ep {
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
+using namespace mm;
+
 constexpr int kWarps = 8;
 constexpr int kRows = 8;       // rows per unit
 constexpr int kChannels = 4;   // channels per warp
 constexpr int kChunk = 2048;   // bytes of a row staged at a time
-
-// Rows [begin, end) of expert e in the expert-major order, for any contents of
-// the offsets: clamped to the rows that the buffers hold.
-__device__ __forceinline__ int expert_rows(const MatmulArgs& a, int e, int& begin) {
-    begin = __ldg(a.expert_offsets + e);
-    int end = __ldg(a.expert_offsets + e + 1);
-    const int limit = a.layout == 0 ? a.rows : INT32_MAX;
-    begin = max(0, min(begin, limit));
-    end = max(begin, min(end, limit));
-    return a.layout == 0 ? end - begin : min(end - begin, a.cap);
-}
-
-// Row of x that output row (begin, i) of expert e reads, -1 for none.
-__device__ __forceinline__ int source_row(const MatmulArgs& a, int e, int begin, int i) {
-    if (a.row_src == nullptr) return a.layout == 0 ? begin + i : e * a.cap + i;
-    const long long p = (long long)begin + i;
-    if (p >= a.n_src) return -1;
-    const int r = __ldg(a.row_src + p);
-    return (r >= 0 && r < a.x_rows) ? r : -1;
-}
 
 __device__ __forceinline__ void store_out(const MatmulArgs& a, size_t at, float v) {
     if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
@@ -57,44 +36,13 @@ matmul_rows_kernel(MatmulArgs a) {
     pdl_prologue();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (a.status != nullptr && blockIdx.x == 0 && tid == 0) *a.status = 0;
-    // prefix of the row groups over the experts, 4 experts a thread
-    int n[4], sum = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int e = tid * 4 + j;
-        int begin;
-        n[j] = e < a.E ? (expert_rows(a, e, begin) + kRows - 1) / kRows : 0;
-        sum += n[j];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(kFull, incl, off);
-        if (lane >= off) incl += o;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    int run = incl - sum;
-    for (int w = 0; w < warp; ++w) run += s_warp[w];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int e = tid * 4 + j;
-        if (e < a.E) s_units[e] = run;
-        run += n[j];
-        if (e == a.E - 1) s_units[a.E] = run;
-    }
-    __syncthreads();
+    tile_prefix(a, kRows, s_units, s_warp);
 
     const int blocks_n = (a.Nc + kWarps * kChannels - 1) / (kWarps * kChannels);
     const long long units = (long long)s_units[a.E] * blocks_n;
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         const int group = (int)(u / blocks_n), nb = (int)(u % blocks_n);
-        int lo = 0, hi = a.E;  // s_units[lo] <= group < s_units[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_units[mid] <= group) lo = mid; else hi = mid;
-        }
-        const int e = lo;
+        const int e = expert_of_tile(s_units, a.E, group);
         int begin;
         const int rows_e = expert_rows(a, e, begin);
         const int first = (group - s_units[e]) * kRows;
@@ -151,7 +99,7 @@ matmul_rows_kernel(MatmulArgs a) {
         if (r < rows && ch < a.Nc) {
             const int src = s_src[r];
             const float xs = src >= 0 ? __ldg(a.x_scales + src) : 0.0f;
-            const size_t to = (a.layout == 0 ? (size_t)begin : (size_t)e * a.cap) + first + r;
+            const size_t to = first_row(a, e, begin) + first + r;
             store_out(a, to * a.Nc + ch, (float)mine * xs * __ldg(a.w_scales + (size_t)e * a.Nc + ch));
         }
         __syncthreads();  // s_src is rewritten by the next unit
@@ -163,7 +111,12 @@ matmul_rows_kernel(MatmulArgs a) {
 cudaError_t launch_expert_matmul(const MatmulArgs& a, cudaStream_t s) {
     if (a.rows == 0)
         return a.status != nullptr ? cudaMemsetAsync(a.status, 0, sizeof(int32_t), s) : cudaSuccess;
-    const cudaError_t err = launch(matmul_rows_kernel, dim3(sm_count() * 4), dim3(kWarps * 32), 0, s, a);
+    const int per = a.layout == 0 ? (a.rows + a.E - 1) / a.E : a.cap;  // rows per expert
+    cudaError_t err;
+    if (per <= 2)
+        err = launch(matmul_rows_kernel, dim3(sm_count() * 4), dim3(kWarps * 32), 0, s, a);
+    else
+        err = launch_matmul_tc(a, per > 128, s);
     note_launch();
     return err;
 }

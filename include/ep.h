@@ -433,7 +433,7 @@ ep_status_t ep_quantize_rows(const void* x, ep_dtype_t x_dtype, ep_act_t act, in
  *           the kernel's bounded waits ran out (results then incomplete; its
  *           waits are for its own copies and products, so this does not occur).
  * x, w and out are 16-byte aligned.  Kd is a multiple of 16.  Limits: E <=
- * 1024, Kd <= 65536, E*Nc <= 2^31 - 1.
+ * 1024, Kd <= 65536, E*Nc < 2^31 - 256.
  */
 ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_rows,
                              const int8_t* w, const float* w_scales, int32_t E, int32_t Nc,
