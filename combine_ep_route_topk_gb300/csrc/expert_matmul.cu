@@ -113,10 +113,10 @@ cudaError_t launch_expert_matmul(const MatmulArgs& a, cudaStream_t s) {
         return a.status != nullptr ? cudaMemsetAsync(a.status, 0, sizeof(int32_t), s) : cudaSuccess;
     const int per = a.layout == 0 ? (a.rows + a.E - 1) / a.E : a.cap;  // rows per expert
     cudaError_t err;
-    if (per <= 2)
+    if (per <= 2 || a.x_rows == 0)
         err = launch(matmul_rows_kernel, dim3(sm_count() * 4), dim3(kWarps * 32), 0, s, a);
     else
-        err = launch_matmul_tc(a, per > 128, s);
+        err = launch_matmul_tc(a, per, s);
     note_launch();
     return err;
 }

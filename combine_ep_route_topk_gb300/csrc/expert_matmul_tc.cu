@@ -10,14 +10,17 @@
 // exact; beyond, an addition rounds at 2^-24 relative, far below the output's.
 //
 // A tile is 128 channels a CTA (the M side: weights) x up to TN rows (the N
-// side).  CG = 1: one CTA, TN = 128, two accumulators.  CG = 2: a pair of CTAs
-// on 256 channels, TN = 256, each holding half of the rows' operand.
+// side).  CG = 1: one CTA.  CG = 2: a pair of CTAs on 256 channels, each
+// holding half of the rows' operand.
 //   TMA warp        weights, [128 channels x 128 bytes] boxes, 128-byte swizzle
-//   4 weight warps  shared memory -> float16 -> TMEM (the A operand's stages)
-//   4 row warps     x rows (gathered, L2) -> float16 -> shared memory (B);
-//                   warp w fills stage w, so four stages load at once
+//   2 copying warps x rows, wherever they lie, by 16-byte background copies
+//   8 weight warps  8-bit stages -> float16 -> TMEM (the A operand's stages)
+//   row warps       8-bit stages -> float16 -> shared memory (B)
 //   MMA warp        one thread issues 8 MMAs of K = 16 per stage
-//   4 output warps  TMEM -> scales -> bf16 / float32 -> rows of out
+//   8 output warps  TMEM -> scales -> bf16 / float32 -> rows of out
+// Within a block of 128 K, both operands hold the first 8 K of each 16 in one
+// half of a stage and the second 8 in the other (a sum's order is free): a row's
+// 8 lanes then store to 8 different banks' groups without exchanging halves.
 // The weights go through TMEM so that their float16 form costs no shared
 // memory bandwidth.  Every wait has a time limit: on expiry the CTA stops,
 // writes status 1, waits for its own copies and frees its TMEM.
@@ -32,19 +35,39 @@ namespace {
 
 using namespace mm;
 
-constexpr int kStages = 4;            // stages of converted operands
-constexpr int kWStages = 5;           // stages of 8-bit weights
+constexpr int kStages = 3;            // stages of converted operands
 constexpr int kBK = 128;              // K of a stage
-constexpr int kWBytes = 128 * kBK;    // one stage of weights
-constexpr int kBBytes = 128 * kBK * 2;  // one stage of rows, float16
-constexpr int kBAtom = 128 * 128;     // 64 K of 128 rows
-constexpr int kThreads = 14 * 32;
+constexpr int kWBytes = 128 * kBK;    // one stage of 8-bit weights
+constexpr int kOutWarps = 8, kWeightWarp0 = kOutWarps, kWeightWarps = 8;
+constexpr int kTmaWarp = kWeightWarp0 + kWeightWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kCopyWarp0 = kMmaWarp + 1, kCopyWarps = 2;
+constexpr int kRowWarp0 = kCopyWarp0 + kCopyWarps;  // a row warp for every 16 rows of a stage
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemA = 256;      // A stages start here: 64 columns each
+constexpr uint32_t kWaitHint = 2000;  // ns that one poll of a barrier may sleep
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
 
+// Rows per tile TN, of which each CTA of the CG holds kRows in shared memory.
+template <int CG_, int TN_>
+struct Shape {
+    static constexpr int CG = CG_, TN = TN_;
+    static constexpr int kRows = TN / CG;
+    static constexpr int kBAtom = kRows * 128;       // 64 K of the rows, float16
+    static constexpr int kBBytes = 2 * kBAtom;       // one stage
+    static constexpr int kXBytes = kRows * kBK;      // one stage of 8-bit rows
+    static constexpr int kWStages = kRows <= 64 ? 8 : 4;  // 8-bit weights in flight
+    static constexpr int kXStages = kRows <= 64 ? 4 : 3;  // 8-bit rows in flight
+    static constexpr int kRowWarps = kRows / 16;
+    static constexpr int kThreads = (kRowWarp0 + kRowWarps) * 32;
+    static constexpr int kAcc = TN <= 128 ? 2 : 1;   // accumulators of TN columns
+    static constexpr int kChannels = 128 * CG;
+    static constexpr int kGrain = 16 * CG;           // an MMA's N is a multiple
+};
+
+constexpr int kMaxWStages = 8, kMaxXStages = 4;
 struct Shared {
-    uint64_t w_full[kWStages], w_empty[kWStages];
+    uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
+    uint64_t x_full[kMaxXStages], x_empty[kMaxXStages];
     uint64_t full[kStages], empty[kStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drained;
@@ -53,7 +76,9 @@ struct Shared {
     int warp_sums[8];
     int tiles[kMaxE + 1];
 };
-constexpr int kSmemBytes = 1024 + kStages * kBBytes + kWStages * kWBytes + (int)sizeof(Shared);
+template <class S>
+constexpr int kSmemBytes = 1024 + kStages * S::kBBytes + S::kWStages * kWBytes + S::kXStages * S::kXBytes +
+                           (int)sizeof(Shared);
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return (uint32_t)__cvta_generic_to_shared(p);
@@ -67,9 +92,9 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
         "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
         "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        : "=r"(done) : "r"(bar), "r"(parity), "r"(kWaitHint) : "memory");
     return done != 0;
 }
 
@@ -89,13 +114,19 @@ __device__ __forceinline__ bool mbar_wait(Shared* sh, uint64_t* bar, uint32_t pa
     return true;
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
+
 // The same by a whole warp, with one answer.
 __device__ __forceinline__ bool mbar_wait_warp(Shared* sh, uint64_t* bar, uint32_t parity) {
     return __all_sync(kFull, mbar_wait(sh, bar, parity));
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Arrives on the barrier at the same place in the pair's first CTA.
@@ -107,7 +138,7 @@ __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
         asm volatile(
             "{\n.reg .b32 a;\n"
             "mapa.shared::cluster.u32 a, %0, 0;\n"
-            "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
+            "mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
             : "memory");
     }
 }
@@ -121,6 +152,26 @@ __device__ __forceinline__ void tma_load(const CUtensorMap* map, uint64_t* bar, 
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
         ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(k), "r"(row) : "memory");
+}
+
+// 16 bytes to shared memory, in the background (zeros where !on).
+__device__ __forceinline__ void copy16(uint32_t dst, const int8_t* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+// Arrives on the barrier once the thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Before a CTA that gave up ends, the copies of its last stages land (waited
+// for with the same limit); c stages were issued.
+template <int STAGES>
+__device__ __forceinline__ void drain_copies(uint64_t* full, uint32_t c) {
+    const uint32_t n = c < STAGES ? c : STAGES;
+    const long long start = clock64();
+    for (uint32_t i = c - n; i != c; ++i)
+        while (!mbar_try(smem_u32(&full[i % STAGES]), (i / STAGES) & 1))
+            if (clock64() - start > kWaitCycles) break;
 }
 
 template <int CG>
@@ -158,14 +209,12 @@ __device__ __forceinline__ void tmem_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16};"
         ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -189,6 +238,17 @@ __device__ __forceinline__ void widen4(uint32_t x, uint32_t& lo, uint32_t& hi) {
     asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
 }
 
+__device__ __forceinline__ uint4 load_shared(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_shared(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // K-major operand of 128-byte rows with the 128-byte swizzle: groups of 8 rows
 // are 1024 bytes apart.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
@@ -203,11 +263,9 @@ struct Unit {
     int n;           // rows rounded up to the MMA's granularity
 };
 
-template <int CG>
+template <class S>
 struct Tiles {
-    static constexpr int TN = 128 * CG;
-    static constexpr int kChannels = 128 * CG;
-    static constexpr int kGrain = 16 * CG;
+    static constexpr int kChannels = S::kChannels, kGrain = S::kGrain;
     int ct;           // channel tiles
     long long units;
 
@@ -233,16 +291,18 @@ struct Tiles {
     }
 };
 
-template <int CG>
-__global__ void __launch_bounds__(kThreads, 1)
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, 1)
 matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
+    constexpr int CG = S::CG, kAcc = S::kAcc, kWStages = S::kWStages, kXStages = S::kXStages;
+    constexpr int kBBytes = S::kBBytes, kBAtom = S::kBAtom;
     extern __shared__ uint8_t s_raw[];
     uint8_t* s_b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* s_w = s_b + kStages * kBBytes;
-    Shared* sh = reinterpret_cast<Shared*>(s_w + kWStages * kWBytes);
+    uint8_t* s_x = s_w + kWStages * kWBytes;
+    Shared* sh = reinterpret_cast<Shared*>(s_x + kXStages * S::kXBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;
-    constexpr int kAcc = CG == 1 ? 2 : 1;
 
     pdl_prologue();
     if (tid == 0) {
@@ -251,19 +311,23 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             mbar_init(&sh->w_full[i], 1);
             mbar_init(&sh->w_empty[i], 4);
         }
+        for (int i = 0; i < kXStages; ++i) {
+            mbar_init(&sh->x_full[i], kCopyWarps * 32);
+            mbar_init(&sh->x_empty[i], S::kRowWarps);
+        }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh->full[i], 5 * CG);
+            mbar_init(&sh->full[i], (4 + S::kRowWarps) * CG);
             mbar_init(&sh->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->acc_full[i], 1);
-            mbar_init(&sh->acc_empty[i], 4 * CG);
+            mbar_init(&sh->acc_empty[i], kOutWarps * CG);
         }
         mbar_init(&sh->drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (a.status != nullptr && blockIdx.x == 0) *a.status = 0;
     }
-    if (warp == 13) {
+    if (warp == kMmaWarp) {
         if constexpr (CG == 1)
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                          ::"r"(smem_u32(&sh->tmem)), "r"(kTmemCols) : "memory");
@@ -272,19 +336,19 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
                          ::"r"(smem_u32(&sh->tmem)), "r"(kTmemCols) : "memory");
     }
     tmem_fence_before();
-    tile_prefix(a, Tiles<CG>::TN, sh->tiles, sh->warp_sums);
+    tile_prefix(a, S::TN, sh->tiles, sh->warp_sums);
     if constexpr (CG == 2) {
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     tmem_fence_after();
     const uint32_t tmem = sh->tmem;
-    const Tiles<CG> tiles(a, sh);
+    const Tiles<S> tiles(a, sh);
     const int kblocks = (a.Kd + kBK - 1) / kBK;
     const long long u0 = blockIdx.x / CG, du = gridDim.x / CG;
 
-    if (warp == 12) {
-        // ---- weights: TMA ----
+    if (warp == kTmaWarp) {
+        // ---- weights: TMA boxes ----
         if (lane == 0) {
             uint32_t c = 0;  // stages issued so far
             bool ok = true;
@@ -292,25 +356,19 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
                 const Unit t = tiles.get(a, sh, u);
                 const int row = t.e * a.Nc + t.channel + rank * 128;
                 for (int kb = 0; kb < kblocks; ++kb, ++c) {
-                    const uint32_t s = c % kWStages, round = c / kWStages;
-                    ok = mbar_wait(sh, &sh->w_empty[s], (round & 1) ^ 1);
+                    const uint32_t s = c % kWStages;
+                    ok = mbar_wait(sh, &sh->w_empty[s], (c / kWStages & 1) ^ 1);
                     if (!ok) break;
                     mbar_expect_tx(&sh->w_full[s], kWBytes);
                     tma_load(&w_map, &sh->w_full[s], s_w + s * kWBytes, kb * kBK, row);
                 }
             }
-            if (!ok) {
-                // the copies still in flight land before the CTA ends
-                const uint32_t n = c < kWStages ? c : kWStages;
-                const long long start = clock64();
-                for (uint32_t i = c - n; i != c; ++i)
-                    while (!mbar_try(smem_u32(&sh->w_full[i % kWStages]), (i / kWStages) & 1))
-                        if (clock64() - start > kWaitCycles) break;
-            }
+            if (!ok) drain_copies<kWStages>(sh->w_full, c);
         }
-    } else if (warp == 13) {
-        // ---- MMA ----
-        if (rank == 0 && lane == 0) {
+    } else if (warp == kMmaWarp) {
+        // ---- MMA: the warp waits together, one elected lane issues ----
+        if (rank == 0) {
+            const uint64_t desc0 = operand_desc(smem_u32(s_b));
             uint32_t c = 0, it = 0;
             bool ok = true;
             for (long long u = u0; ok && u < tiles.units; u += du, ++it) {
@@ -318,162 +376,200 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
                 const uint32_t acc = it % kAcc;
                 // float32 accumulators, float16 operands, both K-major
                 const uint32_t idesc = 1u << 4 | (uint32_t)(t.n >> 3) << 17 | (uint32_t)(128 * CG >> 4) << 24;
-                ok = mbar_wait(sh, &sh->acc_empty[acc], (it / kAcc & 1) ^ 1);
+                ok = mbar_wait_warp(sh, &sh->acc_empty[acc], (it / kAcc & 1) ^ 1);
                 if (!ok) break;
-                tmem_fence_after();
+                const uint32_t d = tmem + acc * S::TN;
                 for (int kb = 0; kb < kblocks; ++kb, ++c) {
                     const uint32_t s = c % kStages;
-                    ok = mbar_wait(sh, &sh->full[s], c / kStages & 1);
+                    ok = mbar_wait_warp(sh, &sh->full[s], c / kStages & 1);
                     if (!ok) break;
                     tmem_fence_after();
-                    const uint32_t b = smem_u32(s_b + s * kBBytes);
-                    const int steps = min(kBK, a.Kd - kb * kBK) / 16;
+                    const uint32_t at = tmem + kTmemA + s * 64;
+                    const uint64_t desc = desc0 + (uint64_t)(s * (kBBytes >> 4));
+                    // 16-byte pieces of the block's rows: each gives 8 K to either atom
+                    const int pieces = min(8, (a.Kd - kb * kBK) / 16);
+                    if (elect_one()) {
+                        if (pieces > 6) {
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k)
-                        if (k < steps)
-                            mma_f16<CG>(tmem + acc * 128, tmem + kTmemA + s * 64 + k * 8,
-                                        operand_desc(b + (k >> 2) * kBAtom + (k & 3) * 32), idesc,
-                                        kb > 0 || k > 0);
-                    mma_commit<CG>(&sh->empty[s]);
+                            for (int k = 0; k < kBK / 16; ++k)
+                                mma_f16<CG>(d, at + k * 8, desc + ((k >> 2) * kBAtom + (k & 3) * 32 >> 4), idesc,
+                                            k > 0 || kb > 0);
+                        } else {  // the last, short block
+                            for (int k = 0; k < kBK / 16; ++k)
+                                if ((k & 3) * 2 < pieces)
+                                    mma_f16<CG>(d, at + k * 8, desc + ((k >> 2) * kBAtom + (k & 3) * 32 >> 4),
+                                                idesc, k > 0 || kb > 0);
+                        }
+                        mma_commit<CG>(&sh->empty[s]);
+                        if (kb == kblocks - 1) mma_commit<CG>(&sh->acc_full[acc]);
+                    }
+                    __syncwarp();
                 }
-                if (ok) mma_commit<CG>(&sh->acc_full[acc]);
             }
-            if (!ok) {  // the MMAs in flight end before their operands' memory is given up
-                mma_commit<CG>(&sh->drained);
-                const long long start = clock64();
-                while (!mbar_try(smem_u32(&sh->drained), 0))
-                    if (clock64() - start > kWaitCycles) break;
+            if (!ok && c > 0) {  // the MMAs in flight end before their operands' memory is given up
+                if (elect_one()) {
+                    mma_commit<CG>(&sh->drained);
+                    const long long start = clock64();
+                    while (!mbar_try(smem_u32(&sh->drained), 0))
+                        if (clock64() - start > kWaitCycles) break;
+                }
+                __syncwarp();
             }
         }
-    } else if (warp >= 8) {
-        // ---- x rows -> float16 -> shared memory; warp w fills stage w ----
-        const int s = warp - 8;
+    } else if (warp >= kCopyWarp0 && warp < kRowWarp0) {
+        // ---- x rows, wherever they lie, -> shared memory in the background;
+        // 8 lanes a row, each copying warp half of the rows ----
+        constexpr int kPer = S::kRows / kCopyWarps / 4;  // rows per lane
+        const int chunk = lane & 7, l8 = lane >> 3;
+        const int r0 = (warp - kCopyWarp0) * 4 + l8;     // then every 8th row
+        const uint32_t to = smem_u32(s_x) + r0 * kBK + chunk * 16;
         uint32_t c = 0;
         bool ok = true;
         for (long long u = u0; ok && u < tiles.units; u += du) {
             const Unit t = tiles.get(a, sh, u);
-            const int half = t.n / CG, r0 = rank * half;  // this CTA's rows of the tile
-            int src[4];
+            const int half = t.n / CG;  // this CTA's rows of the tile, a multiple of 16
+            const int8_t* src[kPer];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = r0 + i * 32 + lane;
-                src[i] = (i * 32 + lane < half && r < t.rows) ? source_row(a, t.e, t.begin, t.first + r) : -1;
+            for (int i = 0; i < kPer; ++i) {
+                const int r = r0 + i * 8, rr = rank * half + r;
+                // a row that reads nothing takes row 0: its output is scaled by 0 or not stored
+                const int row = (r < half && rr < t.rows) ? max(0, source_row(a, t.e, t.begin, t.first + rr)) : 0;
+                src[i] = a.x + (size_t)row * a.Kd + chunk * 16;
             }
             for (int kb = 0; kb < kblocks; ++kb, ++c) {
-                if ((c % kStages) != (uint32_t)s) continue;
-                const int chunk = lane & 7;
-                const int k = kb * kBK + chunk * 16;
-                const bool in_k = k < a.Kd;
-                uint8_t* atom = s_b + s * kBBytes + (chunk >> 2) * kBAtom;
-                const int c0 = (chunk & 3) * 2 + (chunk >> 2);  // the half stored first
-                bool waited = false;
+                const uint32_t s = c % kXStages;
+                ok = mbar_wait_warp(sh, &sh->x_empty[s], (c / kXStages & 1) ^ 1);
+                if (!ok) break;
+                const bool on = kb * kBK + chunk * 16 < a.Kd;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i * 32 >= half) break;
-                    uint4 q[8];
+                for (int i = 0; i < kPer; ++i) {
+                    if (i * 8 < half) copy16(to + s * S::kXBytes + i * 8 * kBK, on ? src[i] : a.x, on);
+                    src[i] += kBK;
+                }
+                copies_arrive(&sh->x_full[s]);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp >= kRowWarp0) {
+        // ---- x rows -> float16 -> shared memory; 16 rows a warp, 8 lanes a row ----
+        const int r0 = (warp - kRowWarp0) * 16, chunk = lane & 7, l8 = lane >> 3;
+        const uint32_t from = smem_u32(s_x) + (r0 + l8) * kBK + chunk * 16;
+        const uint32_t at = smem_u32(s_b) + (r0 + l8) * 128 + ((chunk ^ l8) << 4);
+        uint32_t c = 0, c1 = 0;
+        bool ok = true;
+        for (long long u = u0; ok && u < tiles.units; u += du) {
+            const bool mine = r0 < tiles.get(a, sh, u).n / CG;  // the tile has these rows
+            c1 += kblocks;
+            for (; c < c1; ++c) {
+                const uint32_t sx = c % kXStages, s = c % kStages;
+                ok = mbar_wait_warp(sh, &sh->x_full[sx], c / kXStages & 1);
+                if (!ok) break;
+                uint4 q[4];
+                if (mine) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int row = __shfl_sync(kFull, src[i], j * 4 + (lane >> 3));
-                        q[j] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row >= 0 && in_k)
-                            q[j] = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)row * a.Kd + k));
-                    }
-                    if (!waited) {
-                        ok = mbar_wait_warp(sh, &sh->empty[s], (c / kStages & 1) ^ 1);
-                        waited = true;
-                        if (!ok) break;
-                    }
+                    for (int j = 0; j < 4; ++j) q[j] = load_shared(from + sx * S::kXBytes + j * 4 * kBK);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->x_empty[sx]);
+                ok = mbar_wait_warp(sh, &sh->empty[s], (c / kStages & 1) ^ 1);
+                if (!ok) break;
+                if (mine) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int r = i * 32 + j * 4 + (lane >> 3);
+                    for (int j = 0; j < 4; ++j) {
                         uint4 lo, hi;
                         widen4(q[j].x, lo.x, lo.y);
                         widen4(q[j].y, lo.z, lo.w);
                         widen4(q[j].z, hi.x, hi.y);
                         widen4(q[j].w, hi.z, hi.w);
-                        // chunks 4..7 store their second half first: the 8 lanes of a row then
-                        // cover all 8 bank groups
-                        uint8_t* at = atom + r * 128;
-                        const bool swap = (chunk >> 2) != 0;
-                        *reinterpret_cast<uint4*>(at + ((c0 ^ (r & 7)) << 4)) = swap ? hi : lo;
-                        *reinterpret_cast<uint4*>(at + (((c0 ^ 1) ^ (r & 7)) << 4)) = swap ? lo : hi;
+                        const uint32_t to = ((at + s * kBBytes) ^ (j & 1) * 64) + j * 4 * 128;
+                        store_shared(to, lo);
+                        store_shared(to + kBAtom, hi);
                     }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                if (!ok) break;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive_leader<CG>(&sh->full[s]);
             }
         }
-        // the last MMAs' arrivals on this stage land before the CTA ends
-        const uint32_t uses = c / kStages + (c % kStages > (uint32_t)s ? 1 : 0);
-        if (ok && uses > 0) mbar_wait_warp(sh, &sh->empty[s], (uses - 1) & 1);
-    } else if (warp >= 4) {
-        // ---- weights -> float16 -> TMEM ----
-        const int quarter = warp - 4;
+        // the last MMAs' arrivals on each stage land before the CTA ends
+        for (int s = 0; ok && s < kStages; ++s) {
+            const uint32_t uses = c1 / kStages + (c1 % kStages > (uint32_t)s ? 1 : 0);
+            if (uses > 0) ok = mbar_wait_warp(sh, &sh->empty[s], (uses - 1) & 1);
+        }
+    } else if (warp >= kWeightWarp0) {
+        // ---- weights -> float16 -> TMEM; two groups of 4 warps take turns ----
+        // (kWStages is even, so a group sees every phase of its stages; of the
+        // converted stages it sees every second phase of each, and knows from
+        // the stage before that the phase between them is over.)
+        const int quarter = warp & 3, group = (warp - kWeightWarp0) >> 2;
         const int row = quarter * 32 + lane;
-        uint32_t c = 0;
+        const uint32_t from = smem_u32(s_w) + row * 128 + ((row & 7) << 4);
+        const uint32_t to = tmem + ((uint32_t)quarter << 21) + kTmemA;
+        const uint32_t total = tiles.units > u0 ? (uint32_t)((tiles.units - u0 + du - 1) / du) * kblocks : 0;
         bool ok = true;
-        for (long long u = u0; ok && u < tiles.units; u += du) {
-            for (int kb = 0; kb < kblocks; ++kb, ++c) {
-                const uint32_t sw = c % kWStages, s = c % kStages;
-                ok = mbar_wait_warp(sh, &sh->w_full[sw], c / kWStages & 1);
-                if (!ok) break;
-                const uint8_t* from = s_w + sw * kWBytes + row * 128;
-                uint32_t r[64];
+        for (uint32_t c = group; ok && c < total; c += 2) {
+            const uint32_t sw = c % kWStages, s = c % kStages;
+            ok = mbar_wait_warp(sh, &sh->w_full[sw], c / kWStages & 1);
+            if (!ok) break;
+            uint4 q[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(from + ((j ^ (row & 7)) << 4));
-                    widen4(q.x, r[j * 8], r[j * 8 + 1]);
-                    widen4(q.y, r[j * 8 + 2], r[j * 8 + 3]);
-                    widen4(q.z, r[j * 8 + 4], r[j * 8 + 5]);
-                    widen4(q.w, r[j * 8 + 6], r[j * 8 + 7]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->w_empty[sw]);
-                ok = mbar_wait_warp(sh, &sh->empty[s], (c / kStages & 1) ^ 1);
-                if (!ok) break;
-                tmem_fence_after();
-                const uint32_t at = tmem + ((uint32_t)quarter << 21) + kTmemA + s * 64;
-                tmem_store32(at, reinterpret_cast<const uint32_t(&)[32]>(r[0]));
-                tmem_store32(at + 32, reinterpret_cast<const uint32_t(&)[32]>(r[32]));
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_leader<CG>(&sh->full[s]);
-            }
-        }
-    } else {
-        // ---- accumulators -> out ----
-        uint32_t it = 0;
-        bool ok = true;
-        for (long long u = u0; ok && u < tiles.units; u += du, ++it) {
-            const Unit t = tiles.get(a, sh, u);
-            const uint32_t acc = it % kAcc;
-            const int ch = t.channel + rank * 128 + warp * 32 + lane;
-            const float ws = ch < a.Nc ? __ldg(a.w_scales + (size_t)t.e * a.Nc + ch) : 0.0f;
-            const size_t base = (first_row(a, t.e, t.begin) + t.first) * a.Nc + ch;
-            ok = mbar_wait_warp(sh, &sh->acc_full[acc], it / kAcc & 1);
+            for (int j = 0; j < 8; ++j) q[j] = load_shared((from + sw * kWBytes) ^ (j * 16));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->w_empty[sw]);
+            ok = mbar_wait_warp(sh, &sh->empty[s], (c / kStages & 1) ^ 1);
             if (!ok) break;
             tmem_fence_after();
-            const uint32_t from = tmem + ((uint32_t)warp << 21) + acc * 128;
-            float xs = 0.0f;
-            for (int n0 = 0; n0 < t.n; n0 += 16) {
-                if ((n0 & 31) == 0) {
-                    const int r = n0 + lane;
-                    const int src = r < t.rows ? source_row(a, t.e, t.begin, t.first + r) : -1;
-                    xs = src >= 0 ? __ldg(a.x_scales + src) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                uint32_t lo[16], hi[16];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    widen4(q[j + i].x, lo[i * 4], lo[i * 4 + 1]);
+                    widen4(q[j + i].y, lo[i * 4 + 2], lo[i * 4 + 3]);
                 }
+                tmem_store16(to + s * 64 + j * 4, lo);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    widen4(q[j + i].z, hi[i * 4], hi[i * 4 + 1]);
+                    widen4(q[j + i].w, hi[i * 4 + 2], hi[i * 4 + 3]);
+                }
+                tmem_store16(to + s * 64 + 32 + j * 4, hi);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_leader<CG>(&sh->full[s]);
+        }
+    } else {
+        // ---- accumulators -> out; two warps per 32 channels, 16 of every 32 rows each ----
+        const int quarter = warp & 3, h = warp >> 2;
+        uint32_t it = 0;
+        const int size = a.out_bf16 ? 2 : 4;
+        const size_t pitch = (size_t)a.Nc * size;
+        for (long long u = u0; u < tiles.units; u += du, ++it) {
+            const Unit t = tiles.get(a, sh, u);
+            const uint32_t acc = it % kAcc;
+            const int ch = t.channel + rank * 128 + quarter * 32 + lane;
+            const float ws = ch < a.Nc ? __ldg(a.w_scales + (size_t)t.e * a.Nc + ch) : 0.0f;
+            const int rows = ch < a.Nc ? t.rows : 0;
+            uint8_t* to = static_cast<uint8_t*>(a.out) +
+                          (first_row(a, t.e, t.begin) + t.first) * pitch + (size_t)ch * size;
+            if (!mbar_wait_warp(sh, &sh->acc_full[acc], it / kAcc & 1)) break;
+            tmem_fence_after();
+            const uint32_t from = tmem + ((uint32_t)quarter << 21) + acc * S::TN;
+            for (int n0 = h * 16; n0 < t.n; n0 += 32) {
+                const int r = n0 + (lane & 15);
+                const int src = r < t.rows ? source_row(a, t.e, t.begin, t.first + r) : -1;
+                const float xs = src >= 0 ? __ldg(a.x_scales + src) : 0.0f;
                 uint32_t v[16];
                 tmem_load16(from + n0, v);
+                uint8_t* p = to + n0 * pitch;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float x = __shfl_sync(kFull, xs, (n0 & 16) + j);
-                    const float y = __uint_as_float(v[j]) * x * ws;
-                    if (n0 + j < t.rows && ch < a.Nc) {
-                        const size_t at = base + (size_t)(n0 + j) * a.Nc;
-                        if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
-                        else static_cast<float*>(a.out)[at] = y;
+                for (int j = 0; j < 16; ++j, p += pitch) {
+                    const float y = __uint_as_float(v[j]) * __shfl_sync(kFull, xs, j) * ws;
+                    if (n0 + j < rows) {
+                        if (a.out_bf16) *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(y);
+                        else *reinterpret_cast<float*>(p) = y;
                     }
                 }
             }
@@ -491,7 +587,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     tmem_fence_after();
-    if (warp == 13) {
+    if (warp == kMmaWarp) {
         if constexpr (CG == 1) {
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -526,22 +622,23 @@ EncodeTiled encode_tiled() {
 // Grid of the persistent kernel on the current device: a CTA per SM, or as
 // many pairs as the device holds at once (an SM without a neighbour in its
 // cluster cannot host half a pair).  Looked up once per device.
-template <int CG>
+template <class S>
 cudaError_t persistent_grid(int* grid) {
+    constexpr int CG = S::CG;
     static std::atomic<int> cached[64];
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     int n = dev >= 0 && dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
     if (n <= 0) {
-        err = cudaFuncSetAttribute(matmul_tc_kernel<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        err = cudaFuncSetAttribute(matmul_tc_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<S>);
         if (err != cudaSuccess) return err;
         n = sm_count();
         if (CG == 2) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(n / 2 * 2);
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = kSmemBytes;
+            cfg.blockDim = dim3(S::kThreads);
+            cfg.dynamicSmemBytes = kSmemBytes<S>;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = 2;
@@ -549,7 +646,7 @@ cudaError_t persistent_grid(int* grid) {
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             int pairs = 0;
-            err = cudaOccupancyMaxActiveClusters(&pairs, matmul_tc_kernel<CG>, &cfg);
+            err = cudaOccupancyMaxActiveClusters(&pairs, matmul_tc_kernel<S>, &cfg);
             if (err != cudaSuccess) return err;
             if (pairs < 1) return cudaErrorInvalidConfiguration;
             n = 2 * pairs;
@@ -560,25 +657,26 @@ cudaError_t persistent_grid(int* grid) {
     return cudaSuccess;
 }
 
-template <int CG>
+template <class S>
 cudaError_t launch_tc(const MatmulArgs& a, cudaStream_t s) {
+    constexpr int CG = S::CG;
     const EncodeTiled encode = encode_tiled();
     if (encode == nullptr) return cudaErrorNotSupported;
-    CUtensorMap map;
+    CUtensorMap w_map;
     const cuuint64_t dims[2] = {(cuuint64_t)a.Kd, (cuuint64_t)a.E * a.Nc};
     const cuuint64_t strides[1] = {(cuuint64_t)a.Kd};
     const cuuint32_t box[2] = {kBK, 128}, steps[2] = {1, 1};
-    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(a.w), dims, strides, box, steps,
+    if (encode(&w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(a.w), dims, strides, box, steps,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     int grid = 0;
-    const cudaError_t err = persistent_grid<CG>(&grid);
+    const cudaError_t err = persistent_grid<S>(&grid);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes<S>;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int n = 0;
@@ -595,13 +693,15 @@ cudaError_t launch_tc(const MatmulArgs& a, cudaStream_t s) {
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, matmul_tc_kernel<CG>, a, map);
+    return cudaLaunchKernelEx(&cfg, matmul_tc_kernel<S>, a, w_map);
 }
 
 }  // namespace
 
-cudaError_t launch_matmul_tc(const MatmulArgs& a, bool pair, cudaStream_t s) {
-    return pair ? launch_tc<2>(a, s) : launch_tc<1>(a, s);
+cudaError_t launch_matmul_tc(const MatmulArgs& a, int per, cudaStream_t s) {
+    if (per <= 48) return launch_tc<Shape<1, 64>>(a, s);
+    if (per <= 128) return launch_tc<Shape<2, 128>>(a, s);
+    return launch_tc<Shape<2, 256>>(a, s);
 }
 
 }  // namespace ep
