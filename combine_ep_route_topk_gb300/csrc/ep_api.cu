@@ -431,6 +431,7 @@ ep_status_t ep_gate_topk(const void* logits, ep_dtype_t logits_dtype, int32_t N,
     a.renorm = renorm != 0;
     a.bf16 = bf16;
     a.vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & (bf16 ? 7u : 15u)) == 0;
+    a.bias_vec = E % 4 == 0 && aligned16(bias);
     return cuda_status(launch_gate(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -181,6 +181,8 @@ struct GateArgs {
     int N, E, K, score, groups, topk_groups, group_top, renorm;
     int bf16;
     int vec;                    // rows start on a boundary of 4 elements
+    int bias_vec;               // so does the bias
+    int lanes_per_group;        // set by the launcher: lanes that hold a group, 0 if they share
 };
 cudaError_t launch_gate(const GateArgs& a, cudaStream_t s);
 

@@ -11,11 +11,14 @@
 //   w_k   = scale * s_k [/ sum of the picks' s]
 //
 // One warp per token.  Lane i holds the VPL consecutive experts i*VPL ..
-// i*VPL + VPL-1 as order-preserving 32-bit keys in registers, so that a lower
-// lane always means lower ids: a round of the selection is one redux.sync max
-// over the lanes' best keys, a ballot, and the lowest lane that holds the
-// maximum wins.  Lanes cache their three best slots and rescan after a third
-// win.  Scores are recomputed for the picks alone.
+// i*VPL + VPL-1, so that a lower lane always means lower ids.  It sorts its
+// keys (values alone, by a network of min and max); a round of the selection is
+// then one redux.sync max over the lanes' heads and a ballot, the lowest lane
+// that holds the maximum wins, and the winner moves its list up by one.  Which
+// expert a pick is follows once, after the rounds, from its value, its lane and
+// how many equal values that lane gave before it.  Scores are recomputed, in
+// full accuracy, for the picks alone; the choice uses the hardware's exp2 and
+// reciprocal (an absolute error below 3e-7 in a score of at most 1).
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -27,13 +30,6 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kGateWarps = 8;  // tokens per block
-
-// Larger float -> larger key; -0 folds onto +0.  Key 0 means "not available".
-__device__ __forceinline__ uint32_t order_key(float v) {
-    uint32_t u = __float_as_uint(v);
-    if (u == 0x80000000u) u = 0u;
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
 
 // False for NaN and -inf.
 __device__ __forceinline__ bool available(float v) { return v > -INFINITY; }
@@ -112,19 +108,42 @@ __device__ __forceinline__ void load_row(const T* row, int E, bool vec, int lane
         v[j] = (e0 + j < E) ? load_one(row + e0 + j) : __int_as_float(0x7fffffff);
 }
 
-// Insert slot j into the sorted triple (key descending, slot ascending).
-__device__ __forceinline__ void insert3(int j, uint32_t x, int& s0, uint32_t& b0, int& s1,
-                                        uint32_t& b1, int& s2, uint32_t& b2) {
-    if (x > b0) {
-        s2 = s1; b2 = b1;
-        s1 = s0; b1 = b0;
-        s0 = j;  b0 = x;
-    } else if (x > b1) {
-        s2 = s1; b2 = b1;
-        s1 = j;  b1 = x;
-    } else if (x > b2) {
-        s2 = j;  b2 = x;
-    }
+// Sorts v descending: Batcher's odd-even merge sort (1968).
+template <int N>
+__device__ __forceinline__ void sort_descending(float (&v)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const float hi = fmaxf(v[i + j], v[i + j + k]);
+                        v[i + j + k] = fminf(v[i + j], v[i + j + k]);
+                        v[i + j] = hi;
+                    }
+}
+
+// Maximum over the warp.
+__device__ __forceinline__ float redux_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// Scores for the choice, by the hardware's exp2 and reciprocal.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ void two_best(float x, float& a, float& b) {
@@ -132,7 +151,8 @@ __device__ __forceinline__ void two_best(float x, float& a, float& b) {
     a = fmaxf(a, x);
 }
 
-template <int VPL, typename T>
+// KT > 0: K == KT known at compile time.
+template <int VPL, typename T, int KT>
 __global__ void __launch_bounds__(kGateWarps * 32)
 gate_kernel(GateArgs a) {
     extern __shared__ float s_choice[];  // [warps][E], only for groups that cross lanes unevenly
@@ -141,7 +161,7 @@ gate_kernel(GateArgs a) {
     const int warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kGateWarps + warp;
     if (t >= a.N) return;  // warp-uniform
-    const int E = a.E, K = a.K;
+    const int E = a.E, K = KT > 0 ? KT : a.K;
     const T* row = static_cast<const T*>(a.logits) + (size_t)t * E;
     const int e0 = lane * VPL;
 
@@ -157,7 +177,7 @@ gate_kernel(GateArgs a) {
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
             if (available(v[j])) m = fmaxf(m, clamp_logit(v[j]));
-        m = warp_max(m);
+        m = redux_max(m);
         if (all_scores || !a.renorm) {
             float sum = 0.0f;
 #pragma unroll
@@ -167,81 +187,115 @@ gate_kernel(GateArgs a) {
         }
     }
 
-    // keys, and the groups' scores
-    uint32_t key[VPL];
-    float c[VPL];  // s + bias, where groups are scored by sums
+    // keys (-inf: not available), and s + bias where groups are scored by sums
+    float key[VPL], c[VPL];
+    if (all_scores) {
+        const bool sigmoids = a.score == kScoreSigmoid;
+        const float mul = sigmoids ? -kLog2e : kLog2e, inv_total = rcp_fast(total);
+        float bias[VPL];
+        if (a.bias != nullptr) load_row<VPL>(a.bias, E, a.bias_vec != 0, lane, bias);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-        const float l = clamp_logit(v[j]);
-        float x = l;
-        bool ok = available(v[j]);
-        c[j] = -INFINITY;
-        if (all_scores && ok) {
-            x = a.score == kScoreSigmoid ? sigmoid(l) : __fdiv_rn(expf(l - m), total);
-            if (a.bias != nullptr) x += __ldg(a.bias + e0 + j);
-            ok = available(x);
-            if (ok) c[j] = x;
-            if (a.bias == nullptr) x = l;
+        for (int j = 0; j < VPL; ++j) {
+            const float l = clamp_logit(v[j]);
+            const float e = exp2_fast((l - m) * mul);
+            float x = sigmoids ? rcp_fast(1.0f + e) : e * inv_total;
+            if (a.bias != nullptr) x += bias[j];
+            c[j] = available(v[j]) ? fmaxf(x, -INFINITY) : -INFINITY;  // a NaN of the bias -> -inf
+            key[j] = a.bias != nullptr ? c[j] : available(v[j]) ? l : -INFINITY;
         }
-        key[j] = ok ? order_key(x) : 0u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            key[j] = available(v[j]) ? clamp_logit(v[j]) : -INFINITY;
+            c[j] = key[j];
+        }
     }
     if (a.groups > 1) {
         const int per = E / a.groups;
-        float* mine = s_choice + (size_t)warp * E;
+        if (a.lanes_per_group > 0) {
+            // whole lanes of one group next to each other, a power of two of them
+            float best = -INFINITY, second = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
-            if (e0 + j < E) {
-                float x = c[j];
-                if (!groups_sum) x = key[j] == 0u ? -INFINITY : (all_scores ? c[j] : clamp_logit(v[j]));
-                mine[e0 + j] = x;
-            }
-        __syncwarp();
-        float best = -INFINITY, second = -INFINITY;
-        if (lane < a.groups) {
-            int i = lane % per;  // start apart, so that the lanes' banks differ
-            for (int n = 0; n < per; ++n) {
-                two_best(mine[lane * per + i], best, second);
-                i = i + 1 == per ? 0 : i + 1;
+            for (int j = 0; j < VPL; ++j) two_best(groups_sum ? c[j] : key[j], best, second);
+            for (int off = 1; off < a.lanes_per_group; off <<= 1) {
+                const float o1 = __shfl_xor_sync(kFull, best, off);
+                const float o2 = __shfl_xor_sync(kFull, second, off);
+                second = fmaxf(fminf(best, o1), fmaxf(second, o2));
+                best = fmaxf(best, o1);
             }
             if (groups_sum && second > -INFINITY) best += second;
-        }
-        int before = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const float o = __shfl_sync(kFull, best, g);
-            before += (o > best || (o == best && g < lane)) ? 1 : 0;
-        }
-        const unsigned kept = __ballot_sync(kFull, lane < a.groups && before < a.topk_groups);
+            const int g = lane / a.lanes_per_group;
+            int before = 0;
+            for (int o = 0; o < a.groups; ++o) {
+                const float other = __shfl_sync(kFull, best, o * a.lanes_per_group);
+                before += (other > best || (other == best && o < g)) ? 1 : 0;
+            }
+            if (before >= a.topk_groups) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
-            if (e0 + j < E && !(kept >> ((e0 + j) / per) & 1u)) key[j] = 0u;
+                for (int j = 0; j < VPL; ++j) key[j] = -INFINITY;
+            }
+        } else {
+            float* mine = s_choice + (size_t)warp * E;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (e0 + j < E) mine[e0 + j] = groups_sum ? c[j] : key[j];
+            __syncwarp();
+            float best = -INFINITY, second = -INFINITY;
+            if (lane < a.groups) {
+                int i = lane % per;  // start apart, so that the lanes' banks differ
+                for (int n = 0; n < per; ++n) {
+                    two_best(mine[lane * per + i], best, second);
+                    i = i + 1 == per ? 0 : i + 1;
+                }
+                if (groups_sum && second > -INFINITY) best += second;
+            }
+            int before = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const float o = __shfl_sync(kFull, best, g);
+                before += (o > best || (o == best && g < lane)) ? 1 : 0;
+            }
+            const unsigned kept = __ballot_sync(kFull, lane < a.groups && before < a.topk_groups);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (e0 + j < E && !(kept >> ((e0 + j) / per) & 1u)) key[j] = -INFINITY;
+        }
     }
 
-    int s0 = 0, s1 = 0, s2 = 0;
-    uint32_t b0 = 0u, b1 = 0u, b2 = 0u;
+    float list[VPL];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) insert3(j, key[j], s0, b0, s1, b1, s2, b2);
-    int my_id = -1;
+    for (int j = 0; j < VPL; ++j) list[j] = key[j];
+    sort_descending(list);
+    float my_top = -INFINITY;
+    int my_lane = 0;
+#pragma unroll(KT > 0 ? KT : 1)
     for (int k = 0; k < K; ++k) {
-        const uint32_t top = __reduce_max_sync(kFull, b0);
-        if (top == 0u) break;  // no expert left
-        const int win = __ffs(__ballot_sync(kFull, b0 == top)) - 1;
-        const int id = __shfl_sync(kFull, e0 + s0, win);
-        if (lane == k) my_id = id;
-        const bool won = lane == win;
-        const uint32_t lk = b0;
-        const int ls = s0;
-        if (won) {
-            s0 = s1; b0 = b1;
-            s1 = s2; b1 = b2;
-            b2 = 0u;
+        const float top = redux_max(list[0]);
+        const int win = __ffs(__ballot_sync(kFull, list[0] == top)) - 1;
+        if (lane == k) {
+            my_top = top;
+            my_lane = win;
         }
-        if (VPL > 3 && __any_sync(kFull, won && b0 == 0u)) {
-            if (won && b0 == 0u) {  // the next three after (lk, ls)
+        if (lane == win) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    if (key[j] < lk || (key[j] == lk && j > ls)) insert3(j, key[j], s0, b0, s1, b1, s2, b2);
-            }
+            for (int j = 0; j + 1 < VPL; ++j)
+                if (KT == 0 || j < KT - 1 - k) list[j] = list[j + 1];
+            if (KT == 0 || VPL <= KT - 1 - k) list[VPL - 1] = -INFINITY;
         }
+    }
+    // Lane k: pick k is the (same + 1)-th of its lane's experts with this key,
+    // where `same` picks right before it have the same key and lane.
+    int my_id = -1;
+    {
+        const float up_top = __shfl_up_sync(kFull, my_top, 1);
+        const int up_lane = __shfl_up_sync(kFull, my_lane, 1);
+        const unsigned rest = ~__ballot_sync(kFull, lane > 0 && up_top == my_top && up_lane == my_lane);
+        int same = lane - (31 - __clz(rest & (0xffffffffu >> (31 - lane))));
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const float x = __shfl_sync(kFull, key[j], my_lane);
+            if (x == my_top && same-- == 0) my_id = my_lane * VPL + j;
+        }
+        if (lane >= K || !(my_top > -INFINITY)) my_id = -1;
     }
 
     float l = -INFINITY, s = 0.0f;
@@ -263,15 +317,20 @@ gate_kernel(GateArgs a) {
 }
 
 template <typename T>
-cudaError_t launch_gate_t(const GateArgs& a, cudaStream_t s) {
+cudaError_t launch_gate_t(GateArgs a, cudaStream_t s) {
     const dim3 grid((a.N + kGateWarps - 1) / kGateWarps), block(kGateWarps * 32);
-    const size_t smem = a.groups > 1 ? sizeof(float) * kGateWarps * a.E : 0;
-    if (a.E <= 32) return launch(gate_kernel<1, T>, grid, block, smem, s, a);
-    if (a.E <= 64) return launch(gate_kernel<2, T>, grid, block, smem, s, a);
-    if (a.E <= 128) return launch(gate_kernel<4, T>, grid, block, smem, s, a);
-    if (a.E <= 256) return launch(gate_kernel<8, T>, grid, block, smem, s, a);
-    if (a.E <= 512) return launch(gate_kernel<16, T>, grid, block, smem, s, a);
-    return launch(gate_kernel<32, T>, grid, block, smem, s, a);
+    int vpl = 1;
+    while (vpl * 32 < a.E) vpl *= 2;
+    const int per = a.E / a.groups, lanes = per / vpl;
+    a.lanes_per_group = per % vpl == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    const size_t smem = a.groups > 1 && a.lanes_per_group == 0 ? sizeof(float) * kGateWarps * a.E : 0;
+    if (a.K == 8 && a.E > 128 && a.E <= 256) return launch(gate_kernel<8, T, 8>, grid, block, smem, s, a);
+    if (a.E <= 32) return launch(gate_kernel<1, T, 0>, grid, block, smem, s, a);
+    if (a.E <= 64) return launch(gate_kernel<2, T, 0>, grid, block, smem, s, a);
+    if (a.E <= 128) return launch(gate_kernel<4, T, 0>, grid, block, smem, s, a);
+    if (a.E <= 256) return launch(gate_kernel<8, T, 0>, grid, block, smem, s, a);
+    if (a.E <= 512) return launch(gate_kernel<16, T, 0>, grid, block, smem, s, a);
+    return launch(gate_kernel<32, T, 0>, grid, block, smem, s, a);
 }
 
 // ---- gradient ---------------------------------------------------------------
