@@ -34,20 +34,21 @@ __device__ __forceinline__ size_t first_row(const MatmulArgs& a, int e, int begi
     return a.layout == 0 ? (size_t)begin : (size_t)e * a.cap;
 }
 
-// s_tiles[e] = exclusive prefix over the experts of ceil(rows_e / tile), by the
-// block's first 256 threads (4 experts each); every thread calls it, and it
-// ends with a barrier.
+// Row tiles of the experts: s_tiles[i] = tiles of ceil(rows_e / tile) rows over
+// the experts before 4 i (a quarter of a full table, so that it costs 1 KB of
+// shared memory); s_tiles[kTileGroups] = all of them.  Computed by the block's
+// first 256 threads, 4 experts each; every thread calls it, and it ends with a
+// barrier.
+constexpr int kTileGroups = kMaxE / 4;
 __device__ __forceinline__ void tile_prefix(const MatmulArgs& a, int tile, int* s_tiles, int* s_warp) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kPer = kMaxE / 256;
-    int n[kPer], sum = 0, incl = 0;
-    if (tid < 256) {
+    int sum = 0, incl = 0;
+    if (tid < kTileGroups) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int e = tid * kPer + j;
+        for (int j = 0; j < 4; ++j) {
+            const int e = tid * 4 + j;
             int begin;
-            n[j] = e < a.E ? (expert_rows(a, e, begin) + tile - 1) / tile : 0;
-            sum += n[j];
+            sum += e < a.E ? (expert_rows(a, e, begin) + tile - 1) / tile : 0;
         }
         incl = sum;
 #pragma unroll
@@ -58,28 +59,37 @@ __device__ __forceinline__ void tile_prefix(const MatmulArgs& a, int tile, int* 
         if (lane == 31) s_warp[warp] = incl;
     }
     __syncthreads();
-    if (tid < 256) {
+    if (tid < kTileGroups) {
         int run = incl - sum;
         for (int w = 0; w < warp; ++w) run += s_warp[w];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int e = tid * kPer + j;
-            if (e < a.E) s_tiles[e] = run;
-            run += n[j];
-            if (e == a.E - 1) s_tiles[a.E] = run;
-        }
+        s_tiles[tid] = run;
+        if (tid == kTileGroups - 1) s_tiles[kTileGroups] = run + sum;
     }
     __syncthreads();
 }
 
-// The expert that owns tile t (s_tiles[e] <= t < s_tiles[e + 1]).
-__device__ __forceinline__ int expert_of_tile(const int* s_tiles, int E, int t) {
-    int lo = 0, hi = E;
+struct ExpertTile {
+    int e, begin, rows;   // the expert, its first position in expert-major order, its rows
+    int first, count;     // its first tile, its number of tiles
+};
+
+// The expert that owns tile t < s_tiles[kTileGroups].
+__device__ __forceinline__ ExpertTile expert_of_tile(const MatmulArgs& a, int tile, const int* s_tiles, int t) {
+    int lo = 0, hi = kTileGroups;  // s_tiles[lo] <= t < s_tiles[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s_tiles[mid] <= t) lo = mid; else hi = mid;
     }
-    return lo;
+    ExpertTile x;
+    x.e = lo * 4;
+    x.first = s_tiles[lo];
+    for (;; ++x.e) {
+        x.rows = expert_rows(a, x.e, x.begin);
+        x.count = (x.rows + tile - 1) / tile;
+        if (t < x.first + x.count || (x.e & 3) == 3 || x.e + 1 >= a.E) break;
+        x.first += x.count;
+    }
+    return x;
 }
 
 }  // namespace mm

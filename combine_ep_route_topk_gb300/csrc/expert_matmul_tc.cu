@@ -35,13 +35,13 @@ namespace {
 
 using namespace mm;
 
-constexpr int kStages = 3;            // stages of converted operands
+constexpr int kStages = 4;            // stages of converted operands
 constexpr int kBK = 128;              // K of a stage
 constexpr int kWBytes = 128 * kBK;    // one stage of 8-bit weights
 constexpr int kOutWarps = 8, kWeightWarp0 = kOutWarps, kWeightWarps = 8;
 constexpr int kTmaWarp = kWeightWarp0 + kWeightWarps, kMmaWarp = kTmaWarp + 1;
 constexpr int kCopyWarp0 = kMmaWarp + 1, kCopyWarps = 2;
-constexpr int kRowWarp0 = kCopyWarp0 + kCopyWarps;  // a row warp for every 16 rows of a stage
+constexpr int kRowWarp0 = kCopyWarp0 + kCopyWarps;  // two row warps for every 32 rows of a stage
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemA = 256;      // A stages start here: 64 columns each
 constexpr uint32_t kWaitHint = 2000;  // ns that one poll of a barrier may sleep
@@ -56,7 +56,7 @@ struct Shape {
     static constexpr int kBBytes = 2 * kBAtom;       // one stage
     static constexpr int kXBytes = kRows * kBK;      // one stage of 8-bit rows
     static constexpr int kWStages = kRows <= 64 ? 8 : 4;  // 8-bit weights in flight
-    static constexpr int kXStages = kRows <= 64 ? 4 : 3;  // 8-bit rows in flight
+    static constexpr int kXStages = kRows <= 64 ? 4 : 2;  // 8-bit rows in flight
     static constexpr int kRowWarps = kRows / 16;
     static constexpr int kThreads = (kRowWarp0 + kRowWarps) * 32;
     static constexpr int kAcc = TN <= 128 ? 2 : 1;   // accumulators of TN columns
@@ -74,7 +74,7 @@ struct Shared {
     uint32_t tmem;
     int abort;
     int warp_sums[8];
-    int tiles[kMaxE + 1];
+    int tiles[kTileGroups + 1];
 };
 template <class S>
 constexpr int kSmemBytes = 1024 + kStages * S::kBBytes + S::kWStages * kWBytes + S::kXStages * S::kXBytes +
@@ -249,6 +249,19 @@ __device__ __forceinline__ void store_shared(uint32_t at, uint4 v) {
                  ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// 16 codes of a row, widened: the first 8 to one half of a stage, the second to
+// the other.
+template <int ATOM>
+__device__ __forceinline__ void widen_row(uint32_t to, uint4 q) {
+    uint4 v;
+    widen4(q.x, v.x, v.y);
+    widen4(q.y, v.z, v.w);
+    store_shared(to, v);
+    widen4(q.z, v.x, v.y);
+    widen4(q.w, v.z, v.w);
+    store_shared(to + ATOM, v);
+}
+
 // K-major operand of 128-byte rows with the 128-byte swizzle: groups of 8 rows
 // are 1024 bytes apart.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
@@ -271,17 +284,18 @@ struct Tiles {
 
     __device__ __forceinline__ Tiles(const MatmulArgs& a, const Shared* sh) {
         ct = (a.Nc + kChannels - 1) / kChannels;
-        units = (long long)sh->tiles[a.E] * ct;
+        units = (long long)sh->tiles[kTileGroups] * ct;
     }
     // An expert's units are consecutive, its row tiles innermost, so that CTAs
     // which run together share weights and rows in L2.
     __device__ __forceinline__ Unit get(const MatmulArgs& a, const Shared* sh, long long u) const {
         Unit t;
-        t.e = expert_of_tile(sh->tiles, a.E, (int)(u / ct));
-        const int t0 = sh->tiles[t.e], nt = sh->tiles[t.e + 1] - t0;
-        const long long local = u - (long long)t0 * ct;
+        const ExpertTile x = expert_of_tile(a, S::TN, sh->tiles, (int)(u / ct));
+        const int nt = x.count, rows = x.rows;
+        const long long local = u - (long long)x.first * ct;
         const int c = (int)(local / nt), i = (int)(local - (long long)c * nt);
-        const int rows = expert_rows(a, t.e, t.begin);
+        t.e = x.e;
+        t.begin = x.begin;
         const int per = ((rows + nt - 1) / nt + kGrain - 1) / kGrain * kGrain;
         t.channel = c * kChannels;
         t.first = i * per;
@@ -313,10 +327,10 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         }
         for (int i = 0; i < kXStages; ++i) {
             mbar_init(&sh->x_full[i], kCopyWarps * 32);
-            mbar_init(&sh->x_empty[i], S::kRowWarps);
+            mbar_init(&sh->x_empty[i], S::kRowWarps / 2);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh->full[i], (4 + S::kRowWarps) * CG);
+            mbar_init(&sh->full[i], (4 + S::kRowWarps / 2) * CG);
             mbar_init(&sh->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -440,67 +454,62 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
                 const uint32_t s = c % kXStages;
                 ok = mbar_wait_warp(sh, &sh->x_empty[s], (c / kXStages & 1) ^ 1);
                 if (!ok) break;
-                const bool on = kb * kBK + chunk * 16 < a.Kd;
+                const uint32_t dst = to + s * S::kXBytes;
+                if (kb * kBK + kBK <= a.Kd) {
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    if (i * 8 < half) copy16(to + s * S::kXBytes + i * 8 * kBK, on ? src[i] : a.x, on);
-                    src[i] += kBK;
+                    for (int i = 0; i < kPer; ++i)
+                        if (i * 8 < half) copy16(dst + i * 8 * kBK, src[i] + kb * kBK, true);
+                } else {  // the last, short block: zeros past Kd
+                    const bool on = kb * kBK + chunk * 16 < a.Kd;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+                        if (i * 8 < half) copy16(dst + i * 8 * kBK, on ? src[i] + kb * kBK : a.x, on);
                 }
                 copies_arrive(&sh->x_full[s]);
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= kRowWarp0) {
-        // ---- x rows -> float16 -> shared memory; 16 rows a warp, 8 lanes a row ----
-        const int r0 = (warp - kRowWarp0) * 16, chunk = lane & 7, l8 = lane >> 3;
+        // ---- x rows -> float16 -> shared memory; two groups of warps take
+        // turns, 32 rows a warp, 8 lanes a row ----
+        constexpr int kGroup = S::kRowWarps / 2;
+        const int group = (warp - kRowWarp0) / kGroup, r0 = (warp - kRowWarp0) % kGroup * 32;
+        const int chunk = lane & 7, l8 = lane >> 3;
         const uint32_t from = smem_u32(s_x) + (r0 + l8) * kBK + chunk * 16;
         const uint32_t at = smem_u32(s_b) + (r0 + l8) * 128 + ((chunk ^ l8) << 4);
-        uint32_t c = 0, c1 = 0;
+        uint32_t c = group, c1 = 0;
         bool ok = true;
         for (long long u = u0; ok && u < tiles.units; u += du) {
-            const bool mine = r0 < tiles.get(a, sh, u).n / CG;  // the tile has these rows
+            const int mine = tiles.get(a, sh, u).n / CG - r0;  // rows of this warp, if any: 16, or all 32
             c1 += kblocks;
-            for (; c < c1; ++c) {
+            for (; c < c1; c += 2) {
                 const uint32_t sx = c % kXStages, s = c % kStages;
                 ok = mbar_wait_warp(sh, &sh->x_full[sx], c / kXStages & 1);
                 if (!ok) break;
-                uint4 q[4];
-                if (mine) {
+                uint4 q[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) q[j] = load_shared(from + sx * S::kXBytes + j * 4 * kBK);
-                }
+                for (int j = 0; j < 8; ++j)
+                    if (mine > j / 4 * 16) q[j] = load_shared(from + sx * S::kXBytes + j * 4 * kBK);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->x_empty[sx]);
                 ok = mbar_wait_warp(sh, &sh->empty[s], (c / kStages & 1) ^ 1);
                 if (!ok) break;
-                if (mine) {
+                const uint32_t to = at + s * kBBytes;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint4 lo, hi;
-                        widen4(q[j].x, lo.x, lo.y);
-                        widen4(q[j].y, lo.z, lo.w);
-                        widen4(q[j].z, hi.x, hi.y);
-                        widen4(q[j].w, hi.z, hi.w);
-                        const uint32_t to = ((at + s * kBBytes) ^ (j & 1) * 64) + j * 4 * 128;
-                        store_shared(to, lo);
-                        store_shared(to + kBAtom, hi);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
+                for (int j = 0; j < 8; ++j)
+                    if (mine > j / 4 * 16) widen_row<kBAtom>((to ^ (j & 1) * 64) + j * 4 * 128, q[j]);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive_leader<CG>(&sh->full[s]);
             }
         }
         // the last MMAs' arrivals on each stage land before the CTA ends
-        for (int s = 0; ok && s < kStages; ++s) {
-            const uint32_t uses = c1 / kStages + (c1 % kStages > (uint32_t)s ? 1 : 0);
-            if (uses > 0) ok = mbar_wait_warp(sh, &sh->empty[s], (uses - 1) & 1);
-        }
+        for (uint32_t i = c1 < kStages ? 0 : c1 - kStages; ok && i < c1; ++i)
+            ok = mbar_wait_warp(sh, &sh->empty[i % kStages], i / kStages & 1);
     } else if (warp >= kWeightWarp0) {
         // ---- weights -> float16 -> TMEM; two groups of 4 warps take turns ----
-        // (kWStages is even, so a group sees every phase of its stages; of the
-        // converted stages it sees every second phase of each, and knows from
-        // the stage before that the phase between them is over.)
+        // (the numbers of stages are even, so that a group sees every phase of
+        // the stages it uses)
         const int quarter = warp & 3, group = (warp - kWeightWarp0) >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t from = smem_u32(s_w) + row * 128 + ((row & 7) << 4);
@@ -554,19 +563,28 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             const int rows = ch < a.Nc ? t.rows : 0;
             uint8_t* to = static_cast<uint8_t*>(a.out) +
                           (first_row(a, t.e, t.begin) + t.first) * pitch + (size_t)ch * size;
+            // the rows' scales, two groups of 16 rows to a register
+            constexpr int kPairs = (S::TN + 63) / 64;
+            float xs[kPairs];
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                const int r = h * 16 + (i * 2 + (lane >> 4)) * 32 + (lane & 15);
+                const int src = r < t.rows ? source_row(a, t.e, t.begin, t.first + r) : -1;
+                xs[i] = src >= 0 ? __ldg(a.x_scales + src) : 0.0f;
+            }
             if (!mbar_wait_warp(sh, &sh->acc_full[acc], it / kAcc & 1)) break;
             tmem_fence_after();
             const uint32_t from = tmem + ((uint32_t)quarter << 21) + acc * S::TN;
-            for (int n0 = h * 16; n0 < t.n; n0 += 32) {
-                const int r = n0 + (lane & 15);
-                const int src = r < t.rows ? source_row(a, t.e, t.begin, t.first + r) : -1;
-                const float xs = src >= 0 ? __ldg(a.x_scales + src) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * kPairs; ++i) {
+                const int n0 = h * 16 + i * 32;
+                if (n0 >= t.n) break;  // uniform
                 uint32_t v[16];
                 tmem_load16(from + n0, v);
                 uint8_t* p = to + n0 * pitch;
 #pragma unroll
                 for (int j = 0; j < 16; ++j, p += pitch) {
-                    const float y = __uint_as_float(v[j]) * __shfl_sync(kFull, xs, j) * ws;
+                    const float y = __uint_as_float(v[j]) * __shfl_sync(kFull, xs[i / 2], (i & 1) * 16 + j) * ws;
                     if (n0 + j < rows) {
                         if (a.out_bf16) *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(y);
                         else *reinterpret_cast<float*>(p) = y;
