@@ -35,18 +35,19 @@ __device__ __forceinline__ size_t first_row(const MatmulArgs& a, int e, int begi
 }
 
 // Row tiles of the experts: s_tiles[i] = tiles of ceil(rows_e / tile) rows over
-// the experts before 4 i (a quarter of a full table, so that it costs 1 KB of
-// shared memory); s_tiles[kTileGroups] = all of them.  Computed by the block's
-// first 256 threads, 4 experts each; every thread calls it, and it ends with a
-// barrier.
-constexpr int kTileGroups = kMaxE / 4;
+// the experts before 8 i (an eighth of a full table, so that it takes half a KB
+// of shared memory); s_tiles[kTileGroups] = all of them.  Computed by the
+// block's first 128 threads, 8 experts each; every thread calls it, and it ends
+// with a barrier.
+constexpr int kPerGroup = 8;
+constexpr int kTileGroups = kMaxE / kPerGroup;
 __device__ __forceinline__ void tile_prefix(const MatmulArgs& a, int tile, int* s_tiles, int* s_warp) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int sum = 0, incl = 0;
     if (tid < kTileGroups) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int e = tid * 4 + j;
+        for (int j = 0; j < kPerGroup; ++j) {
+            const int e = tid * kPerGroup + j;
             int begin;
             sum += e < a.E ? (expert_rows(a, e, begin) + tile - 1) / tile : 0;
         }
@@ -73,6 +74,23 @@ struct ExpertTile {
     int first, count;     // its first tile, its number of tiles
 };
 
+// Among the experts of group g, the one that owns tile t: s_tiles[g] <= t <
+// s_tiles[g + 1].  Their offsets load together.
+__device__ __forceinline__ ExpertTile expert_in_group(const MatmulArgs& a, int tile, const int* s_tiles, int g, int t) {
+    int begin[kPerGroup], rows[kPerGroup];
+#pragma unroll
+    for (int j = 0; j < kPerGroup; ++j) {
+        begin[j] = rows[j] = 0;
+        if (g * kPerGroup + j < a.E) rows[j] = expert_rows(a, g * kPerGroup + j, begin[j]);
+    }
+    ExpertTile x = {g * kPerGroup, begin[0], rows[0], s_tiles[g], (rows[0] + tile - 1) / tile};
+#pragma unroll
+    for (int j = 1; j < kPerGroup; ++j)
+        if (t >= x.first + x.count && g * kPerGroup + j < a.E)
+            x = {g * kPerGroup + j, begin[j], rows[j], x.first + x.count, (rows[j] + tile - 1) / tile};
+    return x;
+}
+
 // The expert that owns tile t < s_tiles[kTileGroups].
 __device__ __forceinline__ ExpertTile expert_of_tile(const MatmulArgs& a, int tile, const int* s_tiles, int t) {
     int lo = 0, hi = kTileGroups;  // s_tiles[lo] <= t < s_tiles[hi]
@@ -80,16 +98,7 @@ __device__ __forceinline__ ExpertTile expert_of_tile(const MatmulArgs& a, int ti
         const int mid = (lo + hi) >> 1;
         if (s_tiles[mid] <= t) lo = mid; else hi = mid;
     }
-    ExpertTile x;
-    x.e = lo * 4;
-    x.first = s_tiles[lo];
-    for (;; ++x.e) {
-        x.rows = expert_rows(a, x.e, x.begin);
-        x.count = (x.rows + tile - 1) / tile;
-        if (t < x.first + x.count || (x.e & 3) == 3 || x.e + 1 >= a.E) break;
-        x.first += x.count;
-    }
-    return x;
+    return expert_in_group(a, tile, s_tiles, lo, t);
 }
 
 }  // namespace mm

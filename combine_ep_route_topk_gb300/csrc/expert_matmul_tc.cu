@@ -12,7 +12,7 @@
 // A tile is 128 channels a CTA (the M side: weights) x up to TN rows (the N
 // side).  CG = 1: one CTA.  CG = 2: a pair of CTAs on 256 channels, each
 // holding half of the rows' operand.
-//   TMA warp        weights, [128 channels x 128 bytes] boxes, 128-byte swizzle
+//   TMA warp        the list of tiles; weights, [128 channels x 128 bytes] boxes, 128-byte swizzle
 //   2 copying warps x rows, wherever they lie, by 16-byte background copies
 //   8 weight warps  8-bit stages -> float16 -> TMEM (the A operand's stages)
 //   row warps       8-bit stages -> float16 -> shared memory (B)
@@ -65,12 +65,19 @@ struct Shape {
 };
 
 constexpr int kMaxWStages = 8, kMaxXStages = 4;
+// Units published ahead.  The TMA warp publishes one when it has issued all
+// copies of those before, which its stages keep within 8 + 2 + 4 blocks of the
+// MMAs and the accumulators within 2 units more of the output warps: a slot is
+// read long before it is written again.
+constexpr int kUnitSlots = 32;
 struct Shared {
     uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
     uint64_t x_full[kMaxXStages], x_empty[kMaxXStages];
     uint64_t full[kStages], empty[kStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drained;
+    uint64_t unit_full[kUnitSlots];
+    int4 unit[kUnitSlots];
     uint32_t tmem;
     int abort;
     int warp_sums[8];
@@ -276,34 +283,76 @@ struct Unit {
     int n;           // rows rounded up to the MMA's granularity
 };
 
+// Units of one CTA (or pair): u0, u0 + du, ...  (A unit covers some 2^13
+// elements of an output in memory, so all of them are fewer than 2^32.)
 template <class S>
-struct Tiles {
-    static constexpr int kChannels = S::kChannels, kGrain = S::kGrain;
-    int ct;           // channel tiles
-    long long units;
+__device__ __forceinline__ uint32_t unit_count(const MatmulArgs& a, const Shared* sh, uint32_t u0, uint32_t du) {
+    const uint32_t all = (uint32_t)sh->tiles[kTileGroups] * (((uint32_t)a.Nc + S::kChannels - 1) / S::kChannels);
+    return all > u0 ? (all - u0 + du - 1) / du : 0;
+}
 
-    __device__ __forceinline__ Tiles(const MatmulArgs& a, const Shared* sh) {
-        ct = (a.Nc + kChannels - 1) / kChannels;
-        units = (long long)sh->tiles[kTileGroups] * ct;
+// Steps through them, for the warp that publishes them.  An expert's units are
+// consecutive, its row tiles innermost, so that CTAs which run together share
+// weights and rows in L2.  The place moves without a division, and the groups
+// of experts only forward.
+template <class S>
+struct Steps {
+    uint32_t ct;             // channel tiles
+    uint32_t tile, rest;     // the current unit is tile * ct + rest
+    uint32_t dtile, drest;
+    int group;
+
+    __device__ __forceinline__ Steps(const MatmulArgs& a, uint32_t u0, uint32_t du) {
+        ct = ((uint32_t)a.Nc + S::kChannels - 1) / S::kChannels;
+        tile = u0 / ct;
+        rest = u0 % ct;
+        dtile = du / ct;
+        drest = du % ct;
+        group = 0;
     }
-    // An expert's units are consecutive, its row tiles innermost, so that CTAs
-    // which run together share weights and rows in L2.
-    __device__ __forceinline__ Unit get(const MatmulArgs& a, const Shared* sh, long long u) const {
-        Unit t;
-        const ExpertTile x = expert_of_tile(a, S::TN, sh->tiles, (int)(u / ct));
-        const int nt = x.count, rows = x.rows;
-        const long long local = u - (long long)x.first * ct;
-        const int c = (int)(local / nt), i = (int)(local - (long long)c * nt);
-        t.e = x.e;
-        t.begin = x.begin;
-        const int per = ((rows + nt - 1) / nt + kGrain - 1) / kGrain * kGrain;
-        t.channel = c * kChannels;
-        t.first = i * per;
-        t.rows = min(per, rows - t.first);
-        t.n = (t.rows + kGrain - 1) / kGrain * kGrain;
-        return t;
+    // x: expert and rows of the tile; y: the expert's first position; z: channel
+    // tile; w: first row of the tile among the expert's
+    __device__ __forceinline__ int4 next(const MatmulArgs& a, const Shared* sh) {
+        while (sh->tiles[group + 1] <= (int)tile) ++group;
+        const ExpertTile x = expert_in_group(a, S::TN, sh->tiles, group, (int)tile);
+        uint32_t c = rest, i = 0, per = (uint32_t)x.rows;
+        if (x.count > 1) {  // rows divided evenly among the tiles
+            const uint32_t local = (tile - x.first) * ct + rest;
+            c = local / (uint32_t)x.count;
+            i = local - c * x.count;
+            per = (per + x.count - 1) / (uint32_t)x.count;
+        }
+        per = (per + S::kGrain - 1) / S::kGrain * S::kGrain;
+        const int first = (int)(i * per);
+        tile += dtile;
+        rest += drest;
+        if (rest >= ct) {
+            rest -= ct;
+            ++tile;
+        }
+        return make_int4(x.e | min((int)per, x.rows - first) << 10, x.begin, (int)c, first);
     }
 };
+
+template <class S>
+__device__ __forceinline__ Unit unpack(int4 q) {
+    Unit t;
+    t.e = q.x & (kMaxE - 1);
+    t.begin = q.y;
+    t.channel = q.z * S::kChannels;
+    t.first = q.w;
+    t.rows = q.x >> 10;
+    t.n = (t.rows + S::kGrain - 1) / S::kGrain * S::kGrain;
+    return t;
+}
+
+// Unit u of this CTA, once it is published (by a whole warp).
+template <class S>
+__device__ __forceinline__ bool get_unit(Shared* sh, uint32_t u, Unit& t) {
+    if (!mbar_wait_warp(sh, &sh->unit_full[u % kUnitSlots], u / kUnitSlots & 1)) return false;
+    t = unpack<S>(sh->unit[u % kUnitSlots]);
+    return true;
+}
 
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, 1)
@@ -337,6 +386,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             mbar_init(&sh->acc_full[i], 1);
             mbar_init(&sh->acc_empty[i], kOutWarps * CG);
         }
+        for (int i = 0; i < kUnitSlots; ++i) mbar_init(&sh->unit_full[i], 1);
         mbar_init(&sh->drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (a.status != nullptr && blockIdx.x == 0) *a.status = 0;
@@ -357,36 +407,44 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
     }
     tmem_fence_after();
     const uint32_t tmem = sh->tmem;
-    const Tiles<S> tiles(a, sh);
+    const uint32_t units = unit_count<S>(a, sh, blockIdx.x / CG, gridDim.x / CG);
     const int kblocks = (a.Kd + kBK - 1) / kBK;
-    const long long u0 = blockIdx.x / CG, du = gridDim.x / CG;
 
     if (warp == kTmaWarp) {
-        // ---- weights: TMA boxes ----
-        if (lane == 0) {
-            uint32_t c = 0;  // stages issued so far
-            bool ok = true;
-            for (long long u = u0; ok && u < tiles.units; u += du) {
-                const Unit t = tiles.get(a, sh, u);
-                const int row = t.e * a.Nc + t.channel + rank * 128;
-                for (int kb = 0; kb < kblocks; ++kb, ++c) {
-                    const uint32_t s = c % kWStages;
-                    ok = mbar_wait(sh, &sh->w_empty[s], (c / kWStages & 1) ^ 1);
-                    if (!ok) break;
+        // ---- units, and the weights' TMA boxes ----
+        Steps<S> steps(a, blockIdx.x / CG, gridDim.x / CG);
+        uint32_t c = 0;  // stages issued so far
+        bool ok = true;
+        for (uint32_t u = 0; ok && u < units; ++u) {
+            const int4 packed = steps.next(a, sh);
+            if (lane == 0) {
+                sh->unit[u % kUnitSlots] = packed;
+                mbar_arrive(&sh->unit_full[u % kUnitSlots]);
+            }
+            const Unit t = unpack<S>(packed);
+            const int row = t.e * a.Nc + t.channel + rank * 128;
+            for (int kb = 0; kb < kblocks; ++kb, ++c) {
+                const uint32_t s = c % kWStages;
+                ok = mbar_wait_warp(sh, &sh->w_empty[s], (c / kWStages & 1) ^ 1);
+                if (!ok) break;
+                if (elect_one()) {
                     mbar_expect_tx(&sh->w_full[s], kWBytes);
                     tma_load(&w_map, &sh->w_full[s], s_w + s * kWBytes, kb * kBK, row);
                 }
+                __syncwarp();
             }
-            if (!ok) drain_copies<kWStages>(sh->w_full, c);
         }
+        if (!ok && lane == 0) drain_copies<kWStages>(sh->w_full, c);
     } else if (warp == kMmaWarp) {
         // ---- MMA: the warp waits together, one elected lane issues ----
         if (rank == 0) {
             const uint64_t desc0 = operand_desc(smem_u32(s_b));
             uint32_t c = 0, it = 0;
             bool ok = true;
-            for (long long u = u0; ok && u < tiles.units; u += du, ++it) {
-                const Unit t = tiles.get(a, sh, u);
+            for (uint32_t u = 0; ok && u < units; ++u, ++it) {
+                Unit t;
+                ok = get_unit<S>(sh, u, t);
+                if (!ok) break;
                 const uint32_t acc = it % kAcc;
                 // float32 accumulators, float16 operands, both K-major
                 const uint32_t idesc = 1u << 4 | (uint32_t)(t.n >> 3) << 17 | (uint32_t)(128 * CG >> 4) << 24;
@@ -439,8 +497,10 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         const uint32_t to = smem_u32(s_x) + r0 * kBK + chunk * 16;
         uint32_t c = 0;
         bool ok = true;
-        for (long long u = u0; ok && u < tiles.units; u += du) {
-            const Unit t = tiles.get(a, sh, u);
+        for (uint32_t u = 0; ok && u < units; ++u) {
+            Unit t;
+            ok = get_unit<S>(sh, u, t);
+            if (!ok) break;
             const int half = t.n / CG;  // this CTA's rows of the tile, a multiple of 16
             const int8_t* src[kPer];
 #pragma unroll
@@ -479,8 +539,11 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         const uint32_t at = smem_u32(s_b) + (r0 + l8) * 128 + ((chunk ^ l8) << 4);
         uint32_t c = group, c1 = 0;
         bool ok = true;
-        for (long long u = u0; ok && u < tiles.units; u += du) {
-            const int mine = tiles.get(a, sh, u).n / CG - r0;  // rows of this warp, if any: 16, or all 32
+        for (uint32_t u = 0; ok && u < units; ++u) {
+            Unit t;
+            ok = get_unit<S>(sh, u, t);
+            if (!ok) break;
+            const int mine = t.n / CG - r0;  // rows of this warp, if any: 16, or all 32
             c1 += kblocks;
             for (; c < c1; c += 2) {
                 const uint32_t sx = c % kXStages, s = c % kStages;
@@ -514,7 +577,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         const int row = quarter * 32 + lane;
         const uint32_t from = smem_u32(s_w) + row * 128 + ((row & 7) << 4);
         const uint32_t to = tmem + ((uint32_t)quarter << 21) + kTmemA;
-        const uint32_t total = tiles.units > u0 ? (uint32_t)((tiles.units - u0 + du - 1) / du) * kblocks : 0;
+        const uint32_t total = units * kblocks;
         bool ok = true;
         for (uint32_t c = group; ok && c < total; c += 2) {
             const uint32_t sw = c % kWStages, s = c % kStages;
@@ -555,8 +618,9 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         uint32_t it = 0;
         const int size = a.out_bf16 ? 2 : 4;
         const size_t pitch = (size_t)a.Nc * size;
-        for (long long u = u0; u < tiles.units; u += du, ++it) {
-            const Unit t = tiles.get(a, sh, u);
+        for (uint32_t u = 0; u < units; ++u, ++it) {
+            Unit t;
+            if (!get_unit<S>(sh, u, t)) break;
             const uint32_t acc = it % kAcc;
             const int ch = t.channel + rank * 128 + quarter * 32 + lane;
             const float ws = ch < a.Nc ? __ldg(a.w_scales + (size_t)t.e * a.Nc + ch) : 0.0f;
@@ -678,6 +742,7 @@ cudaError_t persistent_grid(int* grid) {
 template <class S>
 cudaError_t launch_tc(const MatmulArgs& a, cudaStream_t s) {
     constexpr int CG = S::CG;
+    static_assert(kSmemBytes<S> <= 227 * 1024, "a CTA's shared memory");
     const EncodeTiled encode = encode_tiled();
     if (encode == nullptr) return cudaErrorNotSupported;
     CUtensorMap w_map;
