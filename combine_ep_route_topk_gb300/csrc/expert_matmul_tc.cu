@@ -35,7 +35,7 @@ namespace {
 
 using namespace mm;
 
-constexpr int kStages = 4;            // stages of converted operands
+constexpr int kStages = 3;            // stages of converted operands
 constexpr int kBK = 128;              // K of a stage
 constexpr int kWBytes = 128 * kBK;    // one stage of 8-bit weights
 constexpr int kOutWarps = 8, kWeightWarp0 = kOutWarps, kWeightWarps = 8;
@@ -70,6 +70,7 @@ constexpr int kMaxWStages = 8, kMaxXStages = 4;
 // MMAs and the accumulators within 2 units more of the output warps: a slot is
 // read long before it is written again.
 constexpr int kUnitSlots = 32;
+constexpr int kOutPitch = 80;
 struct Shared {
     uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
     uint64_t x_full[kMaxXStages], x_empty[kMaxXStages];
@@ -78,6 +79,10 @@ struct Shared {
     uint64_t drained;
     uint64_t unit_full[kUnitSlots];
     int4 unit[kUnitSlots];
+    float row_scales[kOutWarps][128];  // of the rows that an output warp stores
+    // 16 rows x 32 channels of an output warp on their way to memory; rows 80
+    // bytes apart, so that the 8 rows of a stored matrix hit different banks
+    uint8_t out[kOutWarps][16 * kOutPitch];
     uint32_t tmem;
     int abort;
     int warp_sums[8];
@@ -233,6 +238,26 @@ __device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(at) : "memory");
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// 16 lanes (channels) x 16 columns: registers 4 g .. 4 g + 3 hold columns 8 g +
+// 2 (lane % 4) and the next, of channel lane / 4 and of channel lane / 4 + 8.
+__device__ __forceinline__ void tmem_load_tile(uint32_t at, float (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(at) : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed; lane i gives the address of
+// row i % 8 of matrix i / 8.
+__device__ __forceinline__ void store_matrices(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // Four 8-bit integers -> four float16: with the sign bit flipped a byte u is
@@ -571,8 +596,10 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             ok = mbar_wait_warp(sh, &sh->empty[i % kStages], i / kStages & 1);
     } else if (warp >= kWeightWarp0) {
         // ---- weights -> float16 -> TMEM; two groups of 4 warps take turns ----
-        // (the numbers of stages are even, so that a group sees every phase of
-        // the stages it uses)
+        // (kWStages and kXStages are even, so that a group sees every phase of
+        // the 8-bit stages it uses.  Of a converted stage it sees every second
+        // phase; MMAs end in order, so its wait two blocks before has shown it
+        // that the phase which has the same parity is over.)
         const int quarter = warp & 3, group = (warp - kWeightWarp0) >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t from = smem_u32(s_w) + row * 128 + ((row & 7) << 4);
@@ -615,43 +642,74 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
     } else {
         // ---- accumulators -> out; two warps per 32 channels, 16 of every 32 rows each ----
         const int quarter = warp & 3, h = warp >> 2;
-        uint32_t it = 0;
+        float* row_scales = sh->row_scales[warp];
+        const uint32_t stage = smem_u32(sh->out[warp]);
+        const bool vectors = a.out_bf16 && a.Nc % 8 == 0;  // rows of out start on 16 bytes
         const int size = a.out_bf16 ? 2 : 4;
         const size_t pitch = (size_t)a.Nc * size;
-        for (uint32_t u = 0; u < units; ++u, ++it) {
+        for (uint32_t u = 0; u < units; ++u) {
             Unit t;
             if (!get_unit<S>(sh, u, t)) break;
-            const uint32_t acc = it % kAcc;
-            const int ch = t.channel + rank * 128 + quarter * 32 + lane;
-            const float ws = ch < a.Nc ? __ldg(a.w_scales + (size_t)t.e * a.Nc + ch) : 0.0f;
-            const int rows = ch < a.Nc ? t.rows : 0;
+            const uint32_t acc = u % kAcc;
+            const int ch0 = t.channel + rank * 128 + quarter * 32;  // this warp's channels
             uint8_t* to = static_cast<uint8_t*>(a.out) +
-                          (first_row(a, t.e, t.begin) + t.first) * pitch + (size_t)ch * size;
-            // the rows' scales, two groups of 16 rows to a register
-            constexpr int kPairs = (S::TN + 63) / 64;
-            float xs[kPairs];
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i) {
-                const int r = h * 16 + (i * 2 + (lane >> 4)) * 32 + (lane & 15);
+                          (first_row(a, t.e, t.begin) + t.first) * pitch + (size_t)ch0 * size;
+            for (int i = lane; i < S::TN / 2; i += 32) {
+                const int r = (i >> 4) * 32 + h * 16 + (i & 15);
                 const int src = r < t.rows ? source_row(a, t.e, t.begin, t.first + r) : -1;
-                xs[i] = src >= 0 ? __ldg(a.x_scales + src) : 0.0f;
+                row_scales[i] = src >= 0 ? __ldg(a.x_scales + src) : 0.0f;
             }
-            if (!mbar_wait_warp(sh, &sh->acc_full[acc], it / kAcc & 1)) break;
+            const float* ws_e = a.w_scales + (size_t)t.e * a.Nc;
+            float ws[4];  // of channels lane / 4 + 8 i; or the lane's own
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ch = ch0 + (vectors ? (lane >> 2) + i * 8 : lane);
+                ws[i] = ch < a.Nc ? __ldg(ws_e + ch) : 0.0f;
+            }
+            __syncwarp();
+            if (!mbar_wait_warp(sh, &sh->acc_full[acc], u / kAcc & 1)) break;
             tmem_fence_after();
             const uint32_t from = tmem + ((uint32_t)quarter << 21) + acc * S::TN;
+            if (vectors) {
+                const int part = (lane & 3) * 8;  // 8 channels of one row: 16 bytes
+                const bool in = ch0 + part < a.Nc;
+                for (int n0 = h * 16, i0 = 0; n0 < t.n; n0 += 32, i0 += 16) {
+                    float lo[8], hi[8];  // channels 0 .. 15 and 16 .. 31
+                    tmem_load_tile(from + n0, lo);
+                    tmem_load_tile(from + n0 + (16u << 16), hi);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-            for (int i = 0; i < 2 * kPairs; ++i) {
-                const int n0 = h * 16 + i * 32;
-                if (n0 >= t.n) break;  // uniform
-                uint32_t v[16];
-                tmem_load16(from + n0, v);
-                uint8_t* p = to + n0 * pitch;
+                    for (int g = 0; g < 2; ++g) {
+                        const float2 xs = *reinterpret_cast<const float2*>(row_scales + i0 + g * 8 + (lane & 3) * 2);
+                        const int j = g * 4;
+                        store_matrices(stage + (g * 8 + (lane & 7)) * kOutPitch + (lane >> 3) * 16,
+                                       pack_bf16(lo[j] * xs.x * ws[0], lo[j + 1] * xs.y * ws[0]),
+                                       pack_bf16(lo[j + 2] * xs.x * ws[1], lo[j + 3] * xs.y * ws[1]),
+                                       pack_bf16(hi[j] * xs.x * ws[2], hi[j + 1] * xs.y * ws[2]),
+                                       pack_bf16(hi[j + 2] * xs.x * ws[3], hi[j + 3] * xs.y * ws[3]));
+                    }
+                    __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 16; ++j, p += pitch) {
-                    const float y = __uint_as_float(v[j]) * __shfl_sync(kFull, xs[i / 2], (i & 1) * 16 + j) * ws;
-                    if (n0 + j < rows) {
-                        if (a.out_bf16) *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(y);
-                        else *reinterpret_cast<float*>(p) = y;
+                    for (int g = 0; g < 2; ++g) {
+                        const int r = g * 8 + (lane >> 2);
+                        const uint4 v = load_shared(stage + r * kOutPitch + part * 2);
+                        if (in && n0 + r < t.rows) *reinterpret_cast<uint4*>(to + (n0 + r) * pitch + part * 2) = v;
+                    }
+                    __syncwarp();  // the stage is free again
+                }
+            } else {
+                const int rows = ch0 + lane < a.Nc ? t.rows : 0;
+                for (int n0 = h * 16, i0 = 0; n0 < t.n; n0 += 32, i0 += 16) {
+                    uint32_t v[16];
+                    tmem_load16(from + n0, v);
+                    uint8_t* p = to + n0 * pitch + lane * size;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, p += pitch) {
+                        const float y = __uint_as_float(v[j]) * row_scales[i0 + j] * ws[0];
+                        if (n0 + j < rows) {
+                            if (a.out_bf16) *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(y);
+                            else *reinterpret_cast<float*>(p) = y;
+                        }
                     }
                 }
             }
