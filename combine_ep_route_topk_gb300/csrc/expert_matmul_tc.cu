@@ -35,7 +35,6 @@ namespace {
 
 using namespace mm;
 
-constexpr int kStages = 3;            // stages of converted operands
 constexpr int kBK = 128;              // K of a stage
 constexpr int kWBytes = 128 * kBK;    // one stage of 8-bit weights
 constexpr int kOutWarps = 8, kWeightWarp0 = kOutWarps, kWeightWarps = 8;
@@ -54,8 +53,9 @@ struct Shape {
     static constexpr int kRows = TN / CG;
     static constexpr int kBAtom = kRows * 128;       // 64 K of the rows, float16
     static constexpr int kBBytes = 2 * kBAtom;       // one stage
+    static constexpr int kStages = kRows <= 64 ? 4 : 3;   // converted operands
     static constexpr int kXBytes = kRows * kBK;      // one stage of 8-bit rows
-    static constexpr int kWStages = kRows <= 64 ? 8 : 4;  // 8-bit weights in flight
+    static constexpr int kWStages = kRows <= 64 ? 6 : 4;  // 8-bit weights in flight
     static constexpr int kXStages = kRows <= 64 ? 4 : 2;  // 8-bit rows in flight
     static constexpr int kRowWarps = kRows / 16;
     static constexpr int kThreads = (kRowWarp0 + kRowWarps) * 32;
@@ -64,7 +64,7 @@ struct Shape {
     static constexpr int kGrain = 16 * CG;           // an MMA's N is a multiple
 };
 
-constexpr int kMaxWStages = 8, kMaxXStages = 4;
+constexpr int kMaxStages = 4, kMaxWStages = 8, kMaxXStages = 4;
 // Units published ahead.  The TMA warp publishes one when it has issued all
 // copies of those before, which its stages keep within 8 + 2 + 4 blocks of the
 // MMAs and the accumulators within 2 units more of the output warps: a slot is
@@ -74,7 +74,7 @@ constexpr int kOutPitch = 80;
 struct Shared {
     uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
     uint64_t x_full[kMaxXStages], x_empty[kMaxXStages];
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drained;
     uint64_t unit_full[kUnitSlots];
@@ -89,7 +89,7 @@ struct Shared {
     int tiles[kTileGroups + 1];
 };
 template <class S>
-constexpr int kSmemBytes = 1024 + kStages * S::kBBytes + S::kWStages * kWBytes + S::kXStages * S::kXBytes +
+constexpr int kSmemBytes = 1024 + S::kStages * S::kBBytes + S::kWStages * kWBytes + S::kXStages * S::kXBytes +
                            (int)sizeof(Shared);
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -382,7 +382,7 @@ __device__ __forceinline__ bool get_unit(Shared* sh, uint32_t u, Unit& t) {
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, 1)
 matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
-    constexpr int CG = S::CG, kAcc = S::kAcc, kWStages = S::kWStages, kXStages = S::kXStages;
+    constexpr int CG = S::CG, kAcc = S::kAcc, kStages = S::kStages, kWStages = S::kWStages, kXStages = S::kXStages;
     constexpr int kBBytes = S::kBBytes, kBAtom = S::kBAtom;
     extern __shared__ uint8_t s_raw[];
     uint8_t* s_b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
