@@ -20,6 +20,14 @@ chunked
     latency-bound routing and layout run under the previous round's
     HBM-bound dispatch and combine.
 
+expert_layer
+    A whole layer of 8-bit experts on one GPU: the scored gate, the layout,
+    the tokens quantised once and read in place by the experts' first product
+    (through the layout's row_src, so there is no dispatched copy), SwiGLU and
+    quantisation in one pass, the second product, and the combine.  The same
+    seven calls serve prefill (contiguous) and decode (masked), without an
+    allocation, so a step can be captured in a CUDA graph.
+
 HostPipeline
     Steps whose inputs and result live in pinned host memory: the binding of
     the library's native pipeline (ep_host_pipeline_*).  Copies in, kernels
@@ -235,6 +243,87 @@ def chunked(logits, x, rank_offsets_host, K, dtype, bufs, expert_out, comb, ro_r
         for b in sets:
             main.wait_stream(b.stream)
     return rounds
+
+
+@dataclass
+class ExpertWeights:
+    """Gated-linear experts in 8-bit integers: up [E, 2 I, H] (the gate half
+    first) and down [E, H, I], with a float32 scale per output channel."""
+    up: torch.Tensor
+    up_scales: torch.Tensor
+    down: torch.Tensor
+    down_scales: torch.Tensor
+
+
+def quantize_expert_weights(up, down):
+    """bf16 or float32 weights up [E, 2 I, H] and down [E, H, I] on the GPU ->
+    ExpertWeights: each output channel is a row to ep_quantize_rows."""
+    def one(w):
+        q, scales = _ep.ep_quantize_rows(w.reshape(-1, w.shape[2]))
+        return q.view(w.shape), scales.view(w.shape[:2])
+    if up.dim() != 3 or down.shape != (up.shape[0], up.shape[2], up.shape[1] // 2):
+        raise ValueError(f"up {tuple(up.shape)} and down {tuple(down.shape)} are not "
+                         "[E, 2 I, H] and [E, H, I]")
+    return ExpertWeights(*one(up), *one(down))
+
+
+@dataclass
+class LayerBuffers:
+    """Everything that expert_layer writes for N tokens."""
+    layout: int
+    cap: int
+    idx: torch.Tensor
+    wt: torch.Tensor
+    lay: _ep.Layout
+    ws: torch.Tensor
+    xq: torch.Tensor            # the tokens' codes [N, H] and scales [N]
+    xs: torch.Tensor
+    up: torch.Tensor            # [rows, 2 I] bf16
+    hq: torch.Tensor            # SwiGLU's codes [rows, I] and scales [rows]
+    hs: torch.Tensor
+    down: torch.Tensor          # [rows, H] bf16
+    comb: torch.Tensor          # [N, H] bf16
+
+
+def make_layer_buffers(N, E, K, H, inner, R, cap=0, device="cuda"):
+    """Buffers for N tokens over experts of inner width `inner`; cap > 0: the
+    masked layout with that capacity per expert."""
+    layout = _ep.EP_LAYOUT_MASKED if cap > 0 else _ep.EP_LAYOUT_CONTIG
+    rows = _ep.dispatch_rows(N, K, E, layout, cap)
+
+    def z(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=device)
+    return LayerBuffers(
+        layout, cap, z((N, K), torch.int32), z((N, K), torch.float32),
+        _ep.alloc_layout(N, E, K, R, cap, device),
+        z(_ep.ep_dispatch_layout_workspace_size(N, E, K, R), torch.uint8),
+        z((N, H), torch.int8), z((N,), torch.float32), z((rows, 2 * inner), torch.bfloat16),
+        z((rows, inner), torch.int8), z((rows,), torch.float32), z((rows, H), torch.bfloat16),
+        z((N, H), torch.bfloat16))
+
+
+def expert_layer(x, logits, rank_offsets, weights, buf, score=_ep.EP_SCORE_SIGMOID, bias=None,
+                 groups=1, topk_groups=None, group_top=2, renorm=True, scale=1.0,
+                 expert_map=None):
+    """x bf16 [N, H], logits [N, E] -> buf.comb bf16 [N, H], on the current
+    stream.  The gate's arguments are ep_gate_topk's.  For training, buf.idx and
+    the gradient of buf.wt go to ep_gate_topk_backward."""
+    E = logits.shape[1]
+    K = buf.idx.shape[1]
+    lay, off = buf.lay, buf.lay.expert_offsets
+    _ep.ep_gate_topk(logits, K, score, bias=bias, groups=groups, topk_groups=topk_groups,
+                     group_top=group_top, renorm=renorm, scale=scale, expert_map=expert_map,
+                     topk_idx=buf.idx, topk_w=buf.wt)
+    _ep.ep_dispatch_layout(buf.idx, rank_offsets, E, buf.cap, out=lay, workspace=buf.ws)
+    _ep.ep_quantize_rows(x, q=buf.xq, scales=buf.xs)
+    _ep.ep_expert_matmul(buf.xq, buf.xs, weights.up, weights.up_scales, off, layout=buf.layout,
+                         cap=buf.cap, row_src=lay.row_src, out=buf.up)
+    _ep.ep_quantize_rows(buf.up, act=_ep.EP_ACT_SWIGLU, expert_offsets=off, layout=buf.layout,
+                         cap=buf.cap, q=buf.hq, scales=buf.hs)
+    _ep.ep_expert_matmul(buf.hq, buf.hs, weights.down, weights.down_scales, off,
+                         layout=buf.layout, cap=buf.cap, out=buf.down)
+    return _ep.ep_combine(buf.down, buf.idx, buf.wt, lay.pos, off, E, layout=buf.layout,
+                          cap=buf.cap, out=buf.comb)
 
 
 def host_empty(shape, dtype):
