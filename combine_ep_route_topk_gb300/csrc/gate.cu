@@ -29,7 +29,8 @@ namespace ep {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kGateWarps = 8;  // tokens per block
+constexpr int kGateWarps = 8;
+constexpr int kGradManyTokens = 4096;  // from here four tokens a warp
 
 // False for NaN and -inf.
 __device__ __forceinline__ bool available(float v) { return v > -INFINITY; }
@@ -55,24 +56,28 @@ __device__ __forceinline__ void load_four(const __nv_bfloat16* p, float* v) {
     v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Sum and maximum over aligned groups of G lanes.
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    for (int off = G / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int G>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+    for (int off = G / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
     return v;
 }
 
-// The share s_k / sum_j s_j of the lane's pick (logit l) among the warp's
-// picks; 0 on lanes without one.  The scores are taken relative to the largest
+// The share s_k / sum_j s_j of the lane's pick (logit l) among the picks of its
+// token, which G lanes hold; 0 on lanes without one.  The scores are taken relative to the largest
 // pick's, exp(l - c) with c = max l for the softmax and min(0, max l) for the
 // sigmoid, so that no sum underflows however far below the others' the picks'
 // scores lie.
+template <int G>
 __device__ __forceinline__ float pick_share(float l, bool picked, int score) {
-    float c = warp_max(picked ? l : -INFINITY);
+    float c = lanes_max<G>(picked ? l : -INFINITY);
     float s = 0.0f;
     if (score == kScoreSigmoid) {
         c = fminf(c, 0.0f);
@@ -81,7 +86,7 @@ __device__ __forceinline__ float pick_share(float l, bool picked, int score) {
     } else if (picked) {
         s = expf(l - c);
     }
-    const float sum = warp_sum(s);  // at least 1/2 where anything is picked
+    const float sum = lanes_sum<G>(s);  // at least 1/2 where anything is picked
     return picked ? __fdiv_rn(s, sum) : 0.0f;
 }
 
@@ -108,22 +113,20 @@ __device__ __forceinline__ void load_row(const T* row, int E, bool vec, int lane
         v[j] = (e0 + j < E) ? load_one(row + e0 + j) : __int_as_float(0x7fffffff);
 }
 
-// Sorts v descending: Batcher's odd-even merge sort (1968).
-template <int N>
+// Sorts v descending: Batcher's odd-even merge sort (1968), one step a call.
+template <int N, int P = 1, int K = 1>
 __device__ __forceinline__ void sort_descending(float (&v)[N]) {
+    if constexpr (P < N) {
 #pragma unroll
-    for (int p = 1; p < N; p *= 2)
-#pragma unroll
-        for (int k = p; k >= 1; k /= 2)
-#pragma unroll
-            for (int j = k % p; j + k < N; j += 2 * k)
-#pragma unroll
-                for (int i = 0; i < k; ++i)
-                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-                        const float hi = fmaxf(v[i + j], v[i + j + k]);
-                        v[i + j + k] = fminf(v[i + j], v[i + j + k]);
-                        v[i + j] = hi;
-                    }
+        for (int x = K % P; x + K < N; ++x)
+            if ((x - K % P) % (2 * K) < K && x / (2 * P) == (x + K) / (2 * P)) {
+                const float hi = fmaxf(v[x], v[x + K]);
+                v[x + K] = fminf(v[x], v[x + K]);
+                v[x] = hi;
+            }
+        if constexpr (K > 1) sort_descending<N, P, K / 2>(v);
+        else sort_descending<N, P * 2, P * 2>(v);
+    }
 }
 
 // Maximum over the warp.
@@ -151,6 +154,28 @@ __device__ __forceinline__ void two_best(float x, float& a, float& b) {
     a = fmaxf(a, x);
 }
 
+// For groups of L whole lanes: the lanes' two largest keys are merged, scored,
+// and the number of groups that come before the lane's returned.  (Lanes past E
+// hold groups of nothing, which come last.)
+template <int L, typename F>
+__device__ __forceinline__ int groups_before(float best, float second, int lane, F group_score) {
+#pragma unroll
+    for (int off = 1; off < L; off <<= 1) {
+        const float o1 = __shfl_xor_sync(kFull, best, off);
+        const float o2 = __shfl_xor_sync(kFull, second, off);
+        second = fmaxf(fminf(best, o1), fmaxf(second, o2));
+        best = fmaxf(best, o1);
+    }
+    const float score = group_score(best, second);
+    int before = 0;
+#pragma unroll
+    for (int x = L; x < 32; x += L) {
+        const float other = __shfl_xor_sync(kFull, score, x);
+        before += (lane ^ x) < lane ? other >= score : other > score;
+    }
+    return before;
+}
+
 // KT > 0: K == KT known at compile time.
 template <int VPL, typename T, int KT>
 __global__ void __launch_bounds__(kGateWarps * 32)
@@ -164,90 +189,98 @@ gate_kernel(GateArgs a) {
     const int E = a.E, K = KT > 0 ? KT : a.K;
     const T* row = static_cast<const T*>(a.logits) + (size_t)t * E;
     const int e0 = lane * VPL;
+    const bool groups_sum = a.groups > 1 && a.group_top == 2;
+    const bool sigmoids = a.score == kScoreSigmoid;
+    const unsigned lower = (1u << lane) - 1;  // the lanes below
 
-    float v[VPL];
+    float v[VPL], bias[VPL];
     load_row<VPL>(row, E, a.vec != 0, lane, v);
+    if (a.bias != nullptr) {
+        load_row<VPL>(a.bias, E, a.bias_vec != 0, lane, bias);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) bias[j] = fmaxf(bias[j], -INFINITY);  // NaN: not available
+    }
 
     // softmax: the largest available logit, and the sum where a score is needed
-    const bool groups_sum = a.groups > 1 && a.group_top == 2;
-    const bool all_scores = a.bias != nullptr || groups_sum;
     float m = 0.0f, total = 1.0f;
-    if (a.score == kScoreSoftmax) {
+    if (!sigmoids) {
         m = -INFINITY;
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
             if (available(v[j])) m = fmaxf(m, clamp_logit(v[j]));
         m = redux_max(m);
-        if (all_scores || !a.renorm) {
+        if (a.bias != nullptr || groups_sum || !a.renorm) {
             float sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
                 if (available(v[j])) sum += expf(clamp_logit(v[j]) - m);
-            total = warp_sum(sum);
+            total = lanes_sum<32>(sum);
         }
     }
 
-    // keys (-inf: not available), and s + bias where groups are scored by sums
-    float key[VPL], c[VPL];
-    if (all_scores) {
-        const bool sigmoids = a.score == kScoreSigmoid;
-        const float mul = sigmoids ? -kLog2e : kLog2e, inv_total = rcp_fast(total);
-        float bias[VPL];
-        if (a.bias != nullptr) load_row<VPL>(a.bias, E, a.bias_vec != 0, lane, bias);
+    // keys (-inf: not available)
+    const float inv_total = rcp_fast(total);
+    float key[VPL];
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const float l = clamp_logit(v[j]);
-            const float e = exp2_fast((l - m) * mul);
-            float x = sigmoids ? rcp_fast(1.0f + e) : e * inv_total;
-            if (a.bias != nullptr) x += bias[j];
-            c[j] = available(v[j]) ? fmaxf(x, -INFINITY) : -INFINITY;  // a NaN of the bias -> -inf
-            key[j] = a.bias != nullptr ? c[j] : available(v[j]) ? l : -INFINITY;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            key[j] = available(v[j]) ? clamp_logit(v[j]) : -INFINITY;
-            c[j] = key[j];
-        }
+    for (int j = 0; j < VPL; ++j) {
+        float x;
+        if (a.bias != nullptr)  // a sigmoid of +inf is 1 without a clamp
+            x = (sigmoids ? rcp_fast(1.0f + exp2_fast(v[j] * -kLog2e))
+                          : exp2_fast((clamp_logit(v[j]) - m) * kLog2e) * inv_total) + bias[j];
+        else
+            x = clamp_logit(v[j]);
+        key[j] = available(v[j]) ? x : -INFINITY;
     }
+    float list[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) list[j] = key[j];
+    sort_descending(list);
+
     if (a.groups > 1) {
         const int per = E / a.groups;
+        // a group's score from its two largest keys
+        const auto group_score = [&](float best, float second) {
+            if (!groups_sum) return best;
+            if (a.bias == nullptr) {  // the keys are logits
+                best = !available(best) ? best
+                       : sigmoids ? rcp_fast(1.0f + exp2_fast(best * -kLog2e))
+                                  : exp2_fast((best - m) * kLog2e) * inv_total;
+                second = !available(second) ? second
+                         : sigmoids ? rcp_fast(1.0f + exp2_fast(second * -kLog2e))
+                                    : exp2_fast((second - m) * kLog2e) * inv_total;
+            }
+            return available(second) ? best + second : best;
+        };
         if (a.lanes_per_group > 0) {
             // whole lanes of one group next to each other, a power of two of them
-            float best = -INFINITY, second = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) two_best(groups_sum ? c[j] : key[j], best, second);
-            for (int off = 1; off < a.lanes_per_group; off <<= 1) {
-                const float o1 = __shfl_xor_sync(kFull, best, off);
-                const float o2 = __shfl_xor_sync(kFull, second, off);
-                second = fmaxf(fminf(best, o1), fmaxf(second, o2));
-                best = fmaxf(best, o1);
-            }
-            if (groups_sum && second > -INFINITY) best += second;
-            const int g = lane / a.lanes_per_group;
+            const float second = VPL > 1 ? list[VPL > 1 ? 1 : 0] : -INFINITY;
             int before = 0;
-            for (int o = 0; o < a.groups; ++o) {
-                const float other = __shfl_sync(kFull, best, o * a.lanes_per_group);
-                before += (other > best || (other == best && o < g)) ? 1 : 0;
+            switch (a.lanes_per_group) {
+                case 1: before = groups_before<1>(list[0], second, lane, group_score); break;
+                case 2: before = groups_before<2>(list[0], second, lane, group_score); break;
+                case 4: before = groups_before<4>(list[0], second, lane, group_score); break;
+                case 8: before = groups_before<8>(list[0], second, lane, group_score); break;
+                default: before = groups_before<16>(list[0], second, lane, group_score); break;
             }
             if (before >= a.topk_groups) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) key[j] = -INFINITY;
+                for (int j = 0; j < VPL; ++j) list[j] = -INFINITY;
             }
         } else {
-            float* mine = s_choice + (size_t)warp * E;
+            float* choice = s_choice + (size_t)warp * E;
+            __syncwarp();
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                if (e0 + j < E) mine[e0 + j] = groups_sum ? c[j] : key[j];
+                if (e0 + j < E) choice[e0 + j] = key[j];
             __syncwarp();
             float best = -INFINITY, second = -INFINITY;
             if (lane < a.groups) {
-                int i = lane % per;  // start apart, so that the lanes' banks differ
+                int at = lane % per;  // start apart, so that the lanes' banks differ
                 for (int n = 0; n < per; ++n) {
-                    two_best(mine[lane * per + i], best, second);
-                    i = i + 1 == per ? 0 : i + 1;
+                    two_best(choice[lane * per + at], best, second);
+                    at = at + 1 == per ? 0 : at + 1;
                 }
-                if (groups_sum && second > -INFINITY) best += second;
+                best = group_score(best, second);
             }
             int before = 0;
             for (int g = 0; g < a.groups; ++g) {
@@ -256,54 +289,52 @@ gate_kernel(GateArgs a) {
             }
             const unsigned kept = __ballot_sync(kFull, lane < a.groups && before < a.topk_groups);
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
+            for (int j = 0; j < VPL; ++j) {
                 if (e0 + j < E && !(kept >> ((e0 + j) / per) & 1u)) key[j] = -INFINITY;
+                list[j] = key[j];
+            }
+            sort_descending(list);
         }
     }
 
-    float list[VPL];
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) list[j] = key[j];
-    sort_descending(list);
     float my_top = -INFINITY;
-    int my_lane = 0;
+    unsigned my_heads = 1u;  // lanes whose head was the pick: the lowest gave it
 #pragma unroll(KT > 0 ? KT : 1)
     for (int k = 0; k < K; ++k) {
         const float top = redux_max(list[0]);
-        const int win = __ffs(__ballot_sync(kFull, list[0] == top)) - 1;
+        const unsigned heads = __ballot_sync(kFull, list[0] == top);
         if (lane == k) {
             my_top = top;
-            my_lane = win;
+            my_heads = heads;
         }
-        if (lane == win) {
+        if (list[0] == top && (heads & lower) == 0u) {
 #pragma unroll
             for (int j = 0; j + 1 < VPL; ++j)
                 if (KT == 0 || j < KT - 1 - k) list[j] = list[j + 1];
             if (KT == 0 || VPL <= KT - 1 - k) list[VPL - 1] = -INFINITY;
         }
     }
-    // Lane k: pick k is the (same + 1)-th of its lane's experts with this key,
-    // where `same` picks right before it have the same key and lane.
+    // Pick k is the (same + 1)-th of its lane's experts with this key, where
+    // `same` picks right before it have the same key and lane.
+    const int my_lane = __ffs(my_heads) - 1;
+    const float up_top = __shfl_up_sync(kFull, my_top, 1);
+    const int up_lane = __shfl_up_sync(kFull, my_lane, 1);
+    const unsigned rest = ~__ballot_sync(kFull, lane > 0 && up_top == my_top && up_lane == my_lane);
+    int same = lane - (31 - __clz(rest & (0xffffffffu >> (31 - lane))));
     int my_id = -1;
-    {
-        const float up_top = __shfl_up_sync(kFull, my_top, 1);
-        const int up_lane = __shfl_up_sync(kFull, my_lane, 1);
-        const unsigned rest = ~__ballot_sync(kFull, lane > 0 && up_top == my_top && up_lane == my_lane);
-        int same = lane - (31 - __clz(rest & (0xffffffffu >> (31 - lane))));
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const float x = __shfl_sync(kFull, key[j], my_lane);
-            if (x == my_top && same-- == 0) my_id = my_lane * VPL + j;
-        }
-        if (lane >= K || !(my_top > -INFINITY)) my_id = -1;
+    for (int j = 0; j < VPL; ++j) {
+        const float x = __shfl_sync(kFull, key[j], my_lane);
+        if (x == my_top && same-- == 0) my_id = my_lane * VPL + j;
     }
+    if (lane >= K || !(my_top > -INFINITY)) my_id = -1;
 
     float l = -INFINITY, s = 0.0f;
     if (my_id >= 0) l = clamp_logit(load_one(row + my_id));
     if (a.renorm) {
-        s = pick_share(l, my_id >= 0, a.score);
+        s = pick_share<32>(l, my_id >= 0, a.score);
     } else if (my_id >= 0) {
-        s = a.score == kScoreSigmoid ? sigmoid(l) : __fdiv_rn(expf(l - m), total);
+        s = sigmoids ? sigmoid(l) : __fdiv_rn(expf(l - m), total);
     }
     if (lane < K) {
         int id = my_id;
@@ -316,21 +347,28 @@ gate_kernel(GateArgs a) {
     }
 }
 
+template <int VPL, typename T, int KT>
+cudaError_t launch_gate_k(const GateArgs& a, size_t smem, cudaStream_t s) {
+    return launch(gate_kernel<VPL, T, KT>, dim3((a.N + kGateWarps - 1) / kGateWarps), dim3(kGateWarps * 32), smem,
+                  s, a);
+}
+
 template <typename T>
 cudaError_t launch_gate_t(GateArgs a, cudaStream_t s) {
-    const dim3 grid((a.N + kGateWarps - 1) / kGateWarps), block(kGateWarps * 32);
     int vpl = 1;
     while (vpl * 32 < a.E) vpl *= 2;
     const int per = a.E / a.groups, lanes = per / vpl;
     a.lanes_per_group = per % vpl == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const size_t smem = a.groups > 1 && a.lanes_per_group == 0 ? sizeof(float) * kGateWarps * a.E : 0;
-    if (a.K == 8 && a.E > 128 && a.E <= 256) return launch(gate_kernel<8, T, 8>, grid, block, smem, s, a);
-    if (a.E <= 32) return launch(gate_kernel<1, T, 0>, grid, block, smem, s, a);
-    if (a.E <= 64) return launch(gate_kernel<2, T, 0>, grid, block, smem, s, a);
-    if (a.E <= 128) return launch(gate_kernel<4, T, 0>, grid, block, smem, s, a);
-    if (a.E <= 256) return launch(gate_kernel<8, T, 0>, grid, block, smem, s, a);
-    if (a.E <= 512) return launch(gate_kernel<16, T, 0>, grid, block, smem, s, a);
-    return launch(gate_kernel<32, T, 0>, grid, block, smem, s, a);
+    if (vpl == 8 && a.K == 8) return launch_gate_k<8, T, 8>(a, smem, s);
+    switch (vpl) {
+        case 1: return launch_gate_k<1, T, 0>(a, smem, s);
+        case 2: return launch_gate_k<2, T, 0>(a, smem, s);
+        case 4: return launch_gate_k<4, T, 0>(a, smem, s);
+        case 8: return launch_gate_k<8, T, 0>(a, smem, s);
+        case 16: return launch_gate_k<16, T, 0>(a, smem, s);
+        default: return launch_gate_k<32, T, 0>(a, smem, s);
+    }
 }
 
 // ---- gradient ---------------------------------------------------------------
@@ -356,20 +394,22 @@ __device__ __forceinline__ void store_four(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = q;
 }
 
-// One warp per token; the row's gradient is put together in shared memory
-// (zeros, then the picks) and stored once.
-template <typename T>
+// A warp takes TPW tokens, each with G = 32 / TPW lanes for its picks, so that
+// their loads are under way together; the rows' gradients are put together in
+// shared memory (zeros, then the picks) and stored once.
+template <typename T, int TPW>
 __global__ void __launch_bounds__(kGateWarps * 32)
 gate_backward_kernel(GateGradArgs a) {
     extern __shared__ float4 s_rows4[];
     float* s_rows = reinterpret_cast<float*>(s_rows4);
     pdl_prologue();
+    constexpr int G = 32 / TPW;
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int E = a.E, K = a.K;
     const int pitch = (E + 3) & ~3;
-    float* mine = s_rows + (size_t)warp * pitch;
-    int* inv = reinterpret_cast<int*>(s_rows + (size_t)kGateWarps * pitch);
+    float* mine = s_rows + (size_t)warp * TPW * pitch;
+    int* inv = reinterpret_cast<int*>(s_rows + (size_t)kGateWarps * TPW * pitch);
     if (a.emap != nullptr) {  // new id -> old id; the lowest old id where several map to one
         for (int e = threadIdx.x; e < E; e += kGateWarps * 32) inv[e] = E;
         __syncthreads();
@@ -379,35 +419,35 @@ gate_backward_kernel(GateGradArgs a) {
         }
         __syncthreads();
     }
-    const int t = blockIdx.x * kGateWarps + warp;
-    if (t >= a.N) return;  // warp-uniform
-    const T* row = static_cast<const T*>(a.logits) + (size_t)t * E;
-    T* out = static_cast<T*>(a.d_logits) + (size_t)t * E;
+    const int t0 = (blockIdx.x * kGateWarps + warp) * TPW;
+    if (t0 >= a.N) return;  // warp-uniform
+    const int i = lane / G, k = lane % G, t = t0 + i;
+    const T* row = static_cast<const T*>(a.logits) + (size_t)t0 * E;
+    T* out = static_cast<T*>(a.d_logits) + (size_t)t0 * E;
 
     int id = -1;
     float g = 0.0f, l = -INFINITY;
-    if (lane < K) {
-        id = __ldg(a.topk_idx + (size_t)t * K + lane);
+    if (k < K && t < a.N) {
+        id = __ldg(a.topk_idx + (size_t)t * K + k);
+        g = a.scale * __ldg(a.d_w + (size_t)t * K + k);
         if (id < 0 || id >= E) id = -1;
         if (id >= 0 && a.emap != nullptr) {
             id = inv[id];
             if (id >= E) id = -1;
         }
-        if (id >= 0) {
-            g = a.scale * __ldg(a.d_w + (size_t)t * K + lane);
-            l = load_one(row + id);
-            if (!available(l)) id = -1, g = 0.0f;
-        }
+        if (id >= 0) l = load_one(row + (size_t)i * E + id);
+        if (!available(l)) id = -1;
+        if (id < 0) g = 0.0f;
     }
-    for (int e = lane * 4; e < pitch; e += 128)
+    for (int e = lane * 4; e < TPW * pitch; e += 128)
         *reinterpret_cast<float4*>(mine + e) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
 
     l = clamp_logit(l);
     float d = 0.0f;
     if (a.renorm) {
-        const float q = pick_share(l, id >= 0, a.score);
-        d = (g - warp_sum(g * q)) * q;
+        const float q = pick_share<G>(l, id >= 0, a.score);
+        d = (g - lanes_sum<G>(g * q)) * q;
         if (a.score == kScoreSigmoid && id >= 0) d *= sigmoid(-l);  // 1 - s, without cancellation
     } else if (a.score == kScoreSigmoid) {
         const float e = expf(-fabsf(l));
@@ -415,40 +455,61 @@ gate_backward_kernel(GateGradArgs a) {
     } else {
         d = g;
     }
-    if (id >= 0) mine[id] = d;
+    if (id >= 0) mine[i * pitch + id] = d;
     __syncwarp();
 
+    const int tokens = min(TPW, a.N - t0);
     if (a.score == kScoreSoftmax && !a.renorm) {
-        float m = -INFINITY;
-        for (int e = lane; e < E; e += 32) {
-            const float x = load_one(row + e);
-            if (available(x)) m = fmaxf(m, clamp_logit(x));
-        }
-        m = warp_max(m);
-        float sum = 0.0f, dot = 0.0f;
-        for (int e = lane; e < E; e += 32) {
-            const float x = load_one(row + e);
-            const float p = available(x) ? expf(clamp_logit(x) - m) : 0.0f;
-            sum += p;
-            dot += p * mine[e];
-        }
-        sum = warp_sum(sum);
-        dot = warp_sum(dot);
-        const float inv_sum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-        dot *= inv_sum;
-        for (int e = lane; e < E; e += 32) {
-            const float x = load_one(row + e);
-            const float p = available(x) ? expf(clamp_logit(x) - m) * inv_sum : 0.0f;
-            mine[e] = p * (mine[e] - dot);
+        for (int n = 0; n < tokens; ++n) {
+            const T* x0 = row + (size_t)n * E;
+            float* p0 = mine + n * pitch;
+            float m = -INFINITY;
+            for (int e = lane; e < E; e += 32) {
+                const float x = load_one(x0 + e);
+                if (available(x)) m = fmaxf(m, clamp_logit(x));
+            }
+            m = redux_max(m);
+            float sum = 0.0f, dot = 0.0f;
+            for (int e = lane; e < E; e += 32) {
+                const float x = load_one(x0 + e);
+                const float p = available(x) ? expf(clamp_logit(x) - m) : 0.0f;
+                sum += p;
+                dot += p * p0[e];
+            }
+            sum = lanes_sum<32>(sum);
+            dot = lanes_sum<32>(dot);
+            const float inv_sum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+            dot *= inv_sum;
+            for (int e = lane; e < E; e += 32) {
+                const float x = load_one(x0 + e);
+                const float p = available(x) ? expf(clamp_logit(x) - m) * inv_sum : 0.0f;
+                p0[e] = p * (p0[e] - dot);
+            }
         }
         __syncwarp();
     }
-    if (a.vec) {
-        for (int e = lane * 4; e < E; e += 128)
+    if (a.vec) {  // then E == pitch: the rows follow one another in both places
+        for (int e = lane * 4; e < tokens * E; e += 128)
             store_four(out + e, *reinterpret_cast<const float4*>(mine + e));
     } else {
-        for (int e = lane; e < E; e += 32) store_one(out + e, mine[e]);
+        for (int n = 0; n < tokens; ++n)
+            for (int e = lane; e < E; e += 32) store_one(out + (size_t)n * E + e, mine[n * pitch + e]);
     }
+}
+
+template <typename T, int TPW>
+cudaError_t launch_backward_tpw(const GateGradArgs& a, cudaStream_t s) {
+    constexpr int per = kGateWarps * TPW;
+    const size_t smem = sizeof(float) * per * ((a.E + 3) & ~3) + (a.emap != nullptr ? sizeof(int) * a.E : 0);
+    return launch(gate_backward_kernel<T, TPW>, dim3((a.N + per - 1) / per), dim3(kGateWarps * 32), smem, s, a);
+}
+
+template <typename T>
+cudaError_t launch_backward_t(const GateGradArgs& a, cudaStream_t s) {
+    // four tokens a warp where their picks fit 8 lanes each, their rows 48 KB of
+    // shared memory a block, and there are tokens enough
+    if (a.K <= 8 && a.E <= 256 && a.N >= kGradManyTokens) return launch_backward_tpw<T, 4>(a, s);
+    return launch_backward_tpw<T, 1>(a, s);
 }
 
 }  // namespace
@@ -462,12 +523,7 @@ cudaError_t launch_gate(const GateArgs& a, cudaStream_t s) {
 
 cudaError_t launch_gate_backward(const GateGradArgs& a, cudaStream_t s) {
     if (a.N == 0) return cudaSuccess;
-    const dim3 grid((a.N + kGateWarps - 1) / kGateWarps), block(kGateWarps * 32);
-    const size_t smem = sizeof(float) * kGateWarps * ((a.E + 3) & ~3) +
-                        (a.emap != nullptr ? sizeof(int) * a.E : 0);
-    const cudaError_t err = a.bf16
-        ? launch(gate_backward_kernel<__nv_bfloat16>, grid, block, smem, s, a)
-        : launch(gate_backward_kernel<float>, grid, block, smem, s, a);
+    const cudaError_t err = a.bf16 ? launch_backward_t<__nv_bfloat16>(a, s) : launch_backward_t<float>(a, s);
     note_launch();
     return err;
 }

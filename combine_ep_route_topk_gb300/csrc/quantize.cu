@@ -5,10 +5,10 @@
 //   scale = max_c |v_c| / 127      (1 for a row of zeros)
 //   q_c   = round-to-nearest-even(v_c * (127 / max|v|))
 //
-// One pass over the row: a block holds its values in registers, reduces the
-// maximum and writes the codes, so the bytes moved are the row read and the
-// codes written (HBM-bound).  The values, the maximum and the scale are
-// float32; the code is the only rounding to fewer bits.
+// One pass over the row: a block (a warp for short rows) holds its values in
+// registers, reduces the maximum and writes the codes, so the bytes moved are
+// the row read and the codes written (HBM-bound).  The values, the maximum and
+// the scale are float32; the code is the only rounding to fewer bits.
 #include <cuda_bf16.h>
 
 #include "ep_kernels.cuh"
@@ -33,6 +33,9 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// SwiGLU's exponential and quotient by the hardware's exp2 and reciprocal: the
+// product with log2 e rounds at 2^-24 of |x| and each result at about 2^-23,
+// together far below the 1/254 of the row's maximum that a code rounds.
 template <typename T, bool SWIGLU>
 __device__ __forceinline__ void values8(const T* row, int cols, int c, float (&v)[8]) {
     load8(row + c, v);
@@ -40,37 +43,46 @@ __device__ __forceinline__ void values8(const T* row, int cols, int c, float (&v
         float u[8];
         load8(row + cols + c, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], 1.0f + expf(-v[j])) * u[j];
+        for (int j = 0; j < 8; ++j) {
+            float e, inv;
+            asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(v[j] * -1.4426950408889634f));
+            asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(1.0f + e));
+            v[j] = v[j] * inv * u[j];
+        }
     }
 }
 
-__device__ __forceinline__ uint32_t code(float v, float inv) {
-    const int q = __float2int_rn(v * inv);  // NaN -> 0
-    return (uint32_t)max(-127, min(127, q)) & 0xffu;
+// Four codes: with 1.5 * 2^23 added, a float32 of magnitude up to 127 is rounded
+// to the nearest integer (ties to even), which is its lowest byte.
+__device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
+    constexpr float kMagic = 12582912.0f;
+    const uint32_t a = __float_as_uint(fmaf(v[0], inv, kMagic)), b = __float_as_uint(fmaf(v[1], inv, kMagic));
+    const uint32_t c = __float_as_uint(fmaf(v[2], inv, kMagic)), d = __float_as_uint(fmaf(v[3], inv, kMagic));
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 __device__ __forceinline__ void store8(int8_t* p, const float (&v)[8], float inv) {
-    uint2 q;
-    q.x = code(v[0], inv) | code(v[1], inv) << 8 | code(v[2], inv) << 16 | code(v[3], inv) << 24;
-    q.y = code(v[4], inv) | code(v[5], inv) << 8 | code(v[6], inv) << 16 | code(v[7], inv) << 24;
-    *reinterpret_cast<uint2*>(p) = q;
+    *reinterpret_cast<uint2*>(p) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
 }
 
-// NT threads per row; HELD > 0: the row fits HELD vectors of 8 a thread, held
-// in registers; HELD == 0: any length, the values computed twice.
-template <typename T, bool SWIGLU, int NT, int HELD>
-__global__ void __launch_bounds__(NT) quantize_kernel(QuantArgs a) {
-    __shared__ float s_max[NT / 32];
+// Whether row r holds a token.
+__device__ __forceinline__ bool holds_token(const QuantArgs& a, long long r) {
+    if (a.expert_offsets == nullptr) return true;
+    if (a.layout == 0) return r < __ldg(a.expert_offsets + a.E);
+    const int e = (int)(r / a.cap), slot = (int)(r % a.cap);
+    return slot < __ldg(a.expert_offsets + e + 1) - __ldg(a.expert_offsets + e);
+}
+
+// NT threads per row and ROWS rows per block (ROWS > 1: a warp each); HELD > 0:
+// the row fits HELD vectors of 8 a thread, held in registers; HELD == 0: any
+// length, the values computed twice.
+template <typename T, bool SWIGLU, int NT, int ROWS, int HELD>
+__global__ void __launch_bounds__(NT * ROWS) quantize_kernel(QuantArgs a) {
+    static_assert(ROWS == 1 || NT == 32, "a warp per row");
     pdl_prologue();
-    const long long r = blockIdx.x;
-    if (a.expert_offsets != nullptr) {  // block-uniform: rows that hold no token
-        if (a.layout == 0) {
-            if (r >= __ldg(a.expert_offsets + a.E)) return;
-        } else {
-            const int e = (int)(r / a.cap), slot = (int)(r % a.cap);
-            if (slot >= __ldg(a.expert_offsets + e + 1) - __ldg(a.expert_offsets + e)) return;
-        }
-    }
+    const int tid = threadIdx.x % NT;
+    const long long r = (long long)blockIdx.x * ROWS + threadIdx.x / NT;
+    if (r >= a.rows || !holds_token(a, r)) return;  // uniform over the row's threads
     const int wide = SWIGLU ? 2 * a.cols : a.cols;
     const T* row = static_cast<const T*>(a.x) + r * wide;
     int8_t* out = a.q + r * a.cols;
@@ -80,7 +92,7 @@ __global__ void __launch_bounds__(NT) quantize_kernel(QuantArgs a) {
     if constexpr (HELD > 0) {
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            const int c = (i * NT + threadIdx.x) * 8;
+            const int c = (i * NT + tid) * 8;
             if (c < a.cols) {
                 values8<T, SWIGLU>(row, a.cols, c, v[i]);
             } else {
@@ -93,7 +105,7 @@ __global__ void __launch_bounds__(NT) quantize_kernel(QuantArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
     } else {
-        for (int c = threadIdx.x * 8; c < a.cols; c += NT * 8) {
+        for (int c = tid * 8; c < a.cols; c += NT * 8) {
             values8<T, SWIGLU>(row, a.cols, c, v[0]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[0][j]));
@@ -102,38 +114,51 @@ __global__ void __launch_bounds__(NT) quantize_kernel(QuantArgs a) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
-    __syncthreads();
+    if constexpr (NT > 32) {
+        __shared__ float s_max[NT / 32];
+        if ((tid & 31) == 0) s_max[tid >> 5] = top;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, s_max[w]);
+        for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, s_max[w]);
+    }
     const float inv = top > 0.0f ? __fdiv_rn(127.0f, top) : 1.0f;
-    if (threadIdx.x == 0) a.scales[r] = top > 0.0f ? __fdiv_rn(top, 127.0f) : 1.0f;
+    if (tid == 0) a.scales[r] = top > 0.0f ? __fdiv_rn(top, 127.0f) : 1.0f;
     if constexpr (HELD > 0) {
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            const int c = (i * NT + threadIdx.x) * 8;
+            const int c = (i * NT + tid) * 8;
             if (c < a.cols) store8(out + c, v[i], inv);
         }
     } else {
-        for (int c = threadIdx.x * 8; c < a.cols; c += NT * 8) {
+        for (int c = tid * 8; c < a.cols; c += NT * 8) {
             values8<T, SWIGLU>(row, a.cols, c, v[0]);
             store8(out + c, v[0], inv);
         }
     }
 }
 
+template <typename T, bool SWIGLU, int NT, int ROWS, int HELD>
+cudaError_t launch_shape(const QuantArgs& a, cudaStream_t s) {
+    return launch(quantize_kernel<T, SWIGLU, NT, ROWS, HELD>, dim3((unsigned)((a.rows + ROWS - 1ll) / ROWS)),
+                  dim3(NT * ROWS), 0, s, a);
+}
+
+// Measured on a GB300 (bf16, us; floor at the measured copy rate): 32768 x 7168
+// 108.7 (105); SwiGLU 32768 x 2048 58.2 (50), with 64 and 256 threads a row
+// 61.4 and 64.6; 65536 x 1024 28.0 (30) with a warp a row, 66.3 with 128
+// threads (a block a nanosecond is what the chip starts), but one token's 8 rows
+// 2.7 against 1.5.
 template <typename T, bool SWIGLU>
 cudaError_t launch_quantize_t(const QuantArgs& a, cudaStream_t s) {
-    const dim3 grid((unsigned)a.rows);
-    if (a.cols <= 1024)
-        return launch(quantize_kernel<T, SWIGLU, 128, 1>, grid, dim3(128), 0, s, a);
-    if (a.cols <= 2048)
-        return launch(quantize_kernel<T, SWIGLU, 128, 2>, grid, dim3(128), 0, s, a);
-    if (a.cols <= 4096)
-        return launch(quantize_kernel<T, SWIGLU, 256, 2>, grid, dim3(256), 0, s, a);
-    if (a.cols <= 8192)
-        return launch(quantize_kernel<T, SWIGLU, 256, 4>, grid, dim3(256), 0, s, a);
-    return launch(quantize_kernel<T, SWIGLU, 256, 0>, grid, dim3(256), 0, s, a);
+    if (a.cols <= 256) return launch_shape<T, SWIGLU, 32, 8, 1>(a, s);
+    if (a.cols <= 512) return launch_shape<T, SWIGLU, 32, 8, 2>(a, s);
+    if (a.cols <= 1024 && a.rows >= 4096) return launch_shape<T, SWIGLU, 32, 4, 4>(a, s);
+    if (a.cols <= 1024) return launch_shape<T, SWIGLU, 128, 1, 1>(a, s);
+    if (a.cols <= 2048) return launch_shape<T, SWIGLU, 128, 1, 2>(a, s);
+    if (a.cols <= 4096) return launch_shape<T, SWIGLU, 256, 1, 2>(a, s);
+    if (a.cols <= 8192) return launch_shape<T, SWIGLU, 256, 1, 4>(a, s);
+    if (a.cols <= 16384) return launch_shape<T, SWIGLU, 512, 1, 4>(a, s);
+    return launch_shape<T, SWIGLU, 512, 1, 0>(a, s);
 }
 
 }  // namespace
