@@ -12,18 +12,26 @@
 // A tile is 128 channels a CTA (the M side: weights) x up to TN rows (the N
 // side).  CG = 1: one CTA.  CG = 2: a pair of CTAs on 256 channels, each
 // holding half of the rows' operand.
-//   TMA warp        the list of tiles; weights, [128 channels x 128 bytes] boxes, 128-byte swizzle
+//   TMA warp        the list of tiles; weights, [128 channels x 128 bytes] boxes,
+//                   128-byte swizzle
 //   2 copying warps x rows, wherever they lie, by 16-byte background copies
 //   8 weight warps  8-bit stages -> float16 -> TMEM (the A operand's stages)
 //   row warps       8-bit stages -> float16 -> shared memory (B)
-//   MMA warp        one thread issues 8 MMAs of K = 16 per stage
+//   MMA warp        one elected thread issues 8 MMAs of K = 16 per stage
 //   8 output warps  TMEM -> scales -> bf16 / float32 -> rows of out
 // Within a block of 128 K, both operands hold the first 8 K of each 16 in one
 // half of a stage and the second 8 in the other (a sum's order is free): a row's
 // 8 lanes then store to 8 different banks' groups without exchanging halves.
 // The weights go through TMEM so that their float16 form costs no shared
 // memory bandwidth.  Every wait has a time limit: on expiry the CTA stops,
-// writes status 1, waits for its own copies and frees its TMEM.
+// writes status 1, waits for its own copies and MMAs and frees its TMEM.
+//
+// What bounds it: with few rows per expert the weights' bytes (32 experts of
+// 4096 x 7168, 8 rows each: 149 us = 6.3 TB/s of the 6.7 that a copy reaches),
+// with many the tensor cores (1024 rows each: 1.00 ms = 1.92 PFLOP/s, where a
+// large library product of bf16 reaches 1.95; 1.76 M cycles, of which the MMAs
+// take 1.55 M).  In between, and with short rows of x, the ring: a stage is
+// widened (about 700 cycles after it is free), multiplied and handed back.
 #include <cuda.h>
 
 #include <atomic>
@@ -42,7 +50,6 @@ constexpr int kTmaWarp = kWeightWarp0 + kWeightWarps, kMmaWarp = kTmaWarp + 1;
 constexpr int kCopyWarp0 = kMmaWarp + 1, kCopyWarps = 2;
 constexpr int kRowWarp0 = kCopyWarp0 + kCopyWarps;  // two row warps for every 32 rows of a stage
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemA = 256;      // A stages start here: 64 columns each
 constexpr uint32_t kWaitHint = 2000;  // ns that one poll of a barrier may sleep
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
 
@@ -53,18 +60,21 @@ struct Shape {
     static constexpr int kRows = TN / CG;
     static constexpr int kBAtom = kRows * 128;       // 64 K of the rows, float16
     static constexpr int kBBytes = 2 * kBAtom;       // one stage
-    static constexpr int kStages = kRows <= 64 ? 4 : 3;   // converted operands
     static constexpr int kXBytes = kRows * kBK;      // one stage of 8-bit rows
-    static constexpr int kWStages = kRows <= 64 ? 6 : 4;  // 8-bit weights in flight
-    static constexpr int kXStages = kRows <= 64 ? 4 : 2;  // 8-bit rows in flight
-    static constexpr int kRowWarps = kRows / 16;
+    static constexpr int kStages = kRows <= 64 ? 4 : 3;   // converted operands
+    static constexpr int kWStages = kRows <= 80 ? 6 : 4;  // 8-bit weights in flight
+    static constexpr int kXStages = kRows <= 80 ? 4 : 2;  // 8-bit rows in flight
+    static constexpr int kRowWarps = 2 * ((kRows + 31) / 32);
     static constexpr int kThreads = (kRowWarp0 + kRowWarps) * 32;
-    static constexpr int kAcc = TN <= 128 ? 2 : 1;   // accumulators of TN columns
+    // accumulators of TN columns, then the weights' stages of 64
+    static constexpr int kAcc = 2 * TN + kStages * 64 <= (int)kTmemCols ? 2 : 1;
+    static constexpr uint32_t kTmemA = kAcc * TN;
     static constexpr int kChannels = 128 * CG;
     static constexpr int kGrain = 16 * CG;           // an MMA's N is a multiple
+    static_assert(kBAtom % 1024 == 0 && kTmemA + kStages * 64 <= kTmemCols, "swizzle, TMEM");
 };
 
-constexpr int kMaxStages = 4, kMaxWStages = 8, kMaxXStages = 4;
+constexpr int kMaxStages = 4, kMaxWStages = 6, kMaxXStages = 4;
 // Units published ahead.  The TMA warp publishes one when it has issued all
 // copies of those before, which its stages keep within 8 + 2 + 4 blocks of the
 // MMAs and the accumulators within 2 units more of the output warps: a slot is
@@ -481,7 +491,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
                     ok = mbar_wait_warp(sh, &sh->full[s], c / kStages & 1);
                     if (!ok) break;
                     tmem_fence_after();
-                    const uint32_t at = tmem + kTmemA + s * 64;
+                    const uint32_t at = tmem + S::kTmemA + s * 64;
                     const uint64_t desc = desc0 + (uint64_t)(s * (kBBytes >> 4));
                     // 16-byte pieces of the block's rows: each gives 8 K to either atom
                     const int pieces = min(8, (a.Kd - kb * kBK) / 16);
@@ -603,7 +613,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         const int quarter = warp & 3, group = (warp - kWeightWarp0) >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t from = smem_u32(s_w) + row * 128 + ((row & 7) << 4);
-        const uint32_t to = tmem + ((uint32_t)quarter << 21) + kTmemA;
+        const uint32_t to = tmem + ((uint32_t)quarter << 21) + S::kTmemA;
         const uint32_t total = units * kblocks;
         bool ok = true;
         for (uint32_t c = group; ok && c < total; c += 2) {
@@ -839,9 +849,18 @@ cudaError_t launch_tc(const MatmulArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// By the rows per expert to expect (the capacity, where a masked layout holds
+// more).  A tile that holds an expert's rows whole reads and widens its weights
+// once; narrow tiles leave shared memory for more weights in flight and TMEM for
+// a second accumulator, wide ones use the tensor cores better.  Measured on a
+// GB300 (us; 32 experts of 4096 x 7168 unless noted) with TN = 64, 160, 256:
+//   8 rows 149, 154           32 rows 159, 158, 205     64 rows 170, 166, 214
+//   128 rows 311, 186, 231    160 rows 441, 200, 241    256 rows 594, 338, 284
+//   128 experts of 2880 x 1440: 16 rows 101, 113; 48 rows 112, 122; counts drawn
+//   around 128: 250, 148, 167.  Counts scatter, so 160 serves means up to 140.
 cudaError_t launch_matmul_tc(const MatmulArgs& a, int per, cudaStream_t s) {
     if (per <= 48) return launch_tc<Shape<1, 64>>(a, s);
-    if (per <= 128) return launch_tc<Shape<2, 128>>(a, s);
+    if (per <= 140) return launch_tc<Shape<2, 160>>(a, s);
     return launch_tc<Shape<2, 256>>(a, s);
 }
 
