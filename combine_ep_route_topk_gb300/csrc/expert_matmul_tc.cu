@@ -70,7 +70,7 @@ struct Shape {
     static constexpr int kAcc = 2 * TN + kStages * 64 <= (int)kTmemCols ? 2 : 1;
     static constexpr uint32_t kTmemA = kAcc * TN;
     static constexpr int kChannels = 128 * CG;
-    static constexpr int kGrain = 16 * CG;           // an MMA's N is a multiple
+    static constexpr int kGrain = 16;                // an MMA's N is a multiple
     static_assert(kBAtom % 1024 == 0 && kTmemA + kStages * 64 <= kTmemCols, "swizzle, TMEM");
 };
 
@@ -536,7 +536,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             Unit t;
             ok = get_unit<S>(sh, u, t);
             if (!ok) break;
-            const int half = t.n / CG;  // this CTA's rows of the tile, a multiple of 16
+            const int half = t.n / CG;  // this CTA's rows of the tile, a multiple of 8
             const int8_t* src[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
@@ -578,7 +578,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             Unit t;
             ok = get_unit<S>(sh, u, t);
             if (!ok) break;
-            const int mine = t.n / CG - r0;  // rows of this warp, if any: 16, or all 32
+            const int mine = t.n / CG - r0;  // rows of this warp, if any, in eights
             c1 += kblocks;
             for (; c < c1; c += 2) {
                 const uint32_t sx = c % kXStages, s = c % kStages;
@@ -587,7 +587,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
                 uint4 q[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (mine > j / 4 * 16) q[j] = load_shared(from + sx * S::kXBytes + j * 4 * kBK);
+                    if (mine > j / 2 * 8) q[j] = load_shared(from + sx * S::kXBytes + j * 4 * kBK);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->x_empty[sx]);
                 ok = mbar_wait_warp(sh, &sh->empty[s], (c / kStages & 1) ^ 1);
@@ -595,7 +595,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
                 const uint32_t to = at + s * kBBytes;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (mine > j / 4 * 16) widen_row<kBAtom>((to ^ (j & 1) * 64) + j * 4 * 128, q[j]);
+                    if (mine > j / 2 * 8) widen_row<kBAtom>((to ^ (j & 1) * 64) + j * 4 * 128, q[j]);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive_leader<CG>(&sh->full[s]);
