@@ -394,122 +394,151 @@ __device__ __forceinline__ void store_four(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = q;
 }
 
-// A warp takes TPW tokens, each with G = 32 / TPW lanes for its picks, so that
-// their loads are under way together; the rows' gradients are put together in
-// shared memory (zeros, then the picks) and stored once.
+// Old ids of the mapped ones: inv[new] = the lowest expert that maps there, E for
+// none.  Every thread of the block calls it.
+__device__ __forceinline__ void invert_map(const int32_t* emap, int E, int* inv) {
+    for (int e = threadIdx.x; e < E; e += kGateWarps * 32) inv[e] = E;
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kGateWarps * 32) {
+        const int to = __ldg(emap + e);
+        if (to >= 0 && to < E) atomicMin(inv + to, e);
+    }
+    __syncthreads();
+}
+
+// Pick k of token t: its expert (-1: none, or not available), its logit and
+// scale * gradient of its weight (0 without an expert).
+template <typename T>
+__device__ __forceinline__ int load_pick(const GateGradArgs& a, int t, int k, const int* inv, float& l, float& g) {
+    int id = __ldg(a.topk_idx + (size_t)t * a.K + k);
+    g = a.scale * __ldg(a.d_w + (size_t)t * a.K + k);
+    if (id < 0 || id >= a.E) id = -1;
+    if (id >= 0 && a.emap != nullptr) {
+        id = inv[id];
+        if (id >= a.E) id = -1;
+    }
+    l = -INFINITY;
+    if (id >= 0) l = load_one(static_cast<const T*>(a.logits) + (size_t)t * a.E + id);
+    if (!available(l)) id = -1;
+    if (id < 0) g = 0.0f;
+    l = clamp_logit(l);
+    return id;
+}
+
+// Gradients that only the picks get.  A warp takes TPW tokens, each with G = 32 /
+// TPW lanes for its picks.  The rows' zeros are stored first, while the picks
+// load; the picks' values follow (the barrier orders the two stores).
+// 32768 tokens of 256 experts write 33.5 MB.
 template <typename T, int TPW>
 __global__ void __launch_bounds__(kGateWarps * 32)
 gate_backward_kernel(GateGradArgs a) {
-    extern __shared__ float4 s_rows4[];
-    float* s_rows = reinterpret_cast<float*>(s_rows4);
+    extern __shared__ int s_inv[];
     pdl_prologue();
     constexpr int G = 32 / TPW;
+    if (a.emap != nullptr) invert_map(a.emap, a.E, s_inv);
     const int lane = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5;
-    const int E = a.E, K = a.K;
-    const int pitch = (E + 3) & ~3;
-    float* mine = s_rows + (size_t)warp * TPW * pitch;
-    int* inv = reinterpret_cast<int*>(s_rows + (size_t)kGateWarps * TPW * pitch);
-    if (a.emap != nullptr) {  // new id -> old id; the lowest old id where several map to one
-        for (int e = threadIdx.x; e < E; e += kGateWarps * 32) inv[e] = E;
-        __syncthreads();
-        for (int e = threadIdx.x; e < E; e += kGateWarps * 32) {
-            const int to = __ldg(a.emap + e);
-            if (to >= 0 && to < E) atomicMin(inv + to, e);
-        }
-        __syncthreads();
-    }
-    const int t0 = (blockIdx.x * kGateWarps + warp) * TPW;
+    const int t0 = (blockIdx.x * kGateWarps + (threadIdx.x >> 5)) * TPW;
     if (t0 >= a.N) return;  // warp-uniform
-    const int i = lane / G, k = lane % G, t = t0 + i;
-    const T* row = static_cast<const T*>(a.logits) + (size_t)t0 * E;
-    T* out = static_cast<T*>(a.d_logits) + (size_t)t0 * E;
-
-    int id = -1;
-    float g = 0.0f, l = -INFINITY;
-    if (k < K && t < a.N) {
-        id = __ldg(a.topk_idx + (size_t)t * K + k);
-        g = a.scale * __ldg(a.d_w + (size_t)t * K + k);
-        if (id < 0 || id >= E) id = -1;
-        if (id >= 0 && a.emap != nullptr) {
-            id = inv[id];
-            if (id >= E) id = -1;
-        }
-        if (id >= 0) l = load_one(row + (size_t)i * E + id);
-        if (!available(l)) id = -1;
-        if (id < 0) g = 0.0f;
+    T* out = static_cast<T*>(a.d_logits) + (size_t)t0 * a.E;
+    const int n = min(TPW, a.N - t0) * a.E;
+    if (a.vec) {
+        for (int e = lane * 4; e < n; e += 128) store_four(out + e, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    } else {
+        for (int e = lane; e < n; e += 32) store_one(out + e, 0.0f);
     }
-    for (int e = lane * 4; e < TPW * pitch; e += 128)
-        *reinterpret_cast<float4*>(mine + e) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    __syncwarp();
-
-    l = clamp_logit(l);
-    float d = 0.0f;
+    const int i = lane / G, k = lane % G, t = t0 + i;
+    int id = -1;
+    float g = 0.0f, l = -INFINITY, d = 0.0f;
+    if (k < a.K && t < a.N) id = load_pick<T>(a, t, k, s_inv, l, g);
     if (a.renorm) {
         const float q = pick_share<G>(l, id >= 0, a.score);
         d = (g - lanes_sum<G>(g * q)) * q;
         if (a.score == kScoreSigmoid && id >= 0) d *= sigmoid(-l);  // 1 - s, without cancellation
-    } else if (a.score == kScoreSigmoid) {
+    } else {
         const float e = expf(-fabsf(l));
         if (id >= 0) d = g * __fdiv_rn(e, (1.0f + e) * (1.0f + e));  // s (1 - s), likewise
-    } else {
-        d = g;
     }
-    if (id >= 0) mine[i * pitch + id] = d;
     __syncwarp();
+    if (id >= 0) store_one(out + (size_t)i * a.E + id, d);
+}
 
-    const int tokens = min(TPW, a.N - t0);
-    if (a.score == kScoreSoftmax && !a.renorm) {
-        for (int n = 0; n < tokens; ++n) {
-            const T* x0 = row + (size_t)n * E;
-            float* p0 = mine + n * pitch;
-            float m = -INFINITY;
-            for (int e = lane; e < E; e += 32) {
-                const float x = load_one(x0 + e);
-                if (available(x)) m = fmaxf(m, clamp_logit(x));
-            }
-            m = redux_max(m);
-            float sum = 0.0f, dot = 0.0f;
-            for (int e = lane; e < E; e += 32) {
-                const float x = load_one(x0 + e);
-                const float p = available(x) ? expf(clamp_logit(x) - m) : 0.0f;
-                sum += p;
-                dot += p * p0[e];
-            }
-            sum = lanes_sum<32>(sum);
-            dot = lanes_sum<32>(dot);
-            const float inv_sum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-            dot *= inv_sum;
-            for (int e = lane; e < E; e += 32) {
-                const float x = load_one(x0 + e);
-                const float p = available(x) ? expf(clamp_logit(x) - m) * inv_sum : 0.0f;
-                p0[e] = p * (p0[e] - dot);
-            }
+// The softmax without renormalisation: every expert's logit gets a gradient.  One
+// warp per token, the row in registers: -s_e sum_j c g_j s_j everywhere, then the
+// picks' values over it.
+template <int VPL, typename T>
+__global__ void __launch_bounds__(kGateWarps * 32)
+gate_backward_dense_kernel(GateGradArgs a) {
+    extern __shared__ int s_inv[];
+    pdl_prologue();
+    if (a.emap != nullptr) invert_map(a.emap, a.E, s_inv);
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * kGateWarps + (threadIdx.x >> 5);
+    if (t >= a.N) return;  // warp-uniform
+    const int E = a.E, e0 = lane * VPL;
+    T* out = static_cast<T*>(a.d_logits) + (size_t)t * E;
+    float v[VPL];
+    load_row<VPL>(static_cast<const T*>(a.logits) + (size_t)t * E, E, a.vec != 0, lane, v);
+    int id = -1;
+    float g = 0.0f, l = -INFINITY;
+    if (lane < a.K) id = load_pick<T>(a, t, lane, s_inv, l, g);
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+        if (available(v[j])) m = fmaxf(m, clamp_logit(v[j]));
+    m = redux_max(m);
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        v[j] = available(v[j]) ? expf(clamp_logit(v[j]) - m) : 0.0f;
+        sum += v[j];
+    }
+    sum = lanes_sum<32>(sum);
+    const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+    const float s = id >= 0 ? expf(l - m) * inv : 0.0f;
+    const float dot = lanes_sum<32>(g * s);
+    const float f = -dot * inv;
+    if (VPL >= 4 && a.vec) {
+        if constexpr (VPL >= 4) {
+#pragma unroll
+            for (int j = 0; j < VPL; j += 4)
+                if (e0 + j < E)
+                    store_four(out + e0 + j, make_float4(v[j] * f, v[j + 1] * f, v[j + 2] * f, v[j + 3] * f));
         }
-        __syncwarp();
-    }
-    if (a.vec) {  // then E == pitch: the rows follow one another in both places
-        for (int e = lane * 4; e < tokens * E; e += 128)
-            store_four(out + e, *reinterpret_cast<const float4*>(mine + e));
     } else {
-        for (int n = 0; n < tokens; ++n)
-            for (int e = lane; e < E; e += 32) store_one(out + (size_t)n * E + e, mine[n * pitch + e]);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j < E) store_one(out + e0 + j, v[j] * f);
     }
+    __syncwarp();
+    if (id >= 0) store_one(out + id, s * (g - dot));
+}
+
+template <int VPL, typename T>
+cudaError_t launch_dense(const GateGradArgs& a, size_t smem, cudaStream_t s) {
+    return launch(gate_backward_dense_kernel<VPL, T>, dim3((a.N + kGateWarps - 1) / kGateWarps),
+                  dim3(kGateWarps * 32), smem, s, a);
 }
 
 template <typename T, int TPW>
-cudaError_t launch_backward_tpw(const GateGradArgs& a, cudaStream_t s) {
+cudaError_t launch_sparse(const GateGradArgs& a, size_t smem, cudaStream_t s) {
     constexpr int per = kGateWarps * TPW;
-    const size_t smem = sizeof(float) * per * ((a.E + 3) & ~3) + (a.emap != nullptr ? sizeof(int) * a.E : 0);
     return launch(gate_backward_kernel<T, TPW>, dim3((a.N + per - 1) / per), dim3(kGateWarps * 32), smem, s, a);
 }
 
 template <typename T>
 cudaError_t launch_backward_t(const GateGradArgs& a, cudaStream_t s) {
-    // four tokens a warp where their picks fit 8 lanes each, their rows 48 KB of
-    // shared memory a block, and there are tokens enough
-    if (a.K <= 8 && a.E <= 256 && a.N >= kGradManyTokens) return launch_backward_tpw<T, 4>(a, s);
-    return launch_backward_tpw<T, 1>(a, s);
+    const size_t smem = a.emap != nullptr ? sizeof(int) * a.E : 0;
+    if (a.score == kScoreSoftmax && !a.renorm) {
+        if (a.E <= 32) return launch_dense<1, T>(a, smem, s);
+        if (a.E <= 64) return launch_dense<2, T>(a, smem, s);
+        if (a.E <= 128) return launch_dense<4, T>(a, smem, s);
+        if (a.E <= 256) return launch_dense<8, T>(a, smem, s);
+        if (a.E <= 512) return launch_dense<16, T>(a, smem, s);
+        return launch_dense<32, T>(a, smem, s);
+    }
+    // four tokens a warp where their picks fit 8 lanes each and there are tokens enough
+    if (a.K <= 8 && a.N >= kGradManyTokens) return launch_sparse<T, 4>(a, smem, s);
+    return launch_sparse<T, 1>(a, smem, s);
 }
 
 }  // namespace
