@@ -39,7 +39,6 @@ __device__ __forceinline__ bool available(float v) { return v > -INFINITY; }
 // that no score is inf / inf.
 __device__ __forceinline__ float clamp_logit(float v) { return fminf(v, FLT_MAX); }
 
-__device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
 
 __device__ __forceinline__ float load_one(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_one(const __nv_bfloat16* p) {
@@ -56,6 +55,22 @@ __device__ __forceinline__ void load_four(const __nv_bfloat16* p, float* v) {
     v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
 }
 
+// The hardware's exp2 and reciprocal.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Accurate to the last places, unlike the scores of the choice.
+__device__ __forceinline__ float sigmoid(float l) { return rcp_fast(1.0f + expf(-l)); }
+
 // Sum and maximum over aligned groups of G lanes.
 template <int G>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -71,23 +86,25 @@ __device__ __forceinline__ float lanes_max(float v) {
 }
 
 // The share s_k / sum_j s_j of the lane's pick (logit l) among the picks of its
-// token, which G lanes hold; 0 on lanes without one.  The scores are taken relative to the largest
-// pick's, exp(l - c) with c = max l for the softmax and min(0, max l) for the
-// sigmoid, so that no sum underflows however far below the others' the picks'
-// scores lie.
+// token, which G lanes hold; 0 on lanes without one.  The scores are taken
+// relative to the largest pick's, exp(l - c) with c = max l for the softmax and
+// min(0, max l) for the sigmoid, so that no sum underflows however far below the
+// others' the picks' scores lie.  Quotients by the hardware's reciprocal (1 ulp).
 template <int G>
 __device__ __forceinline__ float pick_share(float l, bool picked, int score) {
     float c = lanes_max<G>(picked ? l : -INFINITY);
     float s = 0.0f;
     if (score == kScoreSigmoid) {
-        c = fminf(c, 0.0f);
-        // l <= 0: exp(l) / (1 + exp(l)); l > 0 (then c = 0): 1 / (1 + exp(-l))
-        if (picked) s = l > 0.0f ? sigmoid(l) : __fdiv_rn(expf(l - c), 1.0f + expf(l));
+        // l > 0 (then c = 0): 1 / (1 + exp(-l)); else exp(l - c) / (1 + exp(l))
+        const float e = expf(-fabsf(l));
+        float num = l > 0.0f ? 1.0f : e;
+        if (c < 0.0f) num = expf(l - c);
+        if (picked) s = num * rcp_fast(1.0f + e);
     } else if (picked) {
         s = expf(l - c);
     }
     const float sum = lanes_sum<G>(s);  // at least 1/2 where anything is picked
-    return picked ? __fdiv_rn(s, sum) : 0.0f;
+    return picked ? s * rcp_fast(sum) : 0.0f;
 }
 
 // The lane's VPL logits (NaN past E), four at a time where rows allow it.
@@ -134,19 +151,6 @@ __device__ __forceinline__ float redux_max(float v) {
     float m;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
     return m;
-}
-
-// Scores for the choice, by the hardware's exp2 and reciprocal.
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-    float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 __device__ __forceinline__ void two_best(float x, float& a, float& b) {
@@ -221,15 +225,21 @@ gate_kernel(GateArgs a) {
     // keys (-inf: not available)
     const float inv_total = rcp_fast(total);
     float key[VPL];
+    if (a.bias == nullptr) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-        float x;
-        if (a.bias != nullptr)  // a sigmoid of +inf is 1 without a clamp
-            x = (sigmoids ? rcp_fast(1.0f + exp2_fast(v[j] * -kLog2e))
-                          : exp2_fast((clamp_logit(v[j]) - m) * kLog2e) * inv_total) + bias[j];
-        else
-            x = clamp_logit(v[j]);
-        key[j] = available(v[j]) ? x : -INFINITY;
+        for (int j = 0; j < VPL; ++j) key[j] = available(v[j]) ? clamp_logit(v[j]) : -INFINITY;
+    } else if (sigmoids) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {  // a sigmoid of +inf is 1 without a clamp
+            const float x = rcp_fast(1.0f + exp2_fast(v[j] * -kLog2e)) + bias[j];
+            key[j] = available(v[j]) ? x : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const float x = exp2_fast((clamp_logit(v[j]) - m) * kLog2e) * inv_total + bias[j];
+            key[j] = available(v[j]) ? x : -INFINITY;
+        }
     }
     float list[VPL];
 #pragma unroll
@@ -334,7 +344,7 @@ gate_kernel(GateArgs a) {
     if (a.renorm) {
         s = pick_share<32>(l, my_id >= 0, a.score);
     } else if (my_id >= 0) {
-        s = sigmoids ? sigmoid(l) : __fdiv_rn(expf(l - m), total);
+        s = sigmoids ? sigmoid(l) : expf(l - m) * inv_total;
     }
     if (lane < K) {
         int id = my_id;

@@ -45,8 +45,8 @@ __device__ __forceinline__ void values8(const T* row, int cols, int c, float (&v
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float e, inv;
-            asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(v[j] * -1.4426950408889634f));
-            asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(1.0f + e));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v[j] * -1.4426950408889634f));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(1.0f + e));
             v[j] = v[j] * inv * u[j];
         }
     }
