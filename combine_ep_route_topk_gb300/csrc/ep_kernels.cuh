@@ -182,7 +182,8 @@ struct GateArgs {
     int bf16;
     int vec;                    // rows start on a boundary of 4 elements
     int bias_vec;               // so does the bias
-    int lanes_per_group;        // set by the launcher: lanes that hold a group, 0 if they share
+    int lanes_per_group;        // set by the launcher: lanes that hold a group, 0 if groups share lanes
+    int share_lanes;            // then: lanes that score a group (a power of two)
 };
 cudaError_t launch_gate(const GateArgs& a, cudaStream_t s);
 

@@ -107,6 +107,14 @@ __device__ __forceinline__ float pick_share(float l, bool picked, int score) {
     return picked ? s * rcp_fast(sum) : 0.0f;
 }
 
+// The two best of this lane's and the other lane's.
+__device__ __forceinline__ void merge_two(float& best, float& second, int off) {
+    const float o1 = __shfl_xor_sync(kFull, best, off);
+    const float o2 = __shfl_xor_sync(kFull, second, off);
+    second = fmaxf(fminf(best, o1), fmaxf(second, o2));
+    best = fmaxf(best, o1);
+}
+
 // The lane's VPL logits (NaN past E), four at a time where rows allow it.
 template <int VPL, typename T>
 __device__ __forceinline__ void load_row(const T* row, int E, bool vec, int lane, float (&v)[VPL]) {
@@ -164,12 +172,7 @@ __device__ __forceinline__ void two_best(float x, float& a, float& b) {
 template <int L, typename F>
 __device__ __forceinline__ int groups_before(float best, float second, int lane, F group_score) {
 #pragma unroll
-    for (int off = 1; off < L; off <<= 1) {
-        const float o1 = __shfl_xor_sync(kFull, best, off);
-        const float o2 = __shfl_xor_sync(kFull, second, off);
-        second = fmaxf(fminf(best, o1), fmaxf(second, o2));
-        best = fmaxf(best, o1);
-    }
+    for (int off = 1; off < L; off <<= 1) merge_two(best, second, off);
     const float score = group_score(best, second);
     int before = 0;
 #pragma unroll
@@ -241,69 +244,69 @@ gate_kernel(GateArgs a) {
             key[j] = available(v[j]) ? x : -INFINITY;
         }
     }
+    // a group's score from its two largest keys
+    const auto group_score = [&](float best, float second) {
+        if (!groups_sum) return best;
+        if (a.bias == nullptr) {  // the keys are logits
+            best = !available(best) ? best
+                   : sigmoids ? rcp_fast(1.0f + exp2_fast(best * -kLog2e))
+                              : exp2_fast((best - m) * kLog2e) * inv_total;
+            second = !available(second) ? second
+                     : sigmoids ? rcp_fast(1.0f + exp2_fast(second * -kLog2e))
+                                : exp2_fast((second - m) * kLog2e) * inv_total;
+        }
+        return available(second) ? best + second : best;
+    };
+    if (a.groups > 1 && a.lanes_per_group == 0) {
+        // groups that share lanes: their keys through shared memory, L lanes a group
+        const int per = E / a.groups, L = a.share_lanes;
+        float* choice = s_choice + (size_t)warp * E;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j < E) choice[e0 + j] = key[j];
+        __syncwarp();
+        float best = -INFINITY, second = -INFINITY;
+        const int g = lane / L;
+        if (g < a.groups)
+            for (int n = lane % L; n < per; n += L) two_best(choice[g * per + n], best, second);
+        for (int off = 1; off < L; off <<= 1) merge_two(best, second, off);
+        best = g < a.groups ? group_score(best, second) : -INFINITY;
+        int before = 0;
+        for (int o = 0; o < a.groups; ++o) {
+            const float other = __shfl_sync(kFull, best, o * L);
+            before += o < g ? other >= best : other > best;
+        }
+        const unsigned kept = __ballot_sync(kFull, g < a.groups && before < a.topk_groups);
+        int group = e0 / per, next = (group + 1) * per - e0;  // the first of the lane's that is in the next group
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            while (j >= next) {
+                ++group;
+                next += per;
+            }
+            if (e0 + j < E && !(kept >> (group * L) & 1u)) key[j] = -INFINITY;
+        }
+    }
+
     float list[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) list[j] = key[j];
     sort_descending(list);
 
-    if (a.groups > 1) {
-        const int per = E / a.groups;
-        // a group's score from its two largest keys
-        const auto group_score = [&](float best, float second) {
-            if (!groups_sum) return best;
-            if (a.bias == nullptr) {  // the keys are logits
-                best = !available(best) ? best
-                       : sigmoids ? rcp_fast(1.0f + exp2_fast(best * -kLog2e))
-                                  : exp2_fast((best - m) * kLog2e) * inv_total;
-                second = !available(second) ? second
-                         : sigmoids ? rcp_fast(1.0f + exp2_fast(second * -kLog2e))
-                                    : exp2_fast((second - m) * kLog2e) * inv_total;
-            }
-            return available(second) ? best + second : best;
-        };
-        if (a.lanes_per_group > 0) {
-            // whole lanes of one group next to each other, a power of two of them
-            const float second = VPL > 1 ? list[VPL > 1 ? 1 : 0] : -INFINITY;
-            int before = 0;
-            switch (a.lanes_per_group) {
-                case 1: before = groups_before<1>(list[0], second, lane, group_score); break;
-                case 2: before = groups_before<2>(list[0], second, lane, group_score); break;
-                case 4: before = groups_before<4>(list[0], second, lane, group_score); break;
-                case 8: before = groups_before<8>(list[0], second, lane, group_score); break;
-                default: before = groups_before<16>(list[0], second, lane, group_score); break;
-            }
-            if (before >= a.topk_groups) {
+    if (a.groups > 1 && a.lanes_per_group > 0) {
+        // whole lanes of one group next to each other, a power of two of them
+        const float second = VPL > 1 ? list[VPL > 1 ? 1 : 0] : -INFINITY;
+        int before = 0;
+        switch (a.lanes_per_group) {
+            case 1: before = groups_before<1>(list[0], second, lane, group_score); break;
+            case 2: before = groups_before<2>(list[0], second, lane, group_score); break;
+            case 4: before = groups_before<4>(list[0], second, lane, group_score); break;
+            case 8: before = groups_before<8>(list[0], second, lane, group_score); break;
+            default: before = groups_before<16>(list[0], second, lane, group_score); break;
+        }
+        if (before >= a.topk_groups) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) list[j] = -INFINITY;
-            }
-        } else {
-            float* choice = s_choice + (size_t)warp * E;
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (e0 + j < E) choice[e0 + j] = key[j];
-            __syncwarp();
-            float best = -INFINITY, second = -INFINITY;
-            if (lane < a.groups) {
-                int at = lane % per;  // start apart, so that the lanes' banks differ
-                for (int n = 0; n < per; ++n) {
-                    two_best(choice[lane * per + at], best, second);
-                    at = at + 1 == per ? 0 : at + 1;
-                }
-                best = group_score(best, second);
-            }
-            int before = 0;
-            for (int g = 0; g < a.groups; ++g) {
-                const float o = __shfl_sync(kFull, best, g);
-                before += (o > best || (o == best && g < lane)) ? 1 : 0;
-            }
-            const unsigned kept = __ballot_sync(kFull, lane < a.groups && before < a.topk_groups);
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                if (e0 + j < E && !(kept >> ((e0 + j) / per) & 1u)) key[j] = -INFINITY;
-                list[j] = key[j];
-            }
-            sort_descending(list);
+            for (int j = 0; j < VPL; ++j) list[j] = -INFINITY;
         }
     }
 
@@ -369,6 +372,8 @@ cudaError_t launch_gate_t(GateArgs a, cudaStream_t s) {
     while (vpl * 32 < a.E) vpl *= 2;
     const int per = a.E / a.groups, lanes = per / vpl;
     a.lanes_per_group = per % vpl == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    a.share_lanes = 1;
+    while (a.share_lanes * 2 * a.groups <= 32) a.share_lanes *= 2;
     const size_t smem = a.groups > 1 && a.lanes_per_group == 0 ? sizeof(float) * kGateWarps * a.E : 0;
     if (vpl == 8 && a.K == 8) return launch_gate_k<8, T, 8>(a, smem, s);
     switch (vpl) {
