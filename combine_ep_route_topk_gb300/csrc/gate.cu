@@ -366,6 +366,18 @@ cudaError_t launch_gate_k(const GateArgs& a, size_t smem, cudaStream_t s) {
                   s, a);
 }
 
+// The rounds unrolled for the usual numbers of picks: a round then moves only as
+// much of the winner's list as the rounds left can need.
+template <int VPL, typename T>
+cudaError_t launch_gate_v(const GateArgs& a, size_t smem, cudaStream_t s) {
+    switch (a.K) {
+        case 4: return launch_gate_k<VPL, T, 4>(a, smem, s);
+        case 6: return launch_gate_k<VPL, T, 6>(a, smem, s);
+        case 8: return launch_gate_k<VPL, T, 8>(a, smem, s);
+        default: return launch_gate_k<VPL, T, 0>(a, smem, s);
+    }
+}
+
 template <typename T>
 cudaError_t launch_gate_t(GateArgs a, cudaStream_t s) {
     int vpl = 1;
@@ -375,12 +387,11 @@ cudaError_t launch_gate_t(GateArgs a, cudaStream_t s) {
     a.share_lanes = 1;
     while (a.share_lanes * 2 * a.groups <= 32) a.share_lanes *= 2;
     const size_t smem = a.groups > 1 && a.lanes_per_group == 0 ? sizeof(float) * kGateWarps * a.E : 0;
-    if (vpl == 8 && a.K == 8) return launch_gate_k<8, T, 8>(a, smem, s);
     switch (vpl) {
         case 1: return launch_gate_k<1, T, 0>(a, smem, s);
         case 2: return launch_gate_k<2, T, 0>(a, smem, s);
-        case 4: return launch_gate_k<4, T, 0>(a, smem, s);
-        case 8: return launch_gate_k<8, T, 0>(a, smem, s);
+        case 4: return launch_gate_v<4, T>(a, smem, s);
+        case 8: return launch_gate_v<8, T>(a, smem, s);
         case 16: return launch_gate_k<16, T, 0>(a, smem, s);
         default: return launch_gate_k<32, T, 0>(a, smem, s);
     }

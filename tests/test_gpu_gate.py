@@ -72,6 +72,11 @@ CASES = [
     (64, 16, 2, SIG, False, 4, 2, 2, True, 1.0, torch.float32, 0.5),
     (64, 12, 4, SIG, True, 12, 5, 2, True, 1.0, torch.float32, 0.2),
     (2050, 128, 4, SIG, True, 4, 2, 1, True, 1.0, torch.bfloat16, 0.0),
+    (70, 100, 8, SIG, True, 5, 3, 2, True, 1.0, torch.float32, 0.1),
+    (70, 128, 6, SOFT, True, 8, 4, 2, False, 1.0, torch.float32, 0.0),
+    (70, 200, 4, SOFT, False, 1, 1, 1, True, 1.0, torch.bfloat16, 0.9),
+    (70, 256, 5, SIG, False, 32, 9, 2, True, 1.0, torch.float32, 0.6),
+    (4099, 256, 8, SOFT, False, 4, 2, 2, True, 1.0, torch.float32, 0.0),
 ]
 
 
@@ -196,6 +201,9 @@ GRAD = [
     (20, 1023, 32, SIG, True, 1.0, torch.float32, 0.1),
     (20, 1, 1, SIG, False, 1.0, torch.float32, 0.0),
     (20, 3, 1, SOFT, True, 1.0, torch.float32, 0.0),
+    (4103, 61, 8, SIG, True, 1.5, torch.float32, 0.2),
+    (4097, 256, 8, SOFT, True, 1.0, torch.bfloat16, 0.0),
+    (4098, 96, 5, SIG, False, 1.0, torch.float32, 0.9),
 ]
 
 
