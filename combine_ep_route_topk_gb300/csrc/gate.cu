@@ -92,16 +92,19 @@ __device__ __forceinline__ float lanes_max(float v) {
 // others' the picks' scores lie.  Quotients by the hardware's reciprocal (1 ulp).
 template <int G>
 __device__ __forceinline__ float pick_share(float l, bool picked, int score) {
-    float c = lanes_max<G>(picked ? l : -INFINITY);
     float s = 0.0f;
     if (score == kScoreSigmoid) {
         // l > 0 (then c = 0): 1 / (1 + exp(-l)); else exp(l - c) / (1 + exp(l))
         const float e = expf(-fabsf(l));
         float num = l > 0.0f ? 1.0f : e;
-        if (c < 0.0f) num = expf(l - c);
+        if (__any_sync(kFull, picked && l < 0.0f)) {  // some token's picks may all be negative
+            const float c = lanes_max<G>(picked ? l : -INFINITY);
+            if (c < 0.0f) num = expf(l - c);
+        }
         if (picked) s = num * rcp_fast(1.0f + e);
-    } else if (picked) {
-        s = expf(l - c);
+    } else {
+        const float c = lanes_max<G>(picked ? l : -INFINITY);
+        if (picked) s = expf(l - c);
     }
     const float sum = lanes_sum<G>(s);  // at least 1/2 where anything is picked
     return picked ? s * rcp_fast(sum) : 0.0f;
@@ -345,7 +348,7 @@ gate_kernel(GateArgs a) {
     float l = -INFINITY, s = 0.0f;
     if (my_id >= 0) l = clamp_logit(load_one(row + my_id));
     if (a.renorm) {
-        s = pick_share<32>(l, my_id >= 0, a.score);
+        s = pick_share<KT == 0 ? 32 : 8>(l, my_id >= 0, a.score);  // the picks are in the first K lanes
     } else if (my_id >= 0) {
         s = sigmoids ? sigmoid(l) : expf(l - m) * inv_total;
     }
@@ -432,12 +435,12 @@ __device__ __forceinline__ void invert_map(const int32_t* emap, int E, int* inv)
     __syncthreads();
 }
 
-// Pick k of token t: its expert (-1: none, or not available), its logit and
-// scale * gradient of its weight (0 without an expert).
+// A pick of token t with the id that topk_idx gave and the gradient of its
+// weight: its expert (-1: none, or not available), its logit and scale times the
+// gradient (0 without an expert).
 template <typename T>
-__device__ __forceinline__ int load_pick(const GateGradArgs& a, int t, int k, const int* inv, float& l, float& g) {
-    int id = __ldg(a.topk_idx + (size_t)t * a.K + k);
-    g = a.scale * __ldg(a.d_w + (size_t)t * a.K + k);
+__device__ __forceinline__ int load_pick(const GateGradArgs& a, int t, int id, const int* inv, float& l, float& g) {
+    g *= a.scale;
     if (id < 0 || id >= a.E) id = -1;
     if (id >= 0 && a.emap != nullptr) {
         id = inv[id];
@@ -467,15 +470,20 @@ gate_backward_kernel(GateGradArgs a) {
     if (t0 >= a.N) return;  // warp-uniform
     T* out = static_cast<T*>(a.d_logits) + (size_t)t0 * a.E;
     const int n = min(TPW, a.N - t0) * a.E;
+    const int i = lane / G, k = lane % G, t = t0 + i;
+    const bool has = k < a.K && t < a.N;
+    int id = -1;
+    float g = 0.0f, l = -INFINITY, d = 0.0f;
+    if (has) {
+        id = __ldg(a.topk_idx + (size_t)t * a.K + k);
+        g = __ldg(a.d_w + (size_t)t * a.K + k);
+    }
     if (a.vec) {
         for (int e = lane * 4; e < n; e += 128) store_four(out + e, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
     } else {
         for (int e = lane; e < n; e += 32) store_one(out + e, 0.0f);
     }
-    const int i = lane / G, k = lane % G, t = t0 + i;
-    int id = -1;
-    float g = 0.0f, l = -INFINITY, d = 0.0f;
-    if (k < a.K && t < a.N) id = load_pick<T>(a, t, k, s_inv, l, g);
+    if (has) id = load_pick<T>(a, t, id, s_inv, l, g);
     if (a.renorm) {
         const float q = pick_share<G>(l, id >= 0, a.score);
         d = (g - lanes_sum<G>(g * q)) * q;
@@ -506,7 +514,11 @@ gate_backward_dense_kernel(GateGradArgs a) {
     load_row<VPL>(static_cast<const T*>(a.logits) + (size_t)t * E, E, a.vec != 0, lane, v);
     int id = -1;
     float g = 0.0f, l = -INFINITY;
-    if (lane < a.K) id = load_pick<T>(a, t, lane, s_inv, l, g);
+    if (lane < a.K) {
+        id = __ldg(a.topk_idx + (size_t)t * a.K + lane);
+        g = __ldg(a.d_w + (size_t)t * a.K + lane);
+        id = load_pick<T>(a, t, id, s_inv, l, g);
+    }
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
