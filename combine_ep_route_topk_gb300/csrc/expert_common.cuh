@@ -38,33 +38,37 @@ __device__ __forceinline__ size_t first_row(const MatmulArgs& a, int e, int begi
 // the experts before 8 i (an eighth of a full table, so that it takes half a KB
 // of shared memory); s_tiles[kTileGroups] = all of them.  Computed by the
 // block's first 128 threads, 8 experts each; every thread calls it, and it ends
-// with a barrier.
+// with a barrier.  (Offsets whose ranges overlap can count a row more than once;
+// sums are taken in 64 bits and held at 2^31 - 1, so that they stay in order.)
 constexpr int kPerGroup = 8;
 constexpr int kTileGroups = kMaxE / kPerGroup;
-__device__ __forceinline__ void tile_prefix(const MatmulArgs& a, int tile, int* s_tiles, int* s_warp) {
+__device__ __forceinline__ int tile_count(int rows, int tile) {
+    return (int)(((uint32_t)rows + tile - 1) / (uint32_t)tile);
+}
+__device__ __forceinline__ void tile_prefix(const MatmulArgs& a, int tile, int* s_tiles, long long* s_warp) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int sum = 0, incl = 0;
+    long long sum = 0, incl = 0;
     if (tid < kTileGroups) {
 #pragma unroll
         for (int j = 0; j < kPerGroup; ++j) {
             const int e = tid * kPerGroup + j;
             int begin;
-            sum += e < a.E ? (expert_rows(a, e, begin) + tile - 1) / tile : 0;
+            sum += e < a.E ? tile_count(expert_rows(a, e, begin), tile) : 0;
         }
         incl = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(kFull, incl, off);
+            const long long o = __shfl_up_sync(kFull, incl, off);
             if (lane >= off) incl += o;
         }
         if (lane == 31) s_warp[warp] = incl;
     }
     __syncthreads();
     if (tid < kTileGroups) {
-        int run = incl - sum;
+        long long run = incl - sum;
         for (int w = 0; w < warp; ++w) run += s_warp[w];
-        s_tiles[tid] = run;
-        if (tid == kTileGroups - 1) s_tiles[kTileGroups] = run + sum;
+        s_tiles[tid] = (int)min(run, (long long)INT32_MAX);
+        if (tid == kTileGroups - 1) s_tiles[kTileGroups] = (int)min(run + sum, (long long)INT32_MAX);
     }
     __syncthreads();
 }
@@ -83,11 +87,11 @@ __device__ __forceinline__ ExpertTile expert_in_group(const MatmulArgs& a, int t
         begin[j] = rows[j] = 0;
         if (g * kPerGroup + j < a.E) rows[j] = expert_rows(a, g * kPerGroup + j, begin[j]);
     }
-    ExpertTile x = {g * kPerGroup, begin[0], rows[0], s_tiles[g], (rows[0] + tile - 1) / tile};
+    ExpertTile x = {g * kPerGroup, begin[0], rows[0], s_tiles[g], tile_count(rows[0], tile)};
 #pragma unroll
     for (int j = 1; j < kPerGroup; ++j)
-        if (t >= x.first + x.count && g * kPerGroup + j < a.E)
-            x = {g * kPerGroup + j, begin[j], rows[j], x.first + x.count, (rows[j] + tile - 1) / tile};
+        if (t - x.first >= x.count && g * kPerGroup + j < a.E)
+            x = {g * kPerGroup + j, begin[j], rows[j], x.first + x.count, tile_count(rows[j], tile)};
     return x;
 }
 

@@ -100,7 +100,7 @@ __device__ __forceinline__ void channels(const MatmulArgs& a, int e, int n, int 
 __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
 matmul_rows_kernel(MatmulArgs a) {
     __shared__ int s_groups[kTileGroups + 1];  // prefix of the experts' row groups
-    __shared__ int s_warp[kWarps];
+    __shared__ long long s_warp[kTileGroups / 32];
     pdl_prologue();
     const int lane = threadIdx.x & 31;
     if (a.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;

@@ -95,7 +95,7 @@ struct Shared {
     uint8_t out[kOutWarps][16 * kOutPitch];
     uint32_t tmem;
     int abort;
-    int warp_sums[8];
+    long long warp_sums[kTileGroups / 32];
     int tiles[kTileGroups + 1];
 };
 template <class S>
@@ -319,11 +319,13 @@ struct Unit {
 };
 
 // Units of one CTA (or pair): u0, u0 + du, ...  (A unit covers some 2^13
-// elements of an output in memory, so all of them are fewer than 2^32.)
+// elements of an output in memory, so all of them are fewer than 2^32, unless
+// the offsets' ranges overlap: then the first 2^32 - 1 are taken.)
 template <class S>
 __device__ __forceinline__ uint32_t unit_count(const MatmulArgs& a, const Shared* sh, uint32_t u0, uint32_t du) {
-    const uint32_t all = (uint32_t)sh->tiles[kTileGroups] * (((uint32_t)a.Nc + S::kChannels - 1) / S::kChannels);
-    return all > u0 ? (all - u0 + du - 1) / du : 0;
+    const uint64_t ct = ((uint32_t)a.Nc + S::kChannels - 1) / S::kChannels;
+    const uint32_t all = (uint32_t)min((uint64_t)UINT32_MAX, (uint64_t)sh->tiles[kTileGroups] * ct);
+    return all > u0 ? (all - 1 - u0) / du + 1 : 0;
 }
 
 // Steps through them, for the warp that publishes them.  An expert's units are

@@ -194,8 +194,8 @@ gate_kernel(GateArgs a) {
     pdl_prologue();
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
-    const int t = blockIdx.x * kGateWarps + warp;
-    if (t >= a.N) return;  // warp-uniform
+    const uint32_t t = blockIdx.x * kGateWarps + warp;  // unsigned: past N near 2^31 too
+    if (t >= (uint32_t)a.N) return;  // warp-uniform
     const int E = a.E, K = KT > 0 ? KT : a.K;
     const T* row = static_cast<const T*>(a.logits) + (size_t)t * E;
     const int e0 = lane * VPL;
@@ -365,7 +365,7 @@ gate_kernel(GateArgs a) {
 
 template <int VPL, typename T, int KT>
 cudaError_t launch_gate_k(const GateArgs& a, size_t smem, cudaStream_t s) {
-    return launch(gate_kernel<VPL, T, KT>, dim3((a.N + kGateWarps - 1) / kGateWarps), dim3(kGateWarps * 32), smem,
+    return launch(gate_kernel<VPL, T, KT>, dim3((a.N - 1) / kGateWarps + 1), dim3(kGateWarps * 32), smem,
                   s, a);
 }
 
@@ -439,7 +439,7 @@ __device__ __forceinline__ void invert_map(const int32_t* emap, int E, int* inv)
 // weight: its expert (-1: none, or not available), its logit and scale times the
 // gradient (0 without an expert).
 template <typename T>
-__device__ __forceinline__ int load_pick(const GateGradArgs& a, int t, int id, const int* inv, float& l, float& g) {
+__device__ __forceinline__ int load_pick(const GateGradArgs& a, uint32_t t, int id, const int* inv, float& l, float& g) {
     g *= a.scale;
     if (id < 0 || id >= a.E) id = -1;
     if (id >= 0 && a.emap != nullptr) {
@@ -466,12 +466,13 @@ gate_backward_kernel(GateGradArgs a) {
     constexpr int G = 32 / TPW;
     if (a.emap != nullptr) invert_map(a.emap, a.E, s_inv);
     const int lane = threadIdx.x & 31;
-    const int t0 = (blockIdx.x * kGateWarps + (threadIdx.x >> 5)) * TPW;
-    if (t0 >= a.N) return;  // warp-uniform
+    const uint32_t t0 = (blockIdx.x * kGateWarps + (threadIdx.x >> 5)) * TPW, N = (uint32_t)a.N;
+    if (t0 >= N) return;  // warp-uniform
     T* out = static_cast<T*>(a.d_logits) + (size_t)t0 * a.E;
-    const int n = min(TPW, a.N - t0) * a.E;
-    const int i = lane / G, k = lane % G, t = t0 + i;
-    const bool has = k < a.K && t < a.N;
+    const int n = (int)min((uint32_t)TPW, N - t0) * a.E;
+    const int i = lane / G, k = lane % G;
+    const uint32_t t = t0 + i;
+    const bool has = k < a.K && t < N;
     int id = -1;
     float g = 0.0f, l = -INFINITY, d = 0.0f;
     if (has) {
@@ -506,8 +507,8 @@ gate_backward_dense_kernel(GateGradArgs a) {
     pdl_prologue();
     if (a.emap != nullptr) invert_map(a.emap, a.E, s_inv);
     const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kGateWarps + (threadIdx.x >> 5);
-    if (t >= a.N) return;  // warp-uniform
+    const uint32_t t = blockIdx.x * kGateWarps + (threadIdx.x >> 5);
+    if (t >= (uint32_t)a.N) return;  // warp-uniform
     const int E = a.E, e0 = lane * VPL;
     T* out = static_cast<T*>(a.d_logits) + (size_t)t * E;
     float v[VPL];
@@ -553,14 +554,14 @@ gate_backward_dense_kernel(GateGradArgs a) {
 
 template <int VPL, typename T>
 cudaError_t launch_dense(const GateGradArgs& a, size_t smem, cudaStream_t s) {
-    return launch(gate_backward_dense_kernel<VPL, T>, dim3((a.N + kGateWarps - 1) / kGateWarps),
+    return launch(gate_backward_dense_kernel<VPL, T>, dim3((a.N - 1) / kGateWarps + 1),
                   dim3(kGateWarps * 32), smem, s, a);
 }
 
 template <typename T, int TPW>
 cudaError_t launch_sparse(const GateGradArgs& a, size_t smem, cudaStream_t s) {
     constexpr int per = kGateWarps * TPW;
-    return launch(gate_backward_kernel<T, TPW>, dim3((a.N + per - 1) / per), dim3(kGateWarps * 32), smem, s, a);
+    return launch(gate_backward_kernel<T, TPW>, dim3((a.N - 1) / per + 1), dim3(kGateWarps * 32), smem, s, a);
 }
 
 template <typename T>

@@ -65,6 +65,11 @@ __device__ __forceinline__ void store8(int8_t* p, const float (&v)[8], float inv
     *reinterpret_cast<uint2*>(p) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
 }
 
+__device__ __forceinline__ void scale8(float (&v)[8], float f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= f;
+}
+
 // Whether row r holds a token.
 __device__ __forceinline__ bool holds_token(const QuantArgs& a, long long r) {
     if (a.expert_offsets == nullptr) return true;
@@ -121,17 +126,22 @@ __global__ void __launch_bounds__(NT * ROWS) quantize_kernel(QuantArgs a) {
 #pragma unroll
         for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, s_max[w]);
     }
-    const float inv = top > 0.0f ? __fdiv_rn(127.0f, top) : 1.0f;
+    // a row whose largest value is below 1e-30 is scaled up first: 127 / top would
+    // leave the range of a float32
+    const float up = top < 1e-30f ? 0x1p96f : 1.0f;
+    const float inv = top > 0.0f ? __fdiv_rn(127.0f, top * up) : 1.0f;
     if (tid == 0) a.scales[r] = top > 0.0f ? __fdiv_rn(top, 127.0f) : 1.0f;
     if constexpr (HELD > 0) {
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             const int c = (i * NT + tid) * 8;
+            if (up != 1.0f) scale8(v[i], up);  // uniform over the row
             if (c < a.cols) store8(out + c, v[i], inv);
         }
     } else {
         for (int c = tid * 8; c < a.cols; c += NT * 8) {
             values8<T, SWIGLU>(row, a.cols, c, v[0]);
+            if (up != 1.0f) scale8(v[0], up);
             store8(out + c, v[0], inv);
         }
     }

@@ -61,6 +61,21 @@ def test_quantize_rounds_ties_to_even():
     assert q[0, :9].tolist() == [127, 0, 2, 2, 0, -2, -2, 126, -126]
 
 
+@pytest.mark.parametrize("cols", [64, 512, 2048, 20000])
+def test_quantize_tiny_rows(cols):
+    """Rows near the bottom of float32's range: 127 over their largest value
+    would overflow.  Scales below the normal range hold fewer bits, so codes are
+    compared with v / (max|v| / 127) and the scale within a denormal unit."""
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn((5, cols), generator=g) * torch.tensor([[1e-30], [1e-34], [1e-37], [1e-40], [1e-44]])
+    x[:, 3] = 0.0
+    q, s = ep.ep_quantize_rows(x.cuda())
+    v = x.double().numpy()
+    want, scale = ref.quantize(v)
+    assert np.abs(q.double().cpu().numpy() - want).max() <= CODE_TOL
+    assert (np.abs(s.double().cpu().numpy() - scale) <= SCALE_RTOL * scale + 2.0 ** -149).all()
+
+
 @pytest.mark.parametrize("layout", [CONTIG, MASKED])
 def test_quantize_skips_rows_without_a_token(layout):
     E, cap, cols = 4, 6, 64
@@ -246,6 +261,48 @@ def test_matmul_runs_on_the_given_stream_in_a_graph_and_repeats():
         want = ep.ep_expert_matmul(x, xs, w, ws, offs)
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_matmul_first_call_of_a_process_inside_a_capture(tmp_path):
+    """Nothing that a first call looks up keeps it from being captured."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+import combine_ep_route_topk_gb300 as ep
+x = torch.randint(-9, 9, (64, 128), device="cuda").to(torch.int8)
+w = torch.randint(-9, 9, (2, 96, 128), device="cuda").to(torch.int8)
+offs = torch.tensor([0, 40, 64], dtype=torch.int32, device="cuda")
+one, ws = torch.ones(64, device="cuda"), torch.ones((2, 96), device="cuda")
+outs = [torch.zeros((64, 96), device="cuda") for _ in range(2)]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    ep.ep_expert_matmul(x, one, w, ws, offs, out=outs[0])
+g.replay()
+torch.cuda.synchronize()
+want = torch.cat([x[:40].double() @ w[0].double().T, x[40:].double() @ w[1].double().T])
+assert torch.equal(outs[0].double(), want)
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("E,rows", [(1024, 2000), (16, 5000)])
+def test_matmul_overlapping_offsets_stay_inside(E, rows):
+    """Every expert claims every row: more tiles than rows, no write outside."""
+    Nc, Kd = 8, 16
+    x = torch.from_numpy(ints((rows, Kd), 1, True)).cuda()
+    w = torch.from_numpy(ints((E, Nc, Kd), 2, True)).cuda()
+    offs = torch.zeros(E + 1, dtype=torch.int32)
+    offs[1::2] = 2 ** 31 - 1
+    buf = torch.full((rows + 64, Nc), 55.0, device="cuda")
+    ep.ep_expert_matmul(x, torch.ones(rows, device="cuda"), w, torch.ones((E, Nc), device="cuda"),
+                        offs.cuda(), out=buf[32:32 + rows])
+    torch.cuda.synchronize()
+    assert (buf[:32] == 55).all() and (buf[32 + rows:] == 55).all()
 
 
 @pytest.mark.slow
