@@ -223,7 +223,7 @@ struct MatmulArgs {
     int x_rows, n_src, rows, E, Nc, Kd, cap, layout, out_bf16;
 };
 cudaError_t launch_expert_matmul(const MatmulArgs& a, cudaStream_t s);
-// The tensor core kernel (expert_matmul_tc.cu); per: rows per expert to expect.
-cudaError_t launch_matmul_tc(const MatmulArgs& a, int per, cudaStream_t s);
+// The tensor core kernel (expert_matmul_tc.cu).
+cudaError_t launch_matmul_tc(const MatmulArgs& a, cudaStream_t s);
 
 }  // namespace ep

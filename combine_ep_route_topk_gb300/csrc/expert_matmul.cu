@@ -149,8 +149,7 @@ cudaError_t launch_expert_matmul(const MatmulArgs& a, cudaStream_t s) {
     if (a.x_rows == 0 || a.rows <= 4 || 5ll * a.rows <= 2ll * a.E) {
         err = launch(matmul_rows_kernel, dim3(sm_count() * kBlocksPerSm), dim3(kWarps * 32), 0, s, a);
     } else {
-        const int per = a.layout == 0 ? (a.rows + a.E - 1) / a.E : a.cap;  // rows per expert
-        err = launch_matmul_tc(a, per, s);
+        err = launch_matmul_tc(a, s);
     }
     note_launch();
     return err;

@@ -34,7 +34,9 @@
 // widened (about 700 cycles after it is free), multiplied and handed back.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "expert_common.cuh"
 
@@ -54,15 +56,19 @@ constexpr uint32_t kWaitHint = 2000;  // ns that one poll of a barrier may sleep
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
 
 // Rows per tile TN, of which each CTA of the CG holds kRows in shared memory.
-template <int CG_, int TN_>
+// KS > 1: the KS CTAs of a cluster divide a tile's K among them and join their
+// sums through each other's shared memory.
+template <int CG_, int TN_, int KS_ = 1>
 struct Shape {
-    static constexpr int CG = CG_, TN = TN_;
+    static constexpr int CG = CG_, TN = TN_, KS = KS_;
+    static constexpr int kCluster = CG * KS;
+    static_assert(KS == 1 || (CG == 1 && TN == 64), "sums are joined in 4 groups of 16 rows");
     static constexpr int kRows = TN / CG;
     static constexpr int kBAtom = kRows * 128;       // 64 K of the rows, float16
     static constexpr int kBBytes = 2 * kBAtom;       // one stage
     static constexpr int kXBytes = kRows * kBK;      // one stage of 8-bit rows
     static constexpr int kStages = kRows <= 64 ? 4 : 3;   // converted operands
-    static constexpr int kWStages = kRows <= 80 ? 6 : 4;  // 8-bit weights in flight
+    static constexpr int kWStages = kRows <= 80 && KS == 1 ? 6 : 4;  // 8-bit weights in flight
     static constexpr int kXStages = kRows <= 80 ? 4 : 2;  // 8-bit rows in flight
     static constexpr int kRowWarps = 2 * ((kRows + 31) / 32);
     static constexpr int kThreads = (kRowWarp0 + kRowWarps) * 32;
@@ -71,12 +77,13 @@ struct Shape {
     static constexpr uint32_t kTmemA = kAcc * TN;
     static constexpr int kChannels = 128 * CG;
     static constexpr int kGrain = 16;                // an MMA's N is a multiple
+    static constexpr int kPartBytes = KS > 1 ? 4 * 16 * 128 * 4 : 0;  // [KS][4 / KS groups][16 rows][128 channels]
     static_assert(kBAtom % 1024 == 0 && kTmemA + kStages * 64 <= kTmemCols, "swizzle, TMEM");
 };
 
 constexpr int kMaxStages = 4, kMaxWStages = 6, kMaxXStages = 4;
 // Units published ahead.  The TMA warp publishes one when it has issued all
-// copies of those before, which its stages keep within 8 + 2 + 4 blocks of the
+// copies of those before, which its stages keep within 6 + 4 + 4 blocks of the
 // MMAs and the accumulators within 2 units more of the output warps: a slot is
 // read long before it is written again.
 constexpr int kUnitSlots = 32;
@@ -87,6 +94,7 @@ struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drained;
+    uint64_t part_full, part_empty;
     uint64_t unit_full[kUnitSlots];
     int4 unit[kUnitSlots];
     float row_scales[kOutWarps][128];  // of the rows that an output warp stores
@@ -100,7 +108,7 @@ struct Shared {
 };
 template <class S>
 constexpr int kSmemBytes = 1024 + S::kStages * S::kBBytes + S::kWStages * kWBytes + S::kXStages * S::kXBytes +
-                           (int)sizeof(Shared);
+                           S::kPartBytes + (int)sizeof(Shared);
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return (uint32_t)__cvta_generic_to_shared(p);
@@ -163,6 +171,28 @@ __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
             "mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
             : "memory");
     }
+}
+
+// The barrier's and a float's place in CTA `cta` of the cluster, with the order
+// that data passed between CTAs by ordinary stores needs.
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t cta) {
+    asm volatile(
+        "{\n.reg .b32 a;\n"
+        "mapa.shared::cluster.u32 a, %0, %1;\n"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar)), "r"(cta)
+        : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t at, uint32_t cta, float v) {
+    asm volatile(
+        "{\n.reg .b32 a;\n"
+        "mapa.shared::cluster.u32 a, %0, %1;\n"
+        "st.shared::cluster.f32 [a], %2;\n}\n" ::"r"(at), "r"(cta), "f"(v) : "memory");
+}
+// A whole warp's wait for what other CTAs stored.
+__device__ __forceinline__ bool mbar_wait_cluster(Shared* sh, uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_wait_warp(sh, bar, parity);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    return ok;
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
@@ -395,14 +425,16 @@ template <class S>
 __global__ void __launch_bounds__(S::kThreads, 1)
 matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
     constexpr int CG = S::CG, kAcc = S::kAcc, kStages = S::kStages, kWStages = S::kWStages, kXStages = S::kXStages;
-    constexpr int kBBytes = S::kBBytes, kBAtom = S::kBAtom;
+    constexpr int kBBytes = S::kBBytes, kBAtom = S::kBAtom, KS = S::KS;
     extern __shared__ uint8_t s_raw[];
     uint8_t* s_b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* s_w = s_b + kStages * kBBytes;
     uint8_t* s_x = s_w + kWStages * kWBytes;
-    Shared* sh = reinterpret_cast<Shared*>(s_x + kXStages * S::kXBytes);
+    uint8_t* s_part = s_x + kXStages * S::kXBytes;
+    Shared* sh = reinterpret_cast<Shared*>(s_part + S::kPartBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;
+    const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;  // of the pair
+    const int part = KS > 1 ? (int)(blockIdx.x % KS) : 0;   // of K
 
     pdl_prologue();
     if (tid == 0) {
@@ -425,6 +457,8 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         }
         for (int i = 0; i < kUnitSlots; ++i) mbar_init(&sh->unit_full[i], 1);
         mbar_init(&sh->drained, 1);
+        mbar_init(&sh->part_full, kOutWarps * KS);
+        mbar_init(&sh->part_empty, kOutWarps * KS);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (a.status != nullptr && blockIdx.x == 0) *a.status = 0;
     }
@@ -438,18 +472,21 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
     }
     tmem_fence_before();
     tile_prefix(a, S::TN, sh->tiles, sh->warp_sums);
-    if constexpr (CG == 2) {
+    if constexpr (S::kCluster > 1) {
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     tmem_fence_after();
     const uint32_t tmem = sh->tmem;
-    const uint32_t units = unit_count<S>(a, sh, blockIdx.x / CG, gridDim.x / CG);
-    const int kblocks = (a.Kd + kBK - 1) / kBK;
+    const uint32_t cluster = blockIdx.x / S::kCluster, clusters = gridDim.x / S::kCluster;
+    const uint32_t units = unit_count<S>(a, sh, cluster, clusters);
+    // this CTA's blocks of K: kb0 .. kb1 - 1, at least one (the launcher sees to it)
+    const int all_blocks = (a.Kd + kBK - 1) / kBK;
+    const int kb0 = all_blocks * part / KS, kb1 = all_blocks * (part + 1) / KS, kblocks = kb1 - kb0;
 
     if (warp == kTmaWarp) {
         // ---- units, and the weights' TMA boxes ----
-        Steps<S> steps(a, blockIdx.x / CG, gridDim.x / CG);
+        Steps<S> steps(a, cluster, clusters);
         uint32_t c = 0;  // stages issued so far
         bool ok = true;
         for (uint32_t u = 0; ok && u < units; ++u) {
@@ -460,7 +497,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             }
             const Unit t = unpack<S>(packed);
             const int row = t.e * a.Nc + t.channel + rank * 128;
-            for (int kb = 0; kb < kblocks; ++kb, ++c) {
+            for (int kb = kb0; kb < kb1; ++kb, ++c) {
                 const uint32_t s = c % kWStages;
                 ok = mbar_wait_warp(sh, &sh->w_empty[s], (c / kWStages & 1) ^ 1);
                 if (!ok) break;
@@ -488,7 +525,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
                 ok = mbar_wait_warp(sh, &sh->acc_empty[acc], (it / kAcc & 1) ^ 1);
                 if (!ok) break;
                 const uint32_t d = tmem + acc * S::TN;
-                for (int kb = 0; kb < kblocks; ++kb, ++c) {
+                for (int kb = kb0; kb < kb1; ++kb, ++c) {
                     const uint32_t s = c % kStages;
                     ok = mbar_wait_warp(sh, &sh->full[s], c / kStages & 1);
                     if (!ok) break;
@@ -502,15 +539,15 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
 #pragma unroll
                             for (int k = 0; k < kBK / 16; ++k)
                                 mma_f16<CG>(d, at + k * 8, desc + ((k >> 2) * kBAtom + (k & 3) * 32 >> 4), idesc,
-                                            k > 0 || kb > 0);
+                                            k > 0 || kb > kb0);
                         } else {  // the last, short block
                             for (int k = 0; k < kBK / 16; ++k)
                                 if ((k & 3) * 2 < pieces)
                                     mma_f16<CG>(d, at + k * 8, desc + ((k >> 2) * kBAtom + (k & 3) * 32 >> 4),
-                                                idesc, k > 0 || kb > 0);
+                                                idesc, k > 0 || kb > kb0);
                         }
                         mma_commit<CG>(&sh->empty[s]);
-                        if (kb == kblocks - 1) mma_commit<CG>(&sh->acc_full[acc]);
+                        if (kb == kb1 - 1) mma_commit<CG>(&sh->acc_full[acc]);
                     }
                     __syncwarp();
                 }
@@ -547,7 +584,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
                 const int row = (r < half && rr < t.rows) ? max(0, source_row(a, t.e, t.begin, t.first + rr)) : 0;
                 src[i] = a.x + (size_t)row * a.Kd + chunk * 16;
             }
-            for (int kb = 0; kb < kblocks; ++kb, ++c) {
+            for (int kb = kb0; kb < kb1; ++kb, ++c) {
                 const uint32_t s = c % kXStages;
                 ok = mbar_wait_warp(sh, &sh->x_empty[s], (c / kXStages & 1) ^ 1);
                 if (!ok) break;
@@ -656,7 +693,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         const int quarter = warp & 3, h = warp >> 2;
         float* row_scales = sh->row_scales[warp];
         const uint32_t stage = smem_u32(sh->out[warp]);
-        const bool vectors = a.out_bf16 && a.Nc % 8 == 0;  // rows of out start on 16 bytes
+        const bool vectors = KS == 1 && a.out_bf16 && a.Nc % 8 == 0;  // rows of out start on 16 bytes
         const int size = a.out_bf16 ? 2 : 4;
         const size_t pitch = (size_t)a.Nc * size;
         for (uint32_t u = 0; u < units; ++u) {
@@ -667,7 +704,8 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             uint8_t* to = static_cast<uint8_t*>(a.out) +
                           (first_row(a, t.e, t.begin) + t.first) * pitch + (size_t)ch0 * size;
             for (int i = lane; i < S::TN / 2; i += 32) {
-                const int r = (i >> 4) * 32 + h * 16 + (i & 15);
+                // the warp's rows; with K divided, those that this CTA joins (the first 64 / KS)
+                const int r = KS == 1 ? (i >> 4) * 32 + h * 16 + (i & 15) : ((i >> 4) * KS + part) * 16 + (i & 15);
                 const int src = r < t.rows ? source_row(a, t.e, t.begin, t.first + r) : -1;
                 row_scales[i] = src >= 0 ? __ldg(a.x_scales + src) : 0.0f;
             }
@@ -682,9 +720,49 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             if (!mbar_wait_warp(sh, &sh->acc_full[acc], u / kAcc & 1)) break;
             tmem_fence_after();
             const uint32_t from = tmem + ((uint32_t)quarter << 21) + acc * S::TN;
+            if constexpr (KS > 1) {
+                // Rows 16 g .. 16 g + 15 are joined by CTA g % KS: every CTA stores its
+                // sums there, and their owner adds them in the order of K.
+                const uint32_t parts = smem_u32(s_part);
+                const float* mine = reinterpret_cast<const float*>(s_part);
+                const int ch = quarter * 32 + lane;
+                if (!mbar_wait_cluster(sh, &sh->part_empty, (u & 1) ^ 1)) break;
+                for (int g = h; g * 16 < t.n; g += 2) {
+                    uint32_t v[16];
+                    tmem_load16(from + g * 16, v);
+                    const uint32_t at = parts + (((part * (4 / KS) + g / KS) * 16) * 128 + ch) * 4;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) store_cluster(at + j * 128 * 4, g % KS, __uint_as_float(v[j]));
+                }
+                tmem_fence_before();
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
+                if (lane < KS) mbar_arrive_cluster(&sh->part_full, lane);
+                if (!mbar_wait_cluster(sh, &sh->part_full, u & 1)) break;
+                for (int gl = 0; gl < 4 / KS; ++gl) {
+                    const int n0 = (gl * KS + part) * 16 + h * 8;  // two warps share the 16 rows
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int p = 0; p < KS; ++p) sum += mine[((p * (4 / KS) + gl) * 16 + h * 8 + j) * 128 + ch];
+                        const float y = sum * row_scales[gl * 16 + h * 8 + j] * ws[0];
+                        if (n0 + j < t.rows && ch0 + lane < a.Nc) {
+                            uint8_t* at = to + (size_t)(n0 + j) * pitch + lane * size;
+                            if (a.out_bf16) *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(y);
+                            else *reinterpret_cast<float*>(at) = y;
+                        }
+                    }
+                }
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                __syncwarp();
+                if (lane < KS) mbar_arrive_cluster(&sh->part_empty, lane);
+                continue;
+            }
             if (vectors) {
-                const int part = (lane & 3) * 8;  // 8 channels of one row: 16 bytes
-                const bool in = ch0 + part < a.Nc;
+                const int piece = (lane & 3) * 8;  // 8 channels of one row: 16 bytes
+                const bool in = ch0 + piece < a.Nc;
                 for (int n0 = h * 16, i0 = 0; n0 < t.n; n0 += 32, i0 += 16) {
                     float lo[8], hi[8];  // channels 0 .. 15 and 16 .. 31
                     tmem_load_tile(from + n0, lo);
@@ -704,8 +782,8 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const int r = g * 8 + (lane >> 2);
-                        const uint4 v = load_shared(stage + r * kOutPitch + part * 2);
-                        if (in && n0 + r < t.rows) *reinterpret_cast<uint4*>(to + (n0 + r) * pitch + part * 2) = v;
+                        const uint4 v = load_shared(stage + r * kOutPitch + piece * 2);
+                        if (in && n0 + r < t.rows) *reinterpret_cast<uint4*>(to + (n0 + r) * pitch + piece * 2) = v;
                     }
                     __syncwarp();  // the stage is free again
                 }
@@ -734,7 +812,7 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) {
+    if constexpr (S::kCluster > 1) {
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
@@ -772,11 +850,10 @@ EncodeTiled encode_tiled() {
 }
 
 // Grid of the persistent kernel on the current device: a CTA per SM, or as
-// many pairs as the device holds at once (an SM without a neighbour in its
-// cluster cannot host half a pair).  Looked up once per device.
+// many clusters as the device holds at once (an SM without a neighbour in its
+// cluster cannot host a part of one).  Looked up once per device.
 template <class S>
 cudaError_t persistent_grid(int* grid) {
-    constexpr int CG = S::CG;
     static std::atomic<int> cached[64];
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -786,22 +863,22 @@ cudaError_t persistent_grid(int* grid) {
         err = cudaFuncSetAttribute(matmul_tc_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<S>);
         if (err != cudaSuccess) return err;
         n = sm_count();
-        if (CG == 2) {
+        if (S::kCluster > 1) {
             cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(n / 2 * 2);
+            cfg.gridDim = dim3(n / S::kCluster * S::kCluster);
             cfg.blockDim = dim3(S::kThreads);
             cfg.dynamicSmemBytes = kSmemBytes<S>;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.x = S::kCluster;
             attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            int pairs = 0;
-            err = cudaOccupancyMaxActiveClusters(&pairs, matmul_tc_kernel<S>, &cfg);
+            int clusters = 0;
+            err = cudaOccupancyMaxActiveClusters(&clusters, matmul_tc_kernel<S>, &cfg);
             if (err != cudaSuccess) return err;
-            if (pairs < 1) return cudaErrorInvalidConfiguration;
-            n = 2 * pairs;
+            if (clusters < 1) return cudaErrorInvalidConfiguration;
+            n = S::kCluster * clusters;
         }
         if (dev >= 0 && dev < 64) cached[dev].store(n, std::memory_order_relaxed);
     }
@@ -811,7 +888,6 @@ cudaError_t persistent_grid(int* grid) {
 
 template <class S>
 cudaError_t launch_tc(const MatmulArgs& a, cudaStream_t s) {
-    constexpr int CG = S::CG;
     static_assert(kSmemBytes<S> <= 227 * 1024, "a CTA's shared memory");
     const EncodeTiled encode = encode_tiled();
     if (encode == nullptr) return cudaErrorNotSupported;
@@ -833,9 +909,9 @@ cudaError_t launch_tc(const MatmulArgs& a, cudaStream_t s) {
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (CG == 2) {
+    if (S::kCluster > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.x = S::kCluster;
         attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
         ++n;
     }
@@ -851,19 +927,57 @@ cudaError_t launch_tc(const MatmulArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// By the rows per expert to expect (the capacity, where a masked layout holds
-// more).  A tile that holds an expert's rows whole reads and widens its weights
-// once; narrow tiles leave shared memory for more weights in flight and TMEM for
-// a second accumulator, wide ones use the tensor cores better.  Measured on a
-// GB300 (us; 32 experts of 4096 x 7168 unless noted) with TN = 64, 160, 256:
-//   8 rows 149, 154           32 rows 159, 158, 205     64 rows 170, 166, 214
-//   128 rows 311, 186, 231    160 rows 441, 200, 241    256 rows 594, 338, 284
-//   128 experts of 2880 x 1440: 16 rows 101, 113; 48 rows 112, 122; counts drawn
-//   around 128: 250, 148, 167.  Counts scatter, so 160 serves means up to 140.
-cudaError_t launch_matmul_tc(const MatmulArgs& a, int per, cudaStream_t s) {
-    if (per <= 48) return launch_tc<Shape<1, 64>>(a, s);
-    if (per <= 140) return launch_tc<Shape<2, 160>>(a, s);
-    return launch_tc<Shape<2, 256>>(a, s);
+namespace {
+
+// Cycles that a shape would take, by the waves of its tiles.  A block of K takes
+// `base` cycles and `slope` more for each row of the tile (measured; the weights
+// arrive, are widened and multiplied), a tile's start and end 3000, sums that are
+// joined 6500 more.  The counts of several experts scatter around their mean as
+// independent picks would, which decides whether an expert needs one tile more;
+// one expert's count and a capacity are taken as they are.
+template <class S>
+double shape_cycles(const MatmulArgs& a, double base, double slope) {
+    const double mean = a.layout == 0 ? (double)a.rows / a.E : a.cap;
+    const double sigma = a.layout == 0 && a.E > 1 ? std::sqrt(mean) : 0.0;
+    // An expert's tiles: one more for each multiple of TN that its count exceeds.
+    double tiles = std::max(1.0, sigma == 0.0 ? std::ceil(mean / S::TN) : std::floor((mean - 4.0 * sigma) / S::TN));
+    for (int k = (int)tiles; sigma > 0.0 && k * (double)S::TN < mean + 4.0 * sigma; ++k)
+        tiles += 0.5 * std::erfc((k * S::TN - mean) / (sigma * std::sqrt(2.0)));
+    double all = a.E * tiles;
+    if (a.layout == 0) all = std::min(all, std::min(a.E, a.rows) + std::floor((double)a.rows / S::TN));
+    const double rows = std::min((double)S::TN, std::max(1.0, mean / tiles));
+    const double blocks = std::ceil(std::ceil(a.Kd / (double)kBK) / S::KS);
+    const double waves = std::ceil(all * std::ceil(a.Nc / (double)S::kChannels) / (sm_count() / S::kCluster));
+    return waves * (blocks * (base + slope * rows) + (S::KS > 1 ? 9500.0 : 3000.0));
+}
+
+}  // namespace
+
+// A tile that holds an expert's rows whole reads and widens its weights once;
+// narrow tiles leave shared memory for more weights in flight and TMEM for a
+// second accumulator, wide ones use the tensor cores better, and where there are
+// few tiles K is divided among CTAs.  The shape with the least estimated cycles
+// is taken.  Measured on a GB300 (us; counts drawn around their mean) with
+// TN = 64, 160, 256:
+//   32 experts of 4096 x 7168: mean 8 147, 151, 192; 64 214, 168, 215;
+//     128 361, 186, 233; 160 445, 266, 244; 320 799, 420, 439; 512 1244, 663, 564
+//   128 experts of 2880 x 1440: mean 8 98, 116, 140; 64 157, 130, 156;
+//     128 260, 146, 171; 200 389, 249, 196; 512 905, 505, 449
+// and with K whole, in 2 and in 4 parts:
+//   1 expert of 4096 x 4096: 8 rows 15.6, 13.6, 12.3; 64 rows 18.0, 15.4, 13.4
+//   4 experts of 4096 x 4096, 64 rows: 18.2, 22.4, 28.6
+//   6 experts of 500 x 1008, 64 rows: 8.4, 9.9, 10.0
+cudaError_t launch_matmul_tc(const MatmulArgs& a, cudaStream_t s) {
+    const int blocks = (a.Kd + kBK - 1) / kBK;
+    const double c64 = shape_cycles<Shape<1, 64>>(a, 560.0, 3.2), c160 = shape_cycles<Shape<2, 160>>(a, 620.0, 1.55),
+                 c256 = shape_cycles<Shape<2, 256>>(a, 820.0, 1.6);
+    const double whole = std::min(c64, std::min(c160, c256));
+    const double two = blocks >= 2 ? shape_cycles<Shape<1, 64, 2>>(a, 560.0, 3.2) : whole;
+    const double four = blocks >= 4 ? shape_cycles<Shape<1, 64, 4>>(a, 560.0, 3.2) : whole;
+    if (std::min(two, four) < whole)
+        return four < two ? launch_tc<Shape<1, 64, 4>>(a, s) : launch_tc<Shape<1, 64, 2>>(a, s);
+    if (c64 == whole) return launch_tc<Shape<1, 64>>(a, s);
+    return c160 == whole ? launch_tc<Shape<2, 160>>(a, s) : launch_tc<Shape<2, 256>>(a, s);
 }
 
 }  // namespace ep

@@ -177,6 +177,22 @@ def test_matmul_one_expert_any_rows(rows):
     run_case([rows], 384, 400, CONTIG, 0, False, torch.float32, seed=rows)
 
 
+@pytest.mark.parametrize("counts,Nc,Kd", [
+    ([40] * 40, 640, 144),            # more tiles than CTAs, narrow
+    ([130, 100, 0, 159] * 8, 1100, 400),
+    ([300, 257] * 10, 1100, 144),     # wide tiles
+    ([700, 1, 0, 90] * 6, 1030, 272),
+    ([5], 2000, 1440),                # few tiles: K divided among CTAs
+    ([64], 256, 2064),
+    ([50, 0, 3], 200, 528),
+    ([17] * 6, 130, 384),
+])
+@pytest.mark.parametrize("layout,gather,out_dtype", [(CONTIG, True, torch.bfloat16), (CONTIG, False, torch.float32),
+                                                     (MASKED, True, torch.float32)])
+def test_matmul_many_and_few_tiles(counts, Nc, Kd, layout, gather, out_dtype):
+    run_case(counts, Nc, Kd, layout, max(counts) if layout == MASKED else 0, gather, out_dtype, seed=Kd)
+
+
 @pytest.mark.parametrize("Kd", [16, 32, 112, 128, 144, 2032, 7168, 65536])
 @pytest.mark.parametrize("rows", [3, 150])
 def test_matmul_lengths(Kd, rows):
