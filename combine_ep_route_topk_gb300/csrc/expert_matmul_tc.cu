@@ -12,13 +12,13 @@
 // A tile is 128 channels a CTA (the M side: weights) x up to TN rows (the N
 // side).  CG = 1: one CTA.  CG = 2: a pair of CTAs on 256 channels, each
 // holding half of the rows' operand.
-//   TMA warp        the list of tiles; weights, [128 channels x 128 bytes] boxes,
-//                   128-byte swizzle
+//   TMA warp        weights, [128 channels x 128 bytes] boxes, 128-byte swizzle
 //   2 copying warps x rows, wherever they lie, by 16-byte background copies
 //   8 weight warps  8-bit stages -> float16 -> TMEM (the A operand's stages)
 //   row warps       8-bit stages -> float16 -> shared memory (B)
 //   MMA warp        one elected thread issues 8 MMAs of K = 16 per stage
-//   8 output warps  TMEM -> scales -> bf16 / float32 -> rows of out
+//   8 output warps  the list of tiles and of their rows of x, in turn;
+//                   TMEM -> scales -> bf16 / float32 -> rows of out
 // Within a block of 128 K, both operands hold the first 8 K of each 16 in one
 // half of a stage and the second 8 in the other (a sum's order is free): a row's
 // 8 lanes then store to 8 different banks' groups without exchanging halves.
@@ -82,11 +82,12 @@ struct Shape {
 };
 
 constexpr int kMaxStages = 4, kMaxWStages = 6, kMaxXStages = 4;
-// Units published ahead.  The TMA warp publishes one when it has issued all
-// copies of those before, which its stages keep within 6 + 4 + 4 blocks of the
-// MMAs and the accumulators within 2 units more of the output warps: a slot is
-// read long before it is written again.
-constexpr int kUnitSlots = 32;
+// Units are published by the output warps in turn, kOutWarps ahead of the one
+// whose sums they wait for: the waits for the offsets and for the index of the
+// rows lie off the path of the operands.  A slot is written again when the MMAs
+// of the unit kOutWarps - 1 after its own are over, and with them every other
+// warp's reading of it (the output warps are at most 2 units apart).
+constexpr int kUnitSlots = 2 * kOutWarps;
 constexpr int kOutPitch = 80;
 struct Shared {
     uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
@@ -97,6 +98,7 @@ struct Shared {
     uint64_t part_full, part_empty;
     uint64_t unit_full[kUnitSlots];
     int4 unit[kUnitSlots];
+    int source[kUnitSlots][128];       // of a unit's rows in this CTA: rows of x
     float row_scales[kOutWarps][128];  // of the rows that an output warp stores
     // 16 rows x 32 channels of an output warp on their way to memory; rows 80
     // bytes apart, so that the 8 rows of a stored matrix hit different banks
@@ -358,7 +360,7 @@ __device__ __forceinline__ uint32_t unit_count(const MatmulArgs& a, const Shared
     return all > u0 ? (all - 1 - u0) / du + 1 : 0;
 }
 
-// Steps through them, for the warp that publishes them.  An expert's units are
+// Steps through them, for a warp that publishes them.  An expert's units are
 // consecutive, its row tiles innermost, so that CTAs which run together share
 // weights and rows in L2.  The place moves without a division, and the groups
 // of experts only forward.
@@ -485,17 +487,13 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
     const int kb0 = all_blocks * part / KS, kb1 = all_blocks * (part + 1) / KS, kblocks = kb1 - kb0;
 
     if (warp == kTmaWarp) {
-        // ---- units, and the weights' TMA boxes ----
-        Steps<S> steps(a, cluster, clusters);
+        // ---- the weights' TMA boxes ----
         uint32_t c = 0;  // stages issued so far
         bool ok = true;
         for (uint32_t u = 0; ok && u < units; ++u) {
-            const int4 packed = steps.next(a, sh);
-            if (lane == 0) {
-                sh->unit[u % kUnitSlots] = packed;
-                mbar_arrive(&sh->unit_full[u % kUnitSlots]);
-            }
-            const Unit t = unpack<S>(packed);
+            Unit t;
+            ok = get_unit<S>(sh, u, t);
+            if (!ok) break;
             const int row = t.e * a.Nc + t.channel + rank * 128;
             for (int kb = kb0; kb < kb1; ++kb, ++c) {
                 const uint32_t s = c % kWStages;
@@ -578,12 +576,8 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
             const int half = t.n / CG;  // this CTA's rows of the tile, a multiple of 8
             const int8_t* src[kPer];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int r = r0 + i * 8, rr = rank * half + r;
-                // a row that reads nothing takes row 0: its output is scaled by 0 or not stored
-                const int row = (r < half && rr < t.rows) ? max(0, source_row(a, t.e, t.begin, t.first + rr)) : 0;
-                src[i] = a.x + (size_t)row * a.Kd + chunk * 16;
-            }
+            for (int i = 0; i < kPer; ++i)
+                src[i] = a.x + (size_t)sh->source[u % kUnitSlots][r0 + i * 8] * a.Kd + chunk * 16;
             for (int kb = kb0; kb < kb1; ++kb, ++c) {
                 const uint32_t s = c % kXStages;
                 ok = mbar_wait_warp(sh, &sh->x_empty[s], (c / kXStages & 1) ^ 1);
@@ -696,7 +690,29 @@ matmul_tc_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map) {
         const bool vectors = KS == 1 && a.out_bf16 && a.Nc % 8 == 0;  // rows of out start on 16 bytes
         const int size = a.out_bf16 ? 2 : 4;
         const size_t pitch = (size_t)a.Nc * size;
+        Steps<S> steps(a, cluster + warp * clusters, kOutWarps * clusters);
+        const auto publish = [&](uint32_t u) {
+            const int4 packed = steps.next(a, sh);
+            const Unit t = unpack<S>(packed);
+            const int half = t.n / CG;
+#pragma unroll
+            for (int i = 0; i < S::kRows; i += 32) {
+                // a row that reads nothing takes row 0: its output is scaled by 0 or not stored
+                const int r = i + lane, rr = rank * half + r;
+                if (S::kRows % 32 == 0 || r < S::kRows)
+                    sh->source[u % kUnitSlots][r] =
+                        r < half && rr < t.rows ? max(0, source_row(a, t.e, t.begin, t.first + rr)) : 0;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                sh->unit[u % kUnitSlots] = packed;
+                mbar_arrive(&sh->unit_full[u % kUnitSlots]);
+            }
+            __syncwarp();
+        };
+        if (warp < units) publish(warp);
         for (uint32_t u = 0; u < units; ++u) {
+            if (u % kOutWarps == warp && units - u > kOutWarps) publish(u + kOutWarps);
             Unit t;
             if (!get_unit<S>(sh, u, t)) break;
             const uint32_t acc = u % kAcc;
