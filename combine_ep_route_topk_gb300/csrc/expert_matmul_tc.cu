@@ -27,11 +27,12 @@
 // writes status 1, waits for its own copies and MMAs and frees its TMEM.
 //
 // What bounds it: with few rows per expert the weights' bytes (32 experts of
-// 4096 x 7168, 8 rows each: 149 us = 6.3 TB/s of the 6.7 that a copy reaches),
-// with many the tensor cores (1024 rows each: 1.00 ms = 1.92 PFLOP/s, where a
-// large library product of bf16 reaches 1.95; 1.76 M cycles, of which the MMAs
-// take 1.55 M).  In between, and with short rows of x, the ring: a stage is
-// widened (about 700 cycles after it is free), multiplied and handed back.
+// 4096 x 7168, 8 rows each: 150 us = 6.3 TB/s of the 6.7 that a copy reaches),
+// with many the tensor cores (1024 rows each: 0.98 ms = 1.96 PFLOP/s, where a
+// large library product of bf16 reaches 1.95; 1.72 M cycles, of which the MMAs
+// take 1.55 M).  In between, shared memory (205 rows a tile: 110 to 136 KB a
+// block and CTA, about 1000 of its 1150 cycles; the MMAs take 820) and, where K
+// is short, a tile's start and end.
 #include <cuda.h>
 
 #include <algorithm>
@@ -948,7 +949,7 @@ namespace {
 // Cycles that a shape would take, by the waves of its tiles.  A block of K takes
 // `base` cycles and `slope` more for each row of the tile (measured; the weights
 // arrive, are widened and multiplied), a tile's start and end 3000, sums that are
-// joined 6500 more.  The counts of several experts scatter around their mean as
+// joined 6500 more, the launch of pairs 2000 more.  The counts of several experts scatter around their mean as
 // independent picks would, which decides whether an expert needs one tile more;
 // one expert's count and a capacity are taken as they are.
 template <class S>
@@ -964,7 +965,7 @@ double shape_cycles(const MatmulArgs& a, double base, double slope) {
     const double rows = std::min((double)S::TN, std::max(1.0, mean / tiles));
     const double blocks = std::ceil(std::ceil(a.Kd / (double)kBK) / S::KS);
     const double waves = std::ceil(all * std::ceil(a.Nc / (double)S::kChannels) / (sm_count() / S::kCluster));
-    return waves * (blocks * (base + slope * rows) + (S::KS > 1 ? 9500.0 : 3000.0));
+    return waves * (blocks * (base + slope * rows) + (S::KS > 1 ? 9500.0 : 3000.0)) + (S::CG > 1 ? 2000.0 : 0.0);
 }
 
 }  // namespace
@@ -975,10 +976,10 @@ double shape_cycles(const MatmulArgs& a, double base, double slope) {
 // few tiles K is divided among CTAs.  The shape with the least estimated cycles
 // is taken.  Measured on a GB300 (us; counts drawn around their mean) with
 // TN = 64, 160, 256:
-//   32 experts of 4096 x 7168: mean 8 147, 151, 192; 64 214, 168, 215;
-//     128 361, 186, 233; 160 445, 266, 244; 320 799, 420, 439; 512 1244, 663, 564
-//   128 experts of 2880 x 1440: mean 8 98, 116, 140; 64 157, 130, 156;
-//     128 260, 146, 171; 200 389, 249, 196; 512 905, 505, 449
+//   32 experts of 4096 x 7168: mean 8 150, 153, 184; 64 211, 167, 208;
+//     128 355, 187, 228; 160 435, 265, 239; 320 779, 423, 420; 512 1214, 682, 559
+//   128 experts of 2880 x 1440: mean 8 94, 104, 120; 64 147, 117, 137;
+//     128 240, 136, 157; 200 355, 237, 187; 512 819, 503, 436
 // and with K whole, in 2 and in 4 parts:
 //   1 expert of 4096 x 4096: 8 rows 15.6, 13.6, 12.3; 64 rows 18.0, 15.4, 13.4
 //   4 experts of 4096 x 4096, 64 rows: 18.2, 22.4, 28.6
