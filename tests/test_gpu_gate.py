@@ -107,6 +107,35 @@ def test_gate_ties_go_to_the_lower_id(score, bias, E, groups):
         assert np.array_equal(idx[t].cpu().numpy(), rid), t
 
 
+WIDE = [(160, 6, 8), (160, 16, 8), (144, 6, 8), (129, 4, 3), (150, 8, 1), (257, 1, 1), (300, 5, 1), (384, 8, 8),
+        (384, 8, 1), (384, 12, 6), (385, 8, 5), (512, 7, 16), (512, 9, 1), (640, 8, 4), (1000, 8, 1), (1024, 3, 4)]
+
+
+@pytest.mark.parametrize("E,K,groups", WIDE)
+@pytest.mark.parametrize("score,bias,dtype", [(SIG, True, torch.float32), (SOFT, False, torch.bfloat16)])
+def test_gate_of_many_experts(E, K, groups, score, bias, dtype):
+    logits = make(41, E, dtype, seed=E + K, masked=0.02)
+    b = torch.randn(E, generator=torch.Generator().manual_seed(6)) * 0.1 if bias else None
+    tg = max(1, groups // 2)
+    idx, w = ep.ep_gate_topk(logits.cuda(), K, score, bias=None if b is None else b.cuda(), groups=groups,
+                             topk_groups=tg, group_top=2)
+    check(logits, K, score, b, groups, tg, 2, True, 1.0, idx, w)
+
+
+@pytest.mark.parametrize("E,K,groups", WIDE)
+def test_gate_of_many_experts_ties(E, K, groups):
+    """Equal keys within a lane and across lanes, in numbers beyond K; rows with fewer than K experts."""
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randint(0, 3, (24, E), generator=g).float()
+    logits[8:16] = 1.0
+    logits[16:][torch.rand(8, E, generator=g) < 0.99] = float("-inf")
+    tg = max(1, groups // 2)
+    idx, w = ep.ep_gate_topk(logits.cuda(), K, SIG, groups=groups, topk_groups=tg, group_top=2)
+    for t in range(24):
+        rid, _, _ = ref.gate_row(logits[t].double().numpy(), K, False, None, groups, tg, 2, True, 1.0)
+        assert np.array_equal(idx[t].cpu().numpy(), rid), t
+
+
 @pytest.mark.parametrize("score", [SIG, SOFT])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("groups", [1, 4])
