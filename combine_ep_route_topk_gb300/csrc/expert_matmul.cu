@@ -141,12 +141,14 @@ matmul_rows_kernel(MatmulArgs a) {
 cudaError_t launch_expert_matmul(const MatmulArgs& a, cudaStream_t s) {
     if (a.rows == 0)
         return a.status != nullptr ? cudaMemsetAsync(a.status, 0, sizeof(int32_t), s) : cudaSuccess;
-    // Few rows, most of them alone with their expert: this kernel.  32 experts of
-    // 4096 x 7168: 8 rows 40 us (tensor cores 49), 12 rows 65 (65), 16 rows 79
-    // (69); 128 experts of 2880 x 1440: 32 rows 26 (35), 64 rows 40 (50), 128
-    // rows 79 (78); one expert of 4096 x 4096: 4 rows 12 (15), 8 rows 22 (15).
+    // Few rows, most of them alone with their expert: this kernel.  Rows alone with
+    // their expert (tensor cores in brackets), 32 experts of 4096 x 7168: 8 rows
+    // 41 us (48), 16 rows 78 (87); 128 experts of 2880 x 1440: 32 rows 28 (34), 64
+    // rows 50 (60).  Rows that pick independently: 12 of 32 56 (49), 16 of 32 72
+    // (68), 32 of 32 102 (88), 64 of 128 53 (49), 32 of 128 25 (28).  One expert
+    // of 4096 x 4096: 2 rows 8 (12), 4 rows 12 (12), 5 rows 22 (12).
     cudaError_t err;
-    if (a.x_rows == 0 || a.rows <= 4 || 5ll * a.rows <= 2ll * a.E) {
+    if (a.x_rows == 0 || a.rows <= 4 || 2ll * a.rows <= a.E) {
         err = launch(matmul_rows_kernel, dim3(sm_count() * kBlocksPerSm), dim3(kWarps * 32), 0, s, a);
     } else {
         err = launch_matmul_tc(a, s);
