@@ -154,7 +154,7 @@ cudaError_t launch_shape(const QuantArgs& a, cudaStream_t s) {
 }
 
 // Measured on a GB300 (bf16, us; floor at the measured copy rate): 32768 x 7168
-// 108.7 (105); SwiGLU 32768 x 2048 58.2 (50), with 64 and 256 threads a row
+// 108.7 (105); SwiGLU 32768 x 2048 53.2 (50), with 64 and 256 threads a row
 // 61.4 and 64.6; 65536 x 1024 28.0 (30) with a warp a row, 66.3 with 128
 // threads (a block a nanosecond is what the chip starts), but one token's 8 rows
 // 2.7 against 1.5.
