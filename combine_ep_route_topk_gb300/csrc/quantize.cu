@@ -11,6 +11,8 @@
 // the scale are float32; the code is the only rounding to fewer bits.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "ep_kernels.cuh"
 
 namespace ep {
@@ -78,15 +80,16 @@ __device__ __forceinline__ bool holds_token(const QuantArgs& a, long long r) {
     return slot < __ldg(a.expert_offsets + e + 1) - __ldg(a.expert_offsets + e);
 }
 
-// NT threads per row and ROWS rows per block (ROWS > 1: a warp each); HELD > 0:
-// the row fits HELD vectors of 8 a thread, held in registers; HELD == 0: any
-// length, the values computed twice.
+// Up to NT threads per row, whole warps, and ROWS rows per block (ROWS > 1: a warp
+// each); HELD > 0: the row fits HELD vectors of 8 a thread, held in registers;
+// HELD == 0: any length, the values computed twice.
 template <typename T, bool SWIGLU, int NT, int ROWS, int HELD>
 __global__ void __launch_bounds__(NT * ROWS) quantize_kernel(QuantArgs a) {
     static_assert(ROWS == 1 || NT == 32, "a warp per row");
     pdl_prologue();
-    const int tid = threadIdx.x % NT;
-    const long long r = (long long)blockIdx.x * ROWS + threadIdx.x / NT;
+    const int nt = ROWS > 1 ? NT : (int)blockDim.x;  // threads of a row
+    const int tid = ROWS > 1 ? (int)threadIdx.x % NT : (int)threadIdx.x;
+    const long long r = (long long)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / NT : 0);
     if (r >= a.rows || !holds_token(a, r)) return;  // uniform over the row's threads
     const int wide = SWIGLU ? 2 * a.cols : a.cols;
     const T* row = static_cast<const T*>(a.x) + r * wide;
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(NT * ROWS) quantize_kernel(QuantArgs a) {
     if constexpr (HELD > 0) {
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            const int c = (i * NT + tid) * 8;
+            const int c = (i * nt + tid) * 8;
             if (c < a.cols) {
                 values8<T, SWIGLU>(row, a.cols, c, v[i]);
             } else {
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(NT * ROWS) quantize_kernel(QuantArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
     } else {
-        for (int c = tid * 8; c < a.cols; c += NT * 8) {
+        for (int c = tid * 8; c < a.cols; c += nt * 8) {
             values8<T, SWIGLU>(row, a.cols, c, v[0]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[0][j]));
@@ -124,7 +127,8 @@ __global__ void __launch_bounds__(NT * ROWS) quantize_kernel(QuantArgs a) {
         if ((tid & 31) == 0) s_max[tid >> 5] = top;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, s_max[w]);
+        for (int w = 0; w < NT / 32; ++w)
+            if (w * 32 < nt) top = fmaxf(top, s_max[w]);
     }
     // a row whose largest value is below 1e-30 is scaled up first: 127 / top would
     // leave the range of a float32
@@ -134,12 +138,12 @@ __global__ void __launch_bounds__(NT * ROWS) quantize_kernel(QuantArgs a) {
     if constexpr (HELD > 0) {
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            const int c = (i * NT + tid) * 8;
+            const int c = (i * nt + tid) * 8;
             if (up != 1.0f) scale8(v[i], up);  // uniform over the row
             if (c < a.cols) store8(out + c, v[i], inv);
         }
     } else {
-        for (int c = tid * 8; c < a.cols; c += NT * 8) {
+        for (int c = tid * 8; c < a.cols; c += nt * 8) {
             values8<T, SWIGLU>(row, a.cols, c, v[0]);
             if (up != 1.0f) scale8(v[0], up);
             store8(out + c, v[0], inv);
@@ -149,20 +153,26 @@ __global__ void __launch_bounds__(NT * ROWS) quantize_kernel(QuantArgs a) {
 
 template <typename T, bool SWIGLU, int NT, int ROWS, int HELD>
 cudaError_t launch_shape(const QuantArgs& a, cudaStream_t s) {
+    const int vectors = (a.cols + 7) / 8, held = HELD > 0 ? HELD : 1;
+    const int nt = ROWS > 1 ? NT : std::min(NT, ((vectors + held - 1) / held + 31) / 32 * 32);
     return launch(quantize_kernel<T, SWIGLU, NT, ROWS, HELD>, dim3((unsigned)((a.rows + ROWS - 1ll) / ROWS)),
-                  dim3(NT * ROWS), 0, s, a);
+                  dim3(nt * ROWS), 0, s, a);
 }
 
 // Measured on a GB300 (bf16, us; floor at the measured copy rate): 32768 x 7168
-// 108.7 (105); SwiGLU 32768 x 2048 53.2 (50), with 64 and 256 threads a row
-// 61.4 and 64.6; 65536 x 1024 28.0 (30) with a warp a row, 66.3 with 128
-// threads (a block a nanosecond is what the chip starts), but one token's 8 rows
-// 2.7 against 1.5.
+// 105.6 (105), with 256 threads for its 224 x 4 vectors 111.2; 8192 x 9216 36.9
+// (34), with 512 threads for 288 54.8; SwiGLU 32768 x 2048 53.8 (50), with 64 and
+// 256 threads a row 59.1 and 56.2.  A warp a row: 65536 x 1024 28.1 (30), with
+// 128 threads 66.1 (a block a nanosecond is what the chip starts); 32768 x 1440
+// 19.5 (21), with 96 threads 33.3, but SwiGLU of 65536 x 1440 97.7 against 78.4
+// (71), and one token's 8 rows 2.1 against 1.5.
 template <typename T, bool SWIGLU>
 cudaError_t launch_quantize_t(const QuantArgs& a, cudaStream_t s) {
     if (a.cols <= 256) return launch_shape<T, SWIGLU, 32, 8, 1>(a, s);
     if (a.cols <= 512) return launch_shape<T, SWIGLU, 32, 8, 2>(a, s);
     if (a.cols <= 1024 && a.rows >= 4096) return launch_shape<T, SWIGLU, 32, 4, 4>(a, s);
+    if constexpr (!SWIGLU)
+        if (a.cols <= 1536 && a.rows >= 4096) return launch_shape<T, SWIGLU, 32, 4, 6>(a, s);
     if (a.cols <= 1024) return launch_shape<T, SWIGLU, 128, 1, 1>(a, s);
     if (a.cols <= 2048) return launch_shape<T, SWIGLU, 128, 1, 2>(a, s);
     if (a.cols <= 4096) return launch_shape<T, SWIGLU, 256, 1, 2>(a, s);

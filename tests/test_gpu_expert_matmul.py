@@ -52,6 +52,22 @@ def test_quantize_against_plain(rows, cols, dtype, act):
     assert (q[zero] == 0).all() and (s[zero] == 1).all()
 
 
+@pytest.mark.parametrize("act", [ep.EP_ACT_NONE, ep.EP_ACT_SWIGLU])
+@pytest.mark.parametrize("rows,cols", [(4096, 512), (4099, 528), (4097, 1056), (4098, 1440), (4096, 1536), (4096, 1552),
+                                       (2, 272), (2, 1440), (2, 2576), (2, 4112), (2, 5136), (2, 9216), (2, 16384)])
+def test_quantize_block_shapes(rows, cols, act):
+    """Lengths that leave threads or vectors of a block idle, by a warp and by a block a row."""
+    x = rows_of(rows, 2 * cols if act == ep.EP_ACT_SWIGLU else cols, torch.bfloat16, cols)
+    q, s = ep.ep_quantize_rows(x.cuda(), act=act)
+    v = x.double().numpy()
+    if act == ep.EP_ACT_SWIGLU:
+        v = ref.swiglu(v)
+    want, scale = ref.quantize(v)
+    ok = np.abs(v).max(1) > 1e-30
+    np.testing.assert_allclose(s.double().cpu().numpy()[ok], scale[ok], rtol=SCALE_RTOL)
+    assert np.abs(q.double().cpu().numpy()[ok] - want[ok]).max() <= CODE_TOL
+
+
 def test_quantize_rounds_ties_to_even():
     x = torch.zeros((1, 32))
     x[0, 0] = 127.0
