@@ -165,7 +165,8 @@ cudaError_t launch_shape(const QuantArgs& a, cudaStream_t s) {
 // 256 threads a row 59.1 and 56.2.  A warp a row: 65536 x 1024 28.1 (30), with
 // 128 threads 66.1 (a block a nanosecond is what the chip starts); 32768 x 1440
 // 19.5 (21), with 96 threads 33.3, but SwiGLU of 65536 x 1440 97.7 against 78.4
-// (71), and one token's 8 rows 2.1 against 1.5.
+// (71), and one token's 8 rows 2.1 against 1.5.  Four vectors a thread: 32768 x
+// 4096 59.5 (60), with two 70.3, but SwiGLU of them 118.0 against 111.8 (100).
 template <typename T, bool SWIGLU>
 cudaError_t launch_quantize_t(const QuantArgs& a, cudaStream_t s) {
     if (a.cols <= 256) return launch_shape<T, SWIGLU, 32, 8, 1>(a, s);
@@ -175,6 +176,8 @@ cudaError_t launch_quantize_t(const QuantArgs& a, cudaStream_t s) {
         if (a.cols <= 1536 && a.rows >= 4096) return launch_shape<T, SWIGLU, 32, 4, 6>(a, s);
     if (a.cols <= 1024) return launch_shape<T, SWIGLU, 128, 1, 1>(a, s);
     if (a.cols <= 2048) return launch_shape<T, SWIGLU, 128, 1, 2>(a, s);
+    if constexpr (!SWIGLU)
+        if (a.cols <= 4096 && a.rows >= 4096) return launch_shape<T, SWIGLU, 128, 1, 4>(a, s);
     if (a.cols <= 4096) return launch_shape<T, SWIGLU, 256, 1, 2>(a, s);
     if (a.cols <= 8192) return launch_shape<T, SWIGLU, 256, 1, 4>(a, s);
     if (a.cols <= 16384) return launch_shape<T, SWIGLU, 512, 1, 4>(a, s);

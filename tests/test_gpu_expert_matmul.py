@@ -53,7 +53,7 @@ def test_quantize_against_plain(rows, cols, dtype, act):
 
 
 @pytest.mark.parametrize("act", [ep.EP_ACT_NONE, ep.EP_ACT_SWIGLU])
-@pytest.mark.parametrize("rows,cols", [(4096, 512), (4099, 528), (4097, 1056), (4098, 1440), (4096, 1536), (4096, 1552),
+@pytest.mark.parametrize("rows,cols", [(4096, 512), (4099, 528), (4097, 1056), (4098, 1440), (4096, 1536), (4096, 1552), (4096, 2064), (4100, 2880),
                                        (2, 272), (2, 1440), (2, 2576), (2, 4112), (2, 5136), (2, 9216), (2, 16384)])
 def test_quantize_block_shapes(rows, cols, act):
     """Lengths that leave threads or vectors of a block idle, by a warp and by a block a row."""
