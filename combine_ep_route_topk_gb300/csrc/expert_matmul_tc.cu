@@ -956,16 +956,22 @@ template <class S>
 double shape_cycles(const MatmulArgs& a, double base, double slope) {
     const double mean = a.layout == 0 ? (double)a.rows / a.E : a.cap;
     const double sigma = a.layout == 0 && a.E > 1 ? std::sqrt(mean) : 0.0;
-    // An expert's tiles: one more for each multiple of TN that its count exceeds.
-    double tiles = std::max(1.0, sigma == 0.0 ? std::ceil(mean / S::TN) : std::floor((mean - 4.0 * sigma) / S::TN));
-    for (int k = (int)tiles; sigma > 0.0 && k * (double)S::TN < mean + 4.0 * sigma; ++k)
-        tiles += 0.5 * std::erfc((k * S::TN - mean) / (sigma * std::sqrt(2.0)));
-    double all = a.E * tiles;
-    if (a.layout == 0) all = std::min(all, std::min(a.E, a.rows) + std::floor((double)a.rows / S::TN));
-    const double rows = std::min((double)S::TN, std::max(1.0, mean / tiles));
+    // An expert's tiles: those that it has for sure, and one more for each multiple
+    // of TN that its count may exceed.
+    const double sure = std::max(1.0, sigma == 0.0 ? std::ceil(mean / S::TN) : std::floor((mean - 4.0 * sigma) / S::TN));
+    double more = 0.0;
+    for (int k = (int)sure; sigma > 0.0 && k * (double)S::TN < mean + 4.0 * sigma; ++k)
+        more += 0.5 * std::erfc((k * S::TN - mean) / (sigma * std::sqrt(2.0)));
+    const double rows = std::min((double)S::TN, std::max(1.0, mean / (sure + more)));
+    const double most = a.layout == 0 ? std::min(a.E, a.rows) + std::floor((double)a.rows / S::TN) : a.E * sure;
+    const double tiles = std::min(a.E * sure, most), extra = std::min(a.E * more, most - tiles);
+    const auto waves = [&](double t) {
+        return std::ceil(t * std::ceil(a.Nc / (double)S::kChannels) / (sm_count() / S::kCluster));
+    };
+    // less than one tile more is the chance of one
+    const double all = extra < 1.0 ? waves(tiles) + extra * (waves(tiles + 1.0) - waves(tiles)) : waves(tiles + extra);
     const double blocks = std::ceil(std::ceil(a.Kd / (double)kBK) / S::KS);
-    const double waves = std::ceil(all * std::ceil(a.Nc / (double)S::kChannels) / (sm_count() / S::kCluster));
-    return waves * (blocks * (base + slope * rows) + (S::KS > 1 ? 9500.0 : 3000.0)) + (S::CG > 1 ? 2000.0 : 0.0);
+    return all * (blocks * (base + slope * rows) + (S::KS > 1 ? 9500.0 : 3000.0)) + (S::CG > 1 ? 2000.0 : 0.0);
 }
 
 }  // namespace
@@ -980,6 +986,7 @@ double shape_cycles(const MatmulArgs& a, double base, double slope) {
 //     128 355, 187, 228; 160 435, 265, 239; 320 779, 423, 420; 512 1214, 682, 559
 //   128 experts of 2880 x 1440: mean 8 94, 104, 120; 64 147, 117, 137;
 //     128 240, 136, 157; 200 355, 237, 187; 512 819, 503, 436
+//   19 experts of 4096 x 7168, 128 rows each (4 whole waves of 160): 175, 109, 136
 // and with K whole, in 2 and in 4 parts:
 //   1 expert of 4096 x 4096: 8 rows 15.6, 13.6, 12.3; 64 rows 18.0, 15.4, 13.4
 //   4 experts of 4096 x 4096, 64 rows: 18.2, 22.4, 28.6

@@ -20,8 +20,8 @@
 // full accuracy, for the picks alone; the choice uses the hardware's exp2 and
 // reciprocal (an absolute error below 3e-7 in a score of at most 1).
 //
-// What bounds it: instructions (575 a token of 256 experts with bias and groups;
-// 76 % of the issue slots): 32768 tokens of float32, 33.6 MB, take 18.9 us where
+// What bounds it: instructions (534 a token of 256 experts with bias and groups;
+// 75 % of the issue slots): 32768 tokens of float32, 33.6 MB, take 18.9 us where
 // the bytes alone would take 5; one token 2.0 us.  The gradient (same sizes, 8
 // picks a token) takes 11.2 us for its 33.5 MB of stores, 7.3 when they stay in
 // L2, and 11.6 where every expert gets one (softmax, not renormalised).
