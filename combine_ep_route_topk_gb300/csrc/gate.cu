@@ -20,9 +20,11 @@
 // full accuracy, for the picks alone; the choice uses the hardware's exp2 and
 // reciprocal (an absolute error below 3e-7 in a score of at most 1).
 //
-// What bounds it: instructions (534 a token of 256 experts with bias and groups;
-// 75 % of the issue slots): 32768 tokens of float32, 33.6 MB, take 18.9 us where
-// the bytes alone would take 5; one token 2.0 us.  The gradient (same sizes, 8
+// What bounds it: instructions (517 a token of 256 experts with bias and groups;
+// 74 % of the issue slots): 32768 tokens of float32, 33.6 MB, take 17.0 us where
+// the bytes alone would take 5; one token 2.2 us.  Rows of finite numbers skip
+// the tests for others and picks without equals in their lane the count of them
+// (18.8 us with neither, and 15.3 against 12.3 for a softmax in one group).  The gradient (same sizes, 8
 // picks a token) takes 11.2 us for its 33.5 MB of stores, 7.3 when they stay in
 // L2, and 11.6 where every expert gets one (softmax, not renormalised).
 #include <cuda_bf16.h>
@@ -223,11 +225,12 @@ __device__ __forceinline__ int groups_before(float best, float second, int lane,
 }
 
 // KT > 0: K == KT, or for more than 8 experts a lane K <= KT, which lets a lane
-// keep its KT largest keys alone (8192 tokens of 1024 experts 27.3 -> 22.3 us).
+// keep its KT largest keys alone (8192 tokens of 1024 experts 27.3 -> 22.1 us).
 template <int VPL, typename T, int KT>
 __global__ void __launch_bounds__(kGateWarps * 32)
 gate_kernel(GateArgs a) {
     extern __shared__ float s_choice[];  // [warps][E], only for groups that cross lanes unevenly
+    __shared__ float2 s_pick[kGateWarps][32];  // a pick's key and the lane that gave it
     pdl_prologue();
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
@@ -244,6 +247,17 @@ gate_kernel(GateArgs a) {
     load_row<VPL>(row, E, a.vec != 0, lane, v);
     if (a.bias != nullptr) {
         load_row<VPL>(a.bias, E, a.bias_vec != 0, lane, bias);
+    }
+    // Whether every logit and bias of the row is finite: 0 x is NaN otherwise (on
+    // another pipe than the comparisons that are spared then).
+    float zero = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        zero = fmaf(v[j], 0.0f, zero);
+        if (a.bias != nullptr) zero = fmaf(bias[j], 0.0f, zero);
+    }
+    const bool finite = __all_sync(kFull, zero == 0.0f);
+    if (a.bias != nullptr && !finite) {
 #pragma unroll
         for (int j = 0; j < VPL; ++j) bias[j] = fmaxf(bias[j], -INFINITY);  // NaN: not available
     }
@@ -252,9 +266,14 @@ gate_kernel(GateArgs a) {
     float m = 0.0f, total = 1.0f;
     if (!sigmoids) {
         m = -INFINITY;
+        if (finite) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
-            if (available(v[j])) m = fmaxf(m, clamp_logit(v[j]));
+            for (int j = 0; j < VPL; ++j) m = fmaxf(m, v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (available(v[j])) m = fmaxf(m, clamp_logit(v[j]));
+        }
         m = redux_max(m);
         if (a.bias != nullptr || groups_sum || !a.renorm) {
             float sum = 0.0f;
@@ -270,19 +289,23 @@ gate_kernel(GateArgs a) {
     float key[VPL];
     if (a.bias == nullptr) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) key[j] = available(v[j]) ? clamp_logit(v[j]) : -INFINITY;
+        for (int j = 0; j < VPL; ++j) key[j] = v[j];
+        if (!finite) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) key[j] = clamp_logit(v[j]);
+        }
     } else if (sigmoids) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {  // a sigmoid of +inf is 1 without a clamp
-            const float x = rcp_fast(1.0f + exp2_fast(v[j] * -kLog2e)) + bias[j];
-            key[j] = available(v[j]) ? x : -INFINITY;
-        }
+        for (int j = 0; j < VPL; ++j)  // a sigmoid of +inf is 1 without a clamp
+            key[j] = rcp_fast(1.0f + exp2_fast(v[j] * -kLog2e)) + bias[j];
     } else {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const float x = exp2_fast((clamp_logit(v[j]) - m) * kLog2e) * inv_total + bias[j];
-            key[j] = available(v[j]) ? x : -INFINITY;
-        }
+        for (int j = 0; j < VPL; ++j)
+            key[j] = exp2_fast((clamp_logit(v[j]) - m) * kLog2e) * inv_total + bias[j];
+    }
+    if (!finite) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) key[j] = available(v[j]) ? key[j] : -INFINITY;
     }
     // a group's score from its two largest keys
     const auto group_score = [&](float best, float second) {
@@ -351,18 +374,13 @@ gate_kernel(GateArgs a) {
         }
     }
 
-    float my_top = -INFINITY;
-    unsigned my_heads = 1u;  // lanes whose head was the pick: the lowest gave it
 #pragma unroll(KT > 0 ? KT : 1)
     for (int k = 0; k < (KT > 0 ? KT : K); ++k) {
         if (k >= K) break;
         const float top = redux_max(list[0]);
         const unsigned heads = __ballot_sync(kFull, list[0] == top);
-        if (lane == k) {
-            my_top = top;
-            my_heads = heads;
-        }
-        if (list[0] == top && (heads & lower) == 0u) {
+        if (list[0] == top && (heads & lower) == 0u) {  // the lowest of the lanes that hold it
+            s_pick[warp][k] = make_float2(top, __int_as_float(lane));
 #pragma unroll
             for (int j = 0; j + 1 < L; ++j)
                 if (KT == 0 || j < KT - 1 - k) list[j] = list[j + 1];
@@ -371,16 +389,31 @@ gate_kernel(GateArgs a) {
     }
     // Pick k is the (same + 1)-th of its lane's experts with this key, where
     // `same` picks right before it have the same key and lane.
-    const int my_lane = __ffs(my_heads) - 1;
+    __syncwarp();
+    float my_top = -INFINITY;
+    int my_lane = 0;
+    if (lane < K) {
+        const float2 pick = s_pick[warp][lane];
+        my_top = pick.x;
+        my_lane = __float_as_int(pick.y);
+    }
     const float up_top = __shfl_up_sync(kFull, my_top, 1);
     const int up_lane = __shfl_up_sync(kFull, my_lane, 1);
     const unsigned rest = ~__ballot_sync(kFull, lane > 0 && up_top == my_top && up_lane == my_lane);
     int same = lane - (31 - __clz(rest & (0xffffffffu >> (31 - lane))));
     int my_id = -1;
+    if (__any_sync(kFull, lane < K && same > 0)) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-        const float x = __shfl_sync(kFull, key[j], my_lane);
-        if (x == my_top && same-- == 0) my_id = my_lane * VPL + j;
+        for (int j = 0; j < VPL; ++j) {
+            const float x = __shfl_sync(kFull, key[j], my_lane);
+            if (x == my_top && same-- == 0) my_id = my_lane * VPL + j;
+        }
+    } else {  // the usual case: the lowest that has it
+#pragma unroll
+        for (int j = VPL - 1; j >= 0; --j) {
+            const float x = __shfl_sync(kFull, key[j], my_lane);
+            if (x == my_top) my_id = my_lane * VPL + j;
+        }
     }
     if (lane >= K || !(my_top > -INFINITY)) my_id = -1;
 
