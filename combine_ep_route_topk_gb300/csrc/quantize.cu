@@ -3,7 +3,8 @@
 //
 //   v_c   = x_c, or x_c / (1 + exp(-x_c)) * x_{c+cols}
 //   scale = max_c |v_c| / 127      (1 for a row of zeros)
-//   q_c   = round-to-nearest-even(v_c * (127 / max|v|))
+//   q_c   = round-to-nearest-even(v_c * (127 / max|v|)), quotient and product
+//           each rounded to float32
 //
 // One pass over the row: a block (a warp for short rows) holds its values in
 // registers, reduces the maximum and writes the codes, so the bytes moved are
@@ -55,11 +56,24 @@ __device__ __forceinline__ void values8(const T* row, int cols, int c, float (&v
 }
 
 // Four codes: with 1.5 * 2^23 added, a float32 of magnitude up to 127 is rounded
-// to the nearest integer (ties to even), which is its lowest byte.
+// to the nearest integer (ties to even), which is its lowest byte.  The product is
+// rounded to float32 first: in one fused step the error of inv would decide the
+// products that lie exactly between two codes (0.07 % of the codes of bf16 rows).
+// Products are taken two an instruction, sums one by one: a sum of two would be
+// fused with them.  32768 x 7168 bf16: 106.7 us as in one step, 109.6 with single
+// products.
+__device__ __forceinline__ void codes2(float x, float y, float inv, uint32_t& a, uint32_t& b) {
+    float p, q;
+    asm("{\n.reg .b64 v, f;\nmov.b64 v, {%2, %3};\nmov.b64 f, {%4, %4};\n"
+        "mul.rn.f32x2 v, v, f;\nmov.b64 {%0, %1}, v;\n}\n"
+        : "=f"(p), "=f"(q) : "f"(x), "f"(y), "f"(inv));
+    a = __float_as_uint(__fadd_rn(p, 12582912.0f));
+    b = __float_as_uint(__fadd_rn(q, 12582912.0f));
+}
 __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
-    constexpr float kMagic = 12582912.0f;
-    const uint32_t a = __float_as_uint(fmaf(v[0], inv, kMagic)), b = __float_as_uint(fmaf(v[1], inv, kMagic));
-    const uint32_t c = __float_as_uint(fmaf(v[2], inv, kMagic)), d = __float_as_uint(fmaf(v[3], inv, kMagic));
+    uint32_t a, b, c, d;
+    codes2(v[0], v[1], inv, a, b);
+    codes2(v[2], v[3], inv, c, d);
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
