@@ -2,7 +2,8 @@
 // (ep_quantize_rows), optionally of the SwiGLU of a row's two halves.
 //
 //   v_c   = x_c, or x_c / (1 + exp(-x_c)) * x_{c+cols}
-//   scale = max_c |v_c| / 127      (1 for a row of zeros)
+//   scale = max_c |v_c| / 127      (1 for a row of zeros; not finite, with codes
+//           of 0, where a v is not: the products of such a row are NaN)
 //   q_c   = round-to-nearest-even(v_c * (127 / max|v|)), quotient and product
 //           each rounded to float32
 //
@@ -13,6 +14,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "ep_kernels.cuh"
 
@@ -86,6 +88,13 @@ __device__ __forceinline__ void scale8(float (&v)[8], float f) {
     for (int j = 0; j < 8; ++j) v[j] *= f;
 }
 
+// The larger one; NaN where either is, so that a NaN reaches the row's scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
 // Whether row r holds a token.
 __device__ __forceinline__ bool holds_token(const QuantArgs& a, long long r) {
     if (a.expert_offsets == nullptr) return true;
@@ -125,30 +134,34 @@ __global__ void __launch_bounds__(NT * ROWS) quantize_kernel(QuantArgs a) {
 #pragma unroll
         for (int i = 0; i < H; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
+            for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(v[i][j]));
     } else {
         for (int c = tid * 8; c < a.cols; c += nt * 8) {
             values8<T, SWIGLU>(row, a.cols, c, v[0]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[0][j]));
+            for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(v[0][j]));
         }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
     if constexpr (NT > 32) {
         __shared__ float s_max[NT / 32];
         if ((tid & 31) == 0) s_max[tid >> 5] = top;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < NT / 32; ++w)
-            if (w * 32 < nt) top = fmaxf(top, s_max[w]);
+            if (w * 32 < nt) top = max_nan(top, s_max[w]);
     }
     // a row whose largest value is below 1e-30 is scaled up first: 127 / top would
     // leave the range of a float32
     const float up = top < 1e-30f ? 0x1p96f : 1.0f;
     const float inv = top > 0.0f ? __fdiv_rn(127.0f, top * up) : 1.0f;
-    if (tid == 0) a.scales[r] = top > 0.0f ? __fdiv_rn(top, 127.0f) : 1.0f;
+    if (tid == 0) a.scales[r] = top == 0.0f ? 1.0f : __fdiv_rn(top, 127.0f);
+    if (!(top <= FLT_MAX)) {  // uniform over the row
+        for (int c = tid * 8; c < a.cols; c += nt * 8) *reinterpret_cast<uint2*>(out + c) = make_uint2(0, 0);
+        return;
+    }
     if constexpr (HELD > 0) {
 #pragma unroll
         for (int i = 0; i < H; ++i) {

@@ -395,7 +395,9 @@ ep_status_t ep_gate_topk_backward(const float* d_topk_w, const void* logits,
  *            rows of 2*cols: the experts' first product, gate half first).
  *   scale  = max|v| / 127 (1 for a row of zeros); q = v * (127 / max|v|), the
  *            quotient and the product each rounded to float32, then rounded to
- *            nearest even.  The rows hold finite values.
+ *            nearest even.  A row in which a v is NaN or infinite gets the
+ *            scale NaN or infinity and codes of 0, so that what
+ *            ep_expert_matmul makes of it is NaN.
  *   x      [rows, cols or 2*cols] float32 or bf16, 16-byte aligned.
  *   expert_offsets int32 [E+1] of the layout, or NULL for every row.  When
  *            given, rows that hold no token (CONTIG: from expert_offsets[E]
