@@ -400,6 +400,16 @@ ep_status_t ep_gate_topk(const void* logits, ep_dtype_t logits_dtype, int32_t N,
                          int32_t topk_groups, int32_t group_top, int32_t renorm, float scale,
                          const int32_t* expert_map, int32_t* topk_idx, float* topk_w,
                          void* stream) {
+    return ep_gate_topk_picks(logits, logits_dtype, N, E, K, score, bias, groups, topk_groups,
+                              group_top, renorm, scale, expert_map, topk_idx, topk_w, nullptr,
+                              stream);
+}
+
+ep_status_t ep_gate_topk_picks(const void* logits, ep_dtype_t logits_dtype, int32_t N, int32_t E,
+                               int32_t K, ep_score_t score, const float* bias, int32_t groups,
+                               int32_t topk_groups, int32_t group_top, int32_t renorm,
+                               float scale, const int32_t* expert_map, int32_t* topk_idx,
+                               float* topk_w, int32_t* picks, void* stream) {
     ep_status_t st = check_sizes(N, E, K);
     if (st != EP_OK) return st;
     if (logits_dtype != EP_DTYPE_F32 && logits_dtype != EP_DTYPE_BF16) return EP_ERR_INVALID_ARG;
@@ -412,7 +422,8 @@ ep_status_t ep_gate_topk(const void* logits, ep_dtype_t logits_dtype, int32_t N,
     if (N > 0 && (!logits || !topk_idx || !topk_w)) return EP_ERR_INVALID_ARG;
     const bool bf16 = logits_dtype == EP_DTYPE_BF16;
     if ((reinterpret_cast<uintptr_t>(logits) & (bf16 ? 1u : 3u)) != 0) return EP_ERR_INVALID_ARG;
-    if (!aligned4(bias) || !aligned4(expert_map) || !aligned4(topk_idx) || !aligned4(topk_w))
+    if (!aligned4(bias) || !aligned4(expert_map) || !aligned4(topk_idx) || !aligned4(topk_w) ||
+        !aligned4(picks))
         return EP_ERR_INVALID_ARG;
     GateArgs a;
     a.logits = logits;
@@ -420,6 +431,7 @@ ep_status_t ep_gate_topk(const void* logits, ep_dtype_t logits_dtype, int32_t N,
     a.emap = expert_map;
     a.topk_idx = topk_idx;
     a.topk_w = topk_w;
+    a.picks = picks;
     a.scale = scale;
     a.N = N;
     a.E = E;

@@ -177,6 +177,7 @@ struct GateArgs {
     const int32_t* emap;        // or nullptr
     int32_t* topk_idx;
     float* topk_w;
+    int32_t* picks;             // or nullptr: the ids before emap
     float scale;
     int N, E, K, score, groups, topk_groups, group_top, renorm;
     int bf16;

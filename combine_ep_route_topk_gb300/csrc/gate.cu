@@ -425,6 +425,7 @@ gate_kernel(GateArgs a) {
         s = sigmoids ? sigmoid(l) : expf(l - m) * inv_total;
     }
     if (lane < K) {
+        if (a.picks != nullptr) a.picks[(size_t)t * K + lane] = my_id;
         int id = my_id;
         if (id >= 0 && a.emap != nullptr) {
             id = __ldg(a.emap + id);

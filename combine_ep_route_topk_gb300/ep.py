@@ -89,12 +89,14 @@ def lib():
         f32, enum = ctypes.c_float, ctypes.c_int
         L.ep_gate_topk.argtypes = [P, enum, i32, i32, i32, enum, P, i32, i32, i32, i32, f32, P, P,
                                    P, P]
+        L.ep_gate_topk_picks.argtypes = [P, enum, i32, i32, i32, enum, P, i32, i32, i32, i32, f32,
+                                         P, P, P, P, P]
         L.ep_gate_topk_backward.argtypes = [P, P, enum, P, i32, i32, i32, enum, i32, f32, P, P, P]
         L.ep_quantize_rows.argtypes = [P, enum, enum, i32, i32, P, i32, enum, i32, P, P, P]
         L.ep_expert_matmul.argtypes = [P, P, i32, P, P, i32, i32, i32, P, enum, i32, i32, P, i32,
                                        enum, P, P, P]
-        for f in ("ep_gate_topk", "ep_gate_topk_backward", "ep_quantize_rows",
-                  "ep_expert_matmul"):
+        for f in ("ep_gate_topk", "ep_gate_topk_picks", "ep_gate_topk_backward",
+                  "ep_quantize_rows", "ep_expert_matmul"):
             getattr(L, f).restype = ctypes.c_int
         L.ep_status_string.argtypes = [ctypes.c_int]
         L.ep_status_string.restype = ctypes.c_char_p
@@ -375,31 +377,34 @@ def _float_type(t, name):
 
 def ep_gate_topk(logits, K, score=EP_SCORE_SOFTMAX, bias=None, groups=1, topk_groups=None,
                  group_top=2, renorm=True, scale=1.0, expert_map=None, topk_idx=None,
-                 topk_w=None, stream=None):
+                 topk_w=None, stream=None, picks=None):
     """logits bf16 or float32 [N, E] -> (topk_idx int32 [N, K], topk_w float32
     [N, K]): softmax or sigmoid scores, optional balance bias [E] on the choice
     alone, the best topk_groups of `groups` groups, the K best experts, their
-    scores (renormalised) times scale."""
+    scores (renormalised) times scale.  picks: int32 [N, K] that receives the
+    ids before expert_map, for ep_gate_topk_backward."""
     N, E = logits.shape
     dt = _float_type(logits, "logits")
     if topk_idx is None:
         topk_idx = _empty((N, K), torch.int32, logits)
     if topk_w is None:
         topk_w = _empty((N, K), torch.float32, logits)
-    _check("ep_gate_topk", lib().ep_gate_topk(
+    _check("ep_gate_topk", lib().ep_gate_topk_picks(
         _dev(logits, logits.dtype, "logits"), dt, N, E, K, score,
         _opt(bias, torch.float32, "bias", (E,)), groups,
         groups if topk_groups is None else topk_groups, group_top, int(renorm), scale,
         _opt(expert_map, torch.int32, "expert_map", (E,)),
         _dev(topk_idx, torch.int32, "topk_idx", (N, K)),
-        _dev(topk_w, torch.float32, "topk_w", (N, K)), _stream(stream)))
+        _dev(topk_w, torch.float32, "topk_w", (N, K)),
+        _opt(picks, torch.int32, "picks", (N, K)), _stream(stream)))
     return topk_idx, topk_w
 
 
 def ep_gate_topk_backward(d_topk_w, logits, topk_idx, score=EP_SCORE_SOFTMAX, renorm=True,
                           scale=1.0, expert_map=None, d_logits=None, stream=None):
     """Gradient of ep_gate_topk's weights: d_topk_w float32 [N, K] -> d_logits
-    [N, E] of the logits' type."""
+    [N, E] of the logits' type.  topk_idx: the forward call's picks; or, with
+    its expert_map, its topk_idx, where that map is a renumbering."""
     N, E = logits.shape
     K = topk_idx.shape[1]
     dt = _float_type(logits, "logits")

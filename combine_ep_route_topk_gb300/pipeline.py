@@ -273,6 +273,7 @@ class LayerBuffers:
     layout: int
     cap: int
     idx: torch.Tensor
+    picks: torch.Tensor         # idx before expert_map
     wt: torch.Tensor
     lay: _ep.Layout
     ws: torch.Tensor
@@ -294,7 +295,7 @@ def make_layer_buffers(N, E, K, H, inner, R, cap=0, device="cuda"):
     def z(shape, dtype):
         return torch.empty(shape, dtype=dtype, device=device)
     return LayerBuffers(
-        layout, cap, z((N, K), torch.int32), z((N, K), torch.float32),
+        layout, cap, z((N, K), torch.int32), z((N, K), torch.int32), z((N, K), torch.float32),
         _ep.alloc_layout(N, E, K, R, cap, device),
         z(_ep.ep_dispatch_layout_workspace_size(N, E, K, R), torch.uint8),
         z((N, H), torch.int8), z((N,), torch.float32), z((rows, 2 * inner), torch.bfloat16),
@@ -306,14 +307,14 @@ def expert_layer(x, logits, rank_offsets, weights, buf, score=_ep.EP_SCORE_SIGMO
                  groups=1, topk_groups=None, group_top=2, renorm=True, scale=1.0,
                  expert_map=None):
     """x bf16 [N, H], logits [N, E] -> buf.comb bf16 [N, H], on the current
-    stream.  The gate's arguments are ep_gate_topk's.  For training, buf.idx and
-    the gradient of buf.wt go to ep_gate_topk_backward."""
+    stream.  The gate's arguments are ep_gate_topk's.  For training, buf.picks and
+    the gradient of buf.wt go to ep_gate_topk_backward, without the map."""
     E = logits.shape[1]
     K = buf.idx.shape[1]
     lay, off = buf.lay, buf.lay.expert_offsets
     _ep.ep_gate_topk(logits, K, score, bias=bias, groups=groups, topk_groups=topk_groups,
                      group_top=group_top, renorm=renorm, scale=scale, expert_map=expert_map,
-                     topk_idx=buf.idx, topk_w=buf.wt)
+                     topk_idx=buf.idx, topk_w=buf.wt, picks=buf.picks)
     _ep.ep_dispatch_layout(buf.idx, rank_offsets, E, buf.cap, out=lay, workspace=buf.ws)
     _ep.ep_quantize_rows(x, q=buf.xq, scales=buf.xs)
     _ep.ep_expert_matmul(buf.xq, buf.xs, weights.up, weights.up_scales, off, layout=buf.layout,

@@ -370,15 +370,31 @@ ep_status_t ep_gate_topk(const void* logits, ep_dtype_t logits_dtype, int32_t N,
                          void* stream);
 
 /*
+ * ep_gate_topk_picks -- the same call, which also writes
+ *   picks      int32 [N, K] or NULL: the picks before expert_map, -1 where none
+ *              was available (topk_idx itself where expert_map is NULL).
+ * The weights are taken over these: an expert that the map drops keeps its
+ * share of the sum, so the gradient needs its id.
+ */
+ep_status_t ep_gate_topk_picks(const void* logits, ep_dtype_t logits_dtype, int32_t N, int32_t E,
+                               int32_t K, ep_score_t score, const float* bias, int32_t groups,
+                               int32_t topk_groups, int32_t group_top, int32_t renorm,
+                               float scale, const int32_t* expert_map, int32_t* topk_idx,
+                               float* topk_w, int32_t* picks, void* stream);
+
+/*
  * ep_gate_topk_backward -- gradient of ep_gate_topk's weights with respect to
  * the logits, for training.  The choice of the experts (hence the bias and the
  * groups) is constant; the scores are recomputed from the logits.
  *   d_topk_w   float32 [N, K]: gradient of each weight.
  *   logits, logits_dtype, score, renorm, scale   as in the forward call.
- *   topk_idx   int32 [N, K] as ep_gate_topk wrote it; a token's ids are
- *              distinct, ids outside [0, E) are "no pick" and get nothing.
- *   expert_map the forward call's, or NULL: the ids are then mapped back (to
- *              the lowest expert, should several map to one id).
+ *   topk_idx   int32 [N, K]: ep_gate_topk_picks's picks, with expert_map NULL,
+ *              whatever the forward call's map.  A token's ids are distinct,
+ *              ids outside [0, E) are "no pick" and get nothing.
+ *   expert_map NULL, or the forward call's with its topk_idx, which are then
+ *              mapped back: only for a map that sends the experts which were
+ *              picked to ids of their own (a renumbering).  Where it drops one
+ *              or joins two, topk_idx no longer tells which they were.
  *   d_logits   [N, E] out, of the logits' type, every element written: 0 for
  *              experts that no weight depends on.  Must not overlap logits.
  */
