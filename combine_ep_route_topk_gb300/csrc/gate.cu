@@ -3,7 +3,8 @@
 // logits (ep_gate_topk_backward).
 //
 //   s_e   = 1 / (1 + exp(-l_e))                  (sigmoid), or
-//           exp(l_e - m) / sum_a exp(l_a - m)    (softmax over available experts)
+//           exp(l_e - m) / sum_a exp(l_a - m)    (softmax over the experts whose
+//           logit is available: neither -inf nor NaN)
 //   key_e = s_e + bias_e, or l_e without a bias (the scores grow with l)
 //   group score = largest key of the group, or the sum of its two largest
 //           s_e + bias_e; only experts of the best topk_groups groups remain

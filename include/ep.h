@@ -352,16 +352,22 @@ ep_status_t ep_route_dispatch(const float* logits, const int32_t* rank_offsets, 
  *            relative to the largest, so that scores too small for a float32
  *            keep their shares), or scale * s_k.  The bias moves the choice,
  *            never the weights.
- * An expert whose logit or key is -inf or NaN is not available: it is never
- * picked and takes no part in the softmax.  Where fewer than K are available,
- * the remaining picks are -1 with weight 0 ("no pick" for the layout).  A
- * logit of +inf counts as the largest finite float.
+ * An expert whose logit is -inf or NaN is not available: it is never picked
+ * and takes no part in the softmax.  A bias of -inf or NaN forbids the pick
+ * alone: the softmax counts the expert, since the bias never moves a weight.
+ * Where fewer than K can be picked, the remaining picks are -1 with weight 0
+ * ("no pick" for the layout).  A logit of +inf counts as the largest finite
+ * float.
  *   logits     [N, E] float32 or bf16 (logits_dtype), row-major.
  *   bias       float32 [E] or NULL.
  *   expert_map int32 [E] or NULL, as for ep_route_topk.
  *   topk_idx   int32 [N, K], topk_w float32 [N, K] out.
- * Scores and sums are float32.  Limits: groups <= 32, E % groups == 0,
- * topk_groups * (E / groups) >= K, besides those above.
+ * Scores and sums are float32.  In the choice (keys with a bias, groups' sums)
+ * a score is within 3e-7 of the formula's, so experts or groups closer than
+ * that rounding may come in either order; equal logits with equal biases are
+ * equal keys.
+ * Limits: groups <= 32, E % groups == 0, topk_groups * (E / groups) >= K,
+ * besides those above.
  */
 ep_status_t ep_gate_topk(const void* logits, ep_dtype_t logits_dtype, int32_t N, int32_t E,
                          int32_t K, ep_score_t score, const float* bias, int32_t groups,
