@@ -201,7 +201,7 @@ struct GateGradArgs {
 cudaError_t launch_gate_backward(const GateGradArgs& a, cudaStream_t s);
 
 // ---- 8-bit rows and the experts' products -----------------------------------
-constexpr int kMaxMatmulK = 65536;  // 2^16 products of at most 2^14 fit 31 bits
+constexpr int kMaxMatmulK = 65536;  // 2^16 products of at most 2^14 fit the 32-bit integers of the kernel for few rows
 
 struct QuantArgs {
     const void* x;

@@ -438,8 +438,14 @@ ep_status_t ep_quantize_rows(const void* x, ep_dtype_t x_dtype, ep_act_t act, in
  * in 8-bit integers with a scale for each row and each output channel; an
  * addition of this library.  For each row r of expert e:
  *   out[r, n] = x_scales[s] * w_scales[e, n] * sum_k x[s, k] * w[e, n, k]
- * with the sum kept in 32 bits, the scales applied in float32 and one rounding
- * to the output's type.  Rows lie as ep_dispatch lays them:
+ * with the scales applied in float32 and one rounding to the output's type.
+ * The sum is held in 32 bits: an integer where a call has few rows, else the
+ * float32 accumulators of the tensor cores, which take 16 products at a time.
+ * It is exact while its partial sums stay below 2^24 in magnitude: always up
+ * to Kd = 1024, and in practice for codes of both signs.  Past 2^24 an
+ * addition may lose up to 2^-23 of the sum so far (codes all 127: 4.6e-5 of
+ * the sum at Kd = 65536), so that a row's last bits can depend on how many
+ * rows the call has.  Rows lie as ep_dispatch lays them:
  *   CONTIG  out is [rows, Nc]; expert e owns rows expert_offsets[e] ..
  *           expert_offsets[e+1]-1.
  *   MASKED  out is [E, cap, Nc] (rows == E*cap); expert e owns its first
