@@ -284,6 +284,15 @@ class LayerBuffers:
     hs: torch.Tensor
     down: torch.Tensor          # [rows, H] bf16
     comb: torch.Tensor          # [N, H] bf16
+    up_status: torch.Tensor     # [1] each: 0 once its product completed, 1 if it gave up
+    down_status: torch.Tensor
+
+    def check(self):
+        """Waits for the last layer's products; raises if one of them gave up (its
+        rows are then incomplete)."""
+        for name, status in (("first", self.up_status), ("second", self.down_status)):
+            if int(status) != 0:
+                raise _ep.EPError(f"expert_layer: the {name} product gave up waiting")
 
 
 def make_layer_buffers(N, E, K, H, inner, R, cap=0, device="cuda"):
@@ -300,7 +309,7 @@ def make_layer_buffers(N, E, K, H, inner, R, cap=0, device="cuda"):
         z(_ep.ep_dispatch_layout_workspace_size(N, E, K, R), torch.uint8),
         z((N, H), torch.int8), z((N,), torch.float32), z((rows, 2 * inner), torch.bfloat16),
         z((rows, inner), torch.int8), z((rows,), torch.float32), z((rows, H), torch.bfloat16),
-        z((N, H), torch.bfloat16))
+        z((N, H), torch.bfloat16), z((1,), torch.int32), z((1,), torch.int32))
 
 
 def expert_layer(x, logits, rank_offsets, weights, buf, score=_ep.EP_SCORE_SIGMOID, bias=None,
@@ -308,7 +317,8 @@ def expert_layer(x, logits, rank_offsets, weights, buf, score=_ep.EP_SCORE_SIGMO
                  expert_map=None):
     """x bf16 [N, H], logits [N, E] -> buf.comb bf16 [N, H], on the current
     stream.  The gate's arguments are ep_gate_topk's.  For training, buf.picks and
-    the gradient of buf.wt go to ep_gate_topk_backward, without the map."""
+    the gradient of buf.wt go to ep_gate_topk_backward, without the map.
+    buf.check() tells, once the step is done, that both products completed."""
     E = logits.shape[1]
     K = buf.idx.shape[1]
     lay, off = buf.lay, buf.lay.expert_offsets
@@ -318,11 +328,11 @@ def expert_layer(x, logits, rank_offsets, weights, buf, score=_ep.EP_SCORE_SIGMO
     _ep.ep_dispatch_layout(buf.idx, rank_offsets, E, buf.cap, out=lay, workspace=buf.ws)
     _ep.ep_quantize_rows(x, q=buf.xq, scales=buf.xs)
     _ep.ep_expert_matmul(buf.xq, buf.xs, weights.up, weights.up_scales, off, layout=buf.layout,
-                         cap=buf.cap, row_src=lay.row_src, out=buf.up)
+                         cap=buf.cap, row_src=lay.row_src, out=buf.up, status=buf.up_status)
     _ep.ep_quantize_rows(buf.up, act=_ep.EP_ACT_SWIGLU, expert_offsets=off, layout=buf.layout,
                          cap=buf.cap, q=buf.hq, scales=buf.hs)
     _ep.ep_expert_matmul(buf.hq, buf.hs, weights.down, weights.down_scales, off,
-                         layout=buf.layout, cap=buf.cap, out=buf.down)
+                         layout=buf.layout, cap=buf.cap, out=buf.down, status=buf.down_status)
     return _ep.ep_combine(buf.down, buf.idx, buf.wt, lay.pos, off, E, layout=buf.layout,
                           cap=buf.cap, out=buf.comb)
 
