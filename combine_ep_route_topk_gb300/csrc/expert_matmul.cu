@@ -11,7 +11,8 @@
 // among the warps of the grid, so that no SM ends much later than another; a
 // warp takes two channels at a time, with 16-byte loads, two rounds of them in
 // flight, and multiplies them by dp4a with the group's rows, which stay in L1.
-// The row loop is compiled for 1, 2, 4 and 8 rows.  8 rows of as many experts
+// The row loop is compiled for 1, 2, 4 and 8 rows; that of 8 spills (48 registers a
+// thread at 5 blocks an SM: 504 bytes stored, 672 loaded).  8 rows of as many experts
 // (4096 x 7168, 235 MB): 39.4 us = 6.0 TB/s; with 4 or 6 blocks per SM 41.6 and
 // 40.6 us, with 3 or 4 channels at a time 40.1 and 41.6 us.
 #include "expert_common.cuh"
@@ -141,12 +142,23 @@ matmul_rows_kernel(MatmulArgs a) {
 cudaError_t launch_expert_matmul(const MatmulArgs& a, cudaStream_t s) {
     if (a.rows == 0)
         return a.status != nullptr ? cudaMemsetAsync(a.status, 0, sizeof(int32_t), s) : cudaSuccess;
-    // Few rows, most of them alone with their expert: this kernel.  Rows alone with
-    // their expert (tensor cores in brackets), 32 experts of 4096 x 7168: 8 rows
-    // 41 us (48), 16 rows 78 (87); 128 experts of 2880 x 1440: 32 rows 28 (34), 64
-    // rows 50 (60).  Rows that pick independently: 12 of 32 56 (49), 16 of 32 72
-    // (68), 32 of 32 102 (88), 64 of 128 53 (49), 32 of 128 25 (28).  One expert
-    // of 4096 x 4096: 2 rows 8 (12), 4 rows 12 (12), 5 rows 22 (12).
+    // Few rows, most of them alone with their expert: this kernel.  It takes a time per
+    // row; the tensor cores one per expert with rows, so that rows which pick
+    // independently and meet count against it.  Mean of 20 draws, us, rows alone with
+    // their expert / rows that pick independently (tensor cores in brackets):
+    //   32 experts of 4096 x 7168:  8 rows 41 (47) / 39 (47), 12 60 (67) / 53 (60),
+    //                               16 78 (87) / 68 (68)
+    //   128 of 2880 x 1440:  32 rows 28 (34) / 27 (31), 48 38 (46) / 37 (39),
+    //                        64 48 (59) / 48 (47)
+    //   128 of 7168 x 2048:  48 rows 117 (117) / 112 (99), 64 154 (194) / 151 (151)
+    //   256 of 4096 x 2048:  32 rows 48 (50) / 47 (48), 64 90 (91) / 94 (82),
+    //                        96 133 (130) / 136 (110), 128 176 (169) / 177 (134)
+    //   512 of 1024 x 2048:  64 rows 27 (31) / 27 (29), 128 49 (50) / 51 (44),
+    //                        256 91 (90) / 94 (72)
+    //   1024 of 512 x 1024:  128 rows 17 (18) / 17 (18), 512 52 (66) / 52 (53)
+    // Past 64 rows that pick independently, large experts would so be faster on the
+    // tensor cores (up to 25 %) and small ones slower; the rule does not tell them apart.
+    // One expert of 4096 x 4096: 2 rows 8 (12), 4 rows 12 (12), 5 rows 22 (12).
     cudaError_t err;
     if (a.x_rows == 0 || a.rows <= 4 || 2ll * a.rows <= a.E) {
         err = launch(matmul_rows_kernel, dim3(sm_count() * kBlocksPerSm), dim3(kWarps * 32), 0, s, a);

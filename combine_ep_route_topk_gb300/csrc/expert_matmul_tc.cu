@@ -955,7 +955,9 @@ namespace {
 // arrive, are widened and multiplied), a tile's start and end 3000, sums that are
 // joined 6500 more, the launch of pairs 2000 more.  The counts of several experts scatter around their mean as
 // independent picks would, which decides whether an expert needs one tile more;
-// one expert's count and a capacity are taken as they are.
+// one expert's count and a capacity are taken as they are, so that a capacity far
+// above the rows gets wide tiles (32 experts of 4096 x 7168 with 8 rows each: 185 us
+// under a capacity of 1024, 146 under one of 16).
 template <class S>
 double shape_cycles(const MatmulArgs& a, double base, double slope) {
     const double mean = a.layout == 0 ? (double)a.rows / a.E : a.cap;

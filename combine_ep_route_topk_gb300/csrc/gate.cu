@@ -21,13 +21,17 @@
 // full accuracy, for the picks alone; the choice uses the hardware's exp2 and
 // reciprocal (an absolute error below 3e-7 in a score of at most 1).
 //
-// What bounds it: instructions (517 a token of 256 experts with bias and groups;
-// 74 % of the issue slots): 32768 tokens of float32, 33.6 MB, take 17.0 us where
-// the bytes alone would take 5; one token 2.2 us.  Rows of finite numbers skip
+// What bounds it: instructions (523 a token of 256 experts with bias and groups;
+// 75 % of the issue slots): 32768 tokens of float32, 33.6 MB, take 17.4 us where
+// the bytes alone would take 5; one token 2.5 us.  Rows of finite numbers skip
 // the tests for others and picks without equals in their lane the count of them
-// (18.8 us with neither, and 15.3 against 12.3 for a softmax in one group).  The gradient (same sizes, 8
-// picks a token) takes 11.2 us for its 33.5 MB of stores, 7.3 when they stay in
-// L2, and 11.6 where every expert gets one (softmax, not renormalised).
+// (18.8 us with neither, and 15.3 against 12.6 for a softmax in one group).  That
+// holds where the experts fill the lanes: 32, 64, 128, 160, 256, 384, 512 and 1024.
+// Otherwise the padding past E, held as NaN, sends every row through the tests (a
+// softmax of 32768 tokens: 96 experts 11.7 us, 128 10.5; 192 14.8, 256 12.6).  The
+// gradient (32768 x 256, 8 picks a token) takes 11.2 us for its 33.5 MB of stores,
+// 7.3 when they stay in L2, and 11.6 where every expert gets one (softmax, not
+// renormalised).
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -250,7 +254,8 @@ gate_kernel(GateArgs a) {
         load_row<VPL>(a.bias, E, a.bias_vec != 0, lane, bias);
     }
     // Whether every logit and bias of the row is finite: 0 x is NaN otherwise (on
-    // another pipe than the comparisons that are spared then).
+    // another pipe than the comparisons that are spared then).  False for every row
+    // that does not fill the lanes, whose padding is NaN.
     float zero = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {

@@ -187,11 +187,11 @@ cudaError_t launch_shape(const QuantArgs& a, cudaStream_t s) {
 }
 
 // Measured on a GB300 (bf16, us; floor at the measured copy rate): 32768 x 7168
-// 105.6 (105), with 256 threads for its 224 x 4 vectors 111.2; 8192 x 9216 36.9
-// (34), with 512 threads for 288 54.8; SwiGLU 32768 x 2048 53.8 (50), with 64 and
+// 105.4 (105), with 256 threads for its 224 x 4 vectors 111.2; 8192 x 9216 37.5
+// (34), with 512 threads for 288 54.8; SwiGLU 32768 x 2048 54.1 (50), with 64 and
 // 256 threads a row 59.1 and 56.2.  A warp a row: 65536 x 1024 28.1 (30), with
 // 128 threads 66.1 (a block a nanosecond is what the chip starts); 32768 x 1440
-// 19.5 (21), with 96 threads 33.3, but SwiGLU of 65536 x 1440 97.7 against 78.4
+// 18.6 (21), with 96 threads 33.3, but SwiGLU of 65536 x 1440 97.7 against 78.4
 // (71), and one token's 8 rows 2.1 against 1.5.  Four vectors a thread: 32768 x
 // 4096 59.5 (60), with two 70.3, but SwiGLU of them 118.0 against 111.8 (100).
 template <typename T, bool SWIGLU>

@@ -34,14 +34,15 @@
  *   - Work is enqueued on `stream` (a cudaStream_t passed as void*; NULL is
  *     the legacy default stream) and returns without synchronising
  *     (ep_host_pipeline_destroy alone waits, for its own streams); no call
- *     reads device memory on the host, so the four calls and the layout
- *     variants can be captured in a CUDA graph.
+ *     reads device memory on the host, so the four calls, the layout variants
+ *     and the expert operators can be captured in a CUDA graph.
  *   - Arguments are checked on the host before anything is launched; a bad
  *     argument returns EP_ERR_INVALID_ARG (or EP_ERR_WORKSPACE /
  *     EP_ERR_UNSUPPORTED) and launches nothing.  A failed launch returns
  *     EP_ERR_CUDA.  No kernel traps or asserts.  Besides the stream-order wait
  *     of programmatic launch (below), the only waits are the bounded grid
- *     barriers inside ep_route_layout.
+ *     barriers inside ep_route_layout and ep_expert_matmul's bounded waits for
+ *     its own copies and products (its status tells if one ran out).
  *   - Device-side data that break a precondition (an expert id outside
  *     [0,E), rank_offsets that are not a non-decreasing 0..N sequence, pos
  *     values that do not come from ep_dispatch_layout) never cause an access
@@ -363,9 +364,8 @@ ep_status_t ep_route_dispatch(const float* logits, const int32_t* rank_offsets, 
  *   expert_map int32 [E] or NULL, as for ep_route_topk.
  *   topk_idx   int32 [N, K], topk_w float32 [N, K] out.
  * Scores and sums are float32.  In the choice (keys with a bias, groups' sums)
- * a score is within 3e-7 of the formula's, so experts or groups closer than
- * that rounding may come in either order; equal logits with equal biases are
- * equal keys.
+ * a score is off by up to some 3e-7, so experts or groups closer than that may
+ * come in either order; equal logits with equal biases are equal keys.
  * Limits: groups <= 32, E % groups == 0, topk_groups * (E / groups) >= K,
  * besides those above.
  */
