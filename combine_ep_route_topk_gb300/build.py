@@ -19,10 +19,10 @@ SOURCES = ["ep_api.cu", "route_topk.cu", "layout.cu", "layout_cluster.cu", "layo
            "host_pipeline.cu",
            "route_layout.cu", "route_dispatch.cu",
            "dispatch.cu", "combine.cu", "gate.cu", "quantize.cu", "expert_matmul.cu",
-           "expert_matmul_tc.cu"]
+           "expert_matmul_tc.cu", "expert_matmul_fp8.cu", "blocks.cu", "norm.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("ep_kernels.cuh", "route_common.cuh",
                                             "layout_common.cuh", "dispatch_common.cuh",
-                                            "expert_common.cuh")] + [
+                                            "expert_common.cuh", "rows_common.cuh", "tc_common.cuh")] + [
     os.path.join(ROOT, "include", "ep.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

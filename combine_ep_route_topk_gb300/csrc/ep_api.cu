@@ -2,6 +2,7 @@
 // then kernel launches on the caller's stream.  Nothing here allocates,
 // synchronises or reads device memory.
 #include <atomic>
+#include <cfloat>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -512,11 +513,12 @@ ep_status_t ep_quantize_rows(const void* x, ep_dtype_t x_dtype, ep_act_t act, in
     return cuda_status(launch_quantize(a, static_cast<cudaStream_t>(stream)));
 }
 
-ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_rows,
-                             const int8_t* w, const float* w_scales, int32_t E, int32_t Nc,
-                             int32_t Kd, const int32_t* expert_offsets, ep_layout_t layout,
-                             int32_t cap, int32_t rows, const int32_t* row_src, int32_t n_src,
-                             ep_dtype_t out_dtype, void* out, int32_t* status, void* stream) {
+// The checks of both products; x and w are rows of bytes.
+static ep_status_t check_matmul(const int8_t* x, const float* x_scales, int32_t x_rows,
+                                const int8_t* w, const float* w_scales, int32_t E, int32_t Nc,
+                                int32_t Kd, const int32_t* expert_offsets, ep_layout_t layout,
+                                int32_t cap, int32_t rows, const int32_t* row_src, int32_t n_src,
+                                ep_dtype_t out_dtype, void* out, int32_t* status, MatmulArgs* args) {
     if (E < 1 || Nc < 1 || rows < 0 || x_rows < 0 || Kd < 16 || Kd % 16 != 0)
         return EP_ERR_INVALID_ARG;
     if (layout != EP_LAYOUT_CONTIG && layout != EP_LAYOUT_MASKED) return EP_ERR_INVALID_ARG;
@@ -532,7 +534,7 @@ ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_r
     const void* ptrs[] = {x_scales, w_scales, expert_offsets, row_src, status};
     for (const void* p : ptrs)
         if (!aligned4(p)) return EP_ERR_INVALID_ARG;
-    MatmulArgs a;
+    MatmulArgs& a = *args;
     a.x = x;
     a.x_scales = x_scales;
     a.w = w;
@@ -550,7 +552,207 @@ ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_r
     a.cap = cap;
     a.layout = (int)layout;
     a.out_bf16 = out_dtype == EP_DTYPE_BF16;
+    return EP_OK;
+}
+
+ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_rows,
+                             const int8_t* w, const float* w_scales, int32_t E, int32_t Nc,
+                             int32_t Kd, const int32_t* expert_offsets, ep_layout_t layout,
+                             int32_t cap, int32_t rows, const int32_t* row_src, int32_t n_src,
+                             ep_dtype_t out_dtype, void* out, int32_t* status, void* stream) {
+    MatmulArgs a;
+    const ep_status_t st = check_matmul(x, x_scales, x_rows, w, w_scales, E, Nc, Kd,
+                                        expert_offsets, layout, cap, rows, row_src, n_src,
+                                        out_dtype, out, status, &a);
+    if (st != EP_OK) return st;
     return cuda_status(launch_expert_matmul(a, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_expert_matmul_fp8(const uint8_t* x, const float* x_scales, int32_t x_rows,
+                             const uint8_t* w, const float* w_scales, int32_t E, int32_t Nc,
+                             int32_t Kd, const int32_t* expert_offsets, ep_layout_t layout,
+                             int32_t cap, int32_t rows, const int32_t* row_src, int32_t n_src,
+                             ep_dtype_t out_dtype, void* out, int32_t* status, void* stream) {
+    MatmulArgs a;
+    const ep_status_t st = check_matmul(reinterpret_cast<const int8_t*>(x), x_scales, x_rows,
+                                        reinterpret_cast<const int8_t*>(w), w_scales, E, Nc, Kd,
+                                        expert_offsets, layout, cap, rows, row_src, n_src,
+                                        out_dtype, out, status, &a);
+    if (st != EP_OK) return st;
+    return cuda_status(launch_expert_matmul_fp8(a, static_cast<cudaStream_t>(stream)));
+}
+
+// The arguments that say which rows of an expert-major buffer hold a token.
+static ep_status_t check_tokens(const int32_t* expert_offsets, int32_t E, ep_layout_t layout,
+                                int32_t cap, int32_t rows, TokenRows* out) {
+    if (layout != EP_LAYOUT_CONTIG && layout != EP_LAYOUT_MASKED) return EP_ERR_INVALID_ARG;
+    if (expert_offsets) {
+        if (E < 1) return EP_ERR_INVALID_ARG;
+        if (E > kMaxE) return EP_ERR_UNSUPPORTED;
+        if (layout == EP_LAYOUT_MASKED && (cap < 1 || (int64_t)E * cap != rows))
+            return EP_ERR_INVALID_ARG;
+        if (!aligned4(expert_offsets)) return EP_ERR_INVALID_ARG;
+    }
+    *out = TokenRows{expert_offsets, E, cap, (int)layout};
+    return EP_OK;
+}
+
+// Rows of `cols` columns and their codes: a multiple of 16 columns, and few enough
+// that rows x blocks of 128 (of `wide` columns) is an int32.
+static ep_status_t check_block_rows(int32_t rows, int32_t cols, int32_t halves) {
+    if (rows < 0 || cols < 16 || cols % 16 != 0) return EP_ERR_INVALID_ARG;
+    if (cols > (INT32_MAX - 128) / halves) return EP_ERR_UNSUPPORTED;
+    if ((int64_t)rows * scale_blocks(cols * halves) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+static bool is_row_type(ep_dtype_t t) { return t == EP_DTYPE_F32 || t == EP_DTYPE_BF16; }
+
+ep_status_t ep_quantize_blocks(const void* x, ep_dtype_t x_dtype, ep_act_t act, int32_t rows,
+                               int32_t cols, const int32_t* expert_offsets, int32_t E,
+                               ep_layout_t layout, int32_t cap, uint8_t* q, float* scales,
+                               uint8_t* x_q, float* x_scales, void* stream) {
+    if (!is_row_type(x_dtype) || (act != EP_ACT_NONE && act != EP_ACT_SWIGLU))
+        return EP_ERR_INVALID_ARG;
+    ep_status_t st = check_block_rows(rows, cols, act == EP_ACT_SWIGLU ? 2 : 1);
+    if (st != EP_OK) return st;
+    BlockQuantArgs a;
+    st = check_tokens(expert_offsets, E, layout, cap, rows, &a.tokens);
+    if (st != EP_OK) return st;
+    if ((x_q == nullptr) != (x_scales == nullptr)) return EP_ERR_INVALID_ARG;
+    if (x_q && act != EP_ACT_SWIGLU) return EP_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !q || !scales)) return EP_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(x_q) || !aligned4(scales) ||
+        !aligned4(x_scales))
+        return EP_ERR_INVALID_ARG;
+    a.x = x;
+    a.q = q;
+    a.scales = scales;
+    a.x_q = x_q;
+    a.x_scales = x_scales;
+    a.rows = rows;
+    a.cols = cols;
+    a.swiglu = act == EP_ACT_SWIGLU;
+    a.bf16 = x_dtype == EP_DTYPE_BF16;
+    return cuda_status(launch_quantize_blocks(a, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_dequantize_blocks(const uint8_t* q, const float* scales, int32_t rows, int32_t cols,
+                                 const int32_t* expert_offsets, int32_t E, ep_layout_t layout,
+                                 int32_t cap, ep_dtype_t out_dtype, void* out, void* stream) {
+    if (!is_row_type(out_dtype)) return EP_ERR_INVALID_ARG;
+    ep_status_t st = check_block_rows(rows, cols, 1);
+    if (st != EP_OK) return st;
+    BlockRestoreArgs a;
+    st = check_tokens(expert_offsets, E, layout, cap, rows, &a.tokens);
+    if (st != EP_OK) return st;
+    if (rows > 0 && (!q || !scales || !out)) return EP_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned4(scales)) return EP_ERR_INVALID_ARG;
+    a.q = q;
+    a.scales = scales;
+    a.out = out;
+    a.rows = rows;
+    a.cols = cols;
+    a.bf16 = out_dtype == EP_DTYPE_BF16;
+    return cuda_status(launch_dequantize_blocks(a, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_swiglu_backward(const void* d_out, ep_dtype_t dtype, const void* x,
+                               const float* x_scales, int32_t rows, int32_t cols,
+                               const int32_t* expert_offsets, int32_t E, ep_layout_t layout,
+                               int32_t cap, void* d_x, void* stream) {
+    if (!is_row_type(dtype)) return EP_ERR_INVALID_ARG;
+    ep_status_t st = check_block_rows(rows, cols, 2);
+    if (st != EP_OK) return st;
+    SwigluGradArgs a;
+    st = check_tokens(expert_offsets, E, layout, cap, rows, &a.tokens);
+    if (st != EP_OK) return st;
+    if (rows > 0 && (!d_out || !x || !d_x)) return EP_ERR_INVALID_ARG;
+    if (!aligned16(d_out) || !aligned16(x) || !aligned16(d_x) || !aligned4(x_scales))
+        return EP_ERR_INVALID_ARG;
+    a.d_out = d_out;
+    a.x = x;
+    a.x_scales = x_scales;
+    a.d_x = d_x;
+    a.rows = rows;
+    a.cols = cols;
+    a.bf16 = dtype == EP_DTYPE_BF16;
+    return cuda_status(launch_swiglu_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+// Sizes of the norm and its gradient.
+static ep_status_t check_norm(int32_t rows, int32_t cols) {
+    if (rows < 0 || cols < 16 || cols % 16 != 0) return EP_ERR_INVALID_ARG;
+    if (cols > kMaxNormCols) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+ep_status_t ep_rms_norm(const void* x, ep_dtype_t dtype, const void* residual, const void* weight,
+                        ep_dtype_t weight_dtype, int32_t rows, int32_t cols, float eps,
+                        void* residual_out, void* y, uint8_t* q, float* scales, float* rstd,
+                        void* stream) {
+    if (!is_row_type(dtype) || !is_row_type(weight_dtype)) return EP_ERR_INVALID_ARG;
+    const ep_status_t st = check_norm(rows, cols);
+    if (st != EP_OK) return st;
+    if (!(eps > 0.0f && eps <= FLT_MAX)) return EP_ERR_INVALID_ARG;
+    if ((q == nullptr) != (scales == nullptr)) return EP_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !weight || (!residual_out && !y && !q && !rstd)))
+        return EP_ERR_INVALID_ARG;
+    const void* wide[] = {x, residual, weight, residual_out, y, q};
+    for (const void* p : wide)
+        if (!aligned16(p)) return EP_ERR_INVALID_ARG;
+    if (!aligned4(scales) || !aligned4(rstd)) return EP_ERR_INVALID_ARG;
+    NormArgs a;
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.residual_out = residual_out;
+    a.y = y;
+    a.q = q;
+    a.scales = scales;
+    a.rstd = rstd;
+    a.eps = eps;
+    a.rows = rows;
+    a.cols = cols;
+    a.bf16 = dtype == EP_DTYPE_BF16;
+    a.weight_bf16 = weight_dtype == EP_DTYPE_BF16;
+    return cuda_status(launch_rms_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ep_rms_norm_backward_workspace_size(int32_t rows, int32_t cols) {
+    if (check_norm(rows, cols) != EP_OK) return 256;
+    return ((size_t)norm_grad_blocks(rows, cols) * cols * sizeof(float) + 511) / 256 * 256;
+}
+
+ep_status_t ep_rms_norm_backward(const void* d_y, ep_dtype_t dtype, const void* z,
+                                 const void* weight, ep_dtype_t weight_dtype, const float* rstd,
+                                 const void* d_residual, int32_t rows, int32_t cols, void* d_x,
+                                 float* d_weight, void* workspace, size_t ws_bytes, void* stream) {
+    if (!is_row_type(dtype) || !is_row_type(weight_dtype)) return EP_ERR_INVALID_ARG;
+    const ep_status_t st = check_norm(rows, cols);
+    if (st != EP_OK) return st;
+    if (rows > 0 && (!d_y || !z || !weight || !rstd || !d_x)) return EP_ERR_INVALID_ARG;
+    const void* wide[] = {d_y, z, weight, d_residual, d_x, workspace};
+    for (const void* p : wide)
+        if (!aligned16(p)) return EP_ERR_INVALID_ARG;
+    if (!aligned4(rstd) || !aligned4(d_weight)) return EP_ERR_INVALID_ARG;
+    if (d_weight && rows > 0 &&
+        (!workspace || ws_bytes < ep_rms_norm_backward_workspace_size(rows, cols)))
+        return EP_ERR_WORKSPACE;
+    NormGradArgs a;
+    a.d_y = d_y;
+    a.z = z;
+    a.weight = weight;
+    a.rstd = rstd;
+    a.d_residual = d_residual;
+    a.d_x = d_x;
+    a.d_weight = d_weight;
+    a.partial = static_cast<float*>(workspace);
+    a.rows = rows;
+    a.cols = cols;
+    a.bf16 = dtype == EP_DTYPE_BF16;
+    a.weight_bf16 = weight_dtype == EP_DTYPE_BF16;
+    return cuda_status(launch_rms_norm_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
 ep_status_t ep_selftest_wait_timeout(int32_t* status, void* workspace, size_t ws_bytes,

@@ -227,4 +227,79 @@ cudaError_t launch_expert_matmul(const MatmulArgs& a, cudaStream_t s);
 // The tensor core kernel (expert_matmul_tc.cu).
 cudaError_t launch_matmul_tc(const MatmulArgs& a, cudaStream_t s);
 
+// ---- rows of E4M3 codes with a scale for every 128 columns -------------------
+constexpr int kScaleBlock = 128;
+__host__ __device__ inline int scale_blocks(int cols) { return (cols + kScaleBlock - 1) / kScaleBlock; }
+
+// The rows of an expert-major buffer that hold a token (all, without offsets).
+struct TokenRows {
+    const int32_t* expert_offsets;
+    int E, cap, layout;
+};
+struct BlockQuantArgs {
+    const void* x;
+    TokenRows tokens;
+    uint8_t* q;
+    float* scales;
+    uint8_t* x_q;               // or nullptr: codes of x itself (SwiGLU)
+    float* x_scales;
+    int rows, cols, swiglu, bf16;
+};
+cudaError_t launch_quantize_blocks(const BlockQuantArgs& a, cudaStream_t s);
+
+struct BlockRestoreArgs {
+    const uint8_t* q;
+    const float* scales;
+    TokenRows tokens;
+    void* out;
+    int rows, cols, bf16;
+};
+cudaError_t launch_dequantize_blocks(const BlockRestoreArgs& a, cudaStream_t s);
+
+struct SwigluGradArgs {
+    const void* d_out;
+    const void* x;              // rows, or their codes where x_scales is given
+    const float* x_scales;
+    TokenRows tokens;
+    void* d_x;
+    int rows, cols, bf16;
+};
+cudaError_t launch_swiglu_backward(const SwigluGradArgs& a, cudaStream_t s);
+
+// x and w hold E4M3 codes; x_scales [x_rows, Kd / 128], w_scales [E, Nc / 128,
+// Kd / 128], both rounded up (expert_matmul_fp8.cu).
+cudaError_t launch_expert_matmul_fp8(const MatmulArgs& a, cudaStream_t s);
+
+// ---- root-mean-square norm ---------------------------------------------------
+constexpr int kMaxNormCols = 16384;
+
+struct NormArgs {
+    const void* x;
+    const void* residual;       // or nullptr
+    const void* weight;
+    void* residual_out;         // each or nullptr
+    void* y;
+    uint8_t* q;
+    float* scales;
+    float* rstd;
+    float eps;
+    int rows, cols, bf16, weight_bf16;
+};
+cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
+
+struct NormGradArgs {
+    const void* d_y;
+    const void* z;
+    const void* weight;
+    const float* rstd;
+    const void* d_residual;     // or nullptr
+    void* d_x;
+    float* d_weight;            // or nullptr
+    float* partial;             // [blocks, cols], where d_weight is given
+    int rows, cols, bf16, weight_bf16;
+};
+// Blocks of the kernel that sums the weight's gradient, each with a partial sum.
+int norm_grad_blocks(int rows, int cols);
+cudaError_t launch_rms_norm_backward(const NormGradArgs& a, cudaStream_t s);
+
 }  // namespace ep

@@ -95,8 +95,18 @@ def lib():
         L.ep_quantize_rows.argtypes = [P, enum, enum, i32, i32, P, i32, enum, i32, P, P, P]
         L.ep_expert_matmul.argtypes = [P, P, i32, P, P, i32, i32, i32, P, enum, i32, i32, P, i32,
                                        enum, P, P, P]
+        L.ep_quantize_blocks.argtypes = [P, enum, enum, i32, i32, P, i32, enum, i32, P, P, P, P, P]
+        L.ep_dequantize_blocks.argtypes = [P, P, i32, i32, P, i32, enum, i32, enum, P, P]
+        L.ep_swiglu_backward.argtypes = [P, enum, P, P, i32, i32, P, i32, enum, i32, P, P]
+        L.ep_expert_matmul_fp8.argtypes = L.ep_expert_matmul.argtypes
+        L.ep_rms_norm.argtypes = [P, enum, P, P, enum, i32, i32, f32, P, P, P, P, P, P]
+        L.ep_rms_norm_backward_workspace_size.argtypes = [i32, i32]
+        L.ep_rms_norm_backward_workspace_size.restype = sz
+        L.ep_rms_norm_backward.argtypes = [P, enum, P, P, enum, P, P, i32, i32, P, P, P, sz, P]
         for f in ("ep_gate_topk", "ep_gate_topk_picks", "ep_gate_topk_backward",
-                  "ep_quantize_rows", "ep_expert_matmul"):
+                  "ep_quantize_rows", "ep_expert_matmul", "ep_quantize_blocks",
+                  "ep_dequantize_blocks", "ep_swiglu_backward", "ep_expert_matmul_fp8",
+                  "ep_rms_norm", "ep_rms_norm_backward"):
             getattr(L, f).restype = ctypes.c_int
         L.ep_status_string.argtypes = [ctypes.c_int]
         L.ep_status_string.restype = ctypes.c_char_p
@@ -467,6 +477,197 @@ def ep_expert_matmul(x, x_scales, w, w_scales, expert_offsets, layout=EP_LAYOUT_
         _opt(row_src, torch.int32, "row_src"), 0 if row_src is None else row_src.numel(), dt,
         _dev(out, out.dtype, "out"), _opt(status, torch.int32, "status", (1,)), _stream(stream)))
     return out
+
+SCALE_BLOCK = 128  # columns of a row that share a scale
+
+
+def scale_blocks(cols) -> int:
+    """Scales of a row of `cols` columns of E4M3 codes."""
+    return -(-cols // SCALE_BLOCK)
+
+
+def _codes(t, name, shape=None):
+    """Device pointer of E4M3 codes: uint8, or torch's own type of them."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float8_e4m3fn:
+        t = t.view(torch.uint8)
+    return _dev(t, torch.uint8, name, shape)
+
+
+def _tokens(expert_offsets):
+    """(pointer, E) of the offsets that say which rows hold a token."""
+    if expert_offsets is None:
+        return None, 0
+    return _dev(expert_offsets, torch.int32, "expert_offsets"), expert_offsets.numel() - 1
+
+
+def _rows2d(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise EPError(f"{name} must be a tensor of rows (two dimensions)")
+    return t.shape
+
+
+def ep_quantize_blocks(x, act=EP_ACT_NONE, expert_offsets=None, layout=EP_LAYOUT_CONTIG, cap=0,
+                       q=None, scales=None, x_q=None, x_scales=None, stream=None):
+    """x bf16 or float32 [rows, cols] (EP_ACT_SWIGLU: [rows, 2*cols]) -> (q uint8
+    E4M3 codes [rows, cols], scales float32 [rows, ceil(cols / 128)]).  With x_q
+    [rows, 2*cols] and x_scales (SwiGLU), the codes of x itself are written too:
+    the checkpoint that ep_swiglu_backward reads.  With expert_offsets, rows that
+    hold no token are skipped."""
+    rows, wide = _rows2d(x, "x")
+    dt = _float_type(x, "x")
+    if act == EP_ACT_SWIGLU and wide % 2:
+        raise EPError("x must have an even number of columns for SwiGLU")
+    cols = wide // 2 if act == EP_ACT_SWIGLU else wide
+    if q is None:
+        q = _empty((rows, cols), torch.uint8, x)
+    if scales is None:
+        scales = _empty((rows, scale_blocks(cols)), torch.float32, x)
+    offs, E = _tokens(expert_offsets)
+    _check("ep_quantize_blocks", lib().ep_quantize_blocks(
+        _dev(x, x.dtype, "x"), dt, act, rows, cols, offs, E, layout, cap,
+        _codes(q, "q", (rows, cols)),
+        _dev(scales, torch.float32, "scales", (rows, scale_blocks(cols))),
+        None if x_q is None else _codes(x_q, "x_q", (rows, wide)),
+        _opt(x_scales, torch.float32, "x_scales", (rows, scale_blocks(wide))), _stream(stream)))
+    return q, scales
+
+
+def ep_dequantize_blocks(q, scales, expert_offsets=None, layout=EP_LAYOUT_CONTIG, cap=0, out=None,
+                         out_dtype=torch.bfloat16, stream=None):
+    """E4M3 codes [rows, cols] and their scales [rows, ceil(cols / 128)] -> the
+    values that they stand for, bf16 or float32 [rows, cols]."""
+    rows, cols = _rows2d(q, "q")
+    if out is None:
+        out = _empty((rows, cols), out_dtype, q)
+    dt = _float_type(out, "out")
+    offs, E = _tokens(expert_offsets)
+    _check("ep_dequantize_blocks", lib().ep_dequantize_blocks(
+        _codes(q, "q"), _dev(scales, torch.float32, "scales", (rows, scale_blocks(cols))), rows,
+        cols, offs, E, layout, cap, dt, _dev(out, out.dtype, "out", (rows, cols)),
+        _stream(stream)))
+    return out
+
+
+def ep_swiglu_backward(d_out, x, x_scales=None, expert_offsets=None, layout=EP_LAYOUT_CONTIG,
+                       cap=0, d_x=None, stream=None):
+    """Gradient of silu(g) * u to x = (g, u): d_out bf16 or float32 [rows, cols]
+    -> d_x [rows, 2*cols] of its type.  x: the rows [rows, 2*cols] of the same
+    type, or their E4M3 codes with x_scales [rows, ceil(2*cols / 128)]."""
+    rows, cols = _rows2d(d_out, "d_out")
+    dt = _float_type(d_out, "d_out")
+    if d_x is None:
+        d_x = _empty((rows, 2 * cols), d_out.dtype, d_out)
+    if x_scales is None:
+        px = _dev(x, d_out.dtype, "x", (rows, 2 * cols))
+    else:
+        px = _codes(x, "x", (rows, 2 * cols))
+    offs, E = _tokens(expert_offsets)
+    _check("ep_swiglu_backward", lib().ep_swiglu_backward(
+        _dev(d_out, d_out.dtype, "d_out"), dt, px,
+        _opt(x_scales, torch.float32, "x_scales", (rows, scale_blocks(2 * cols))), rows, cols,
+        offs, E, layout, cap, _dev(d_x, d_out.dtype, "d_x", (rows, 2 * cols)), _stream(stream)))
+    return d_x
+
+
+def ep_expert_matmul_fp8(x, x_scales, w, w_scales, expert_offsets, layout=EP_LAYOUT_CONTIG, cap=0,
+                         row_src=None, out=None, out_dtype=torch.bfloat16, status=None,
+                         stream=None):
+    """Every expert's rows times its weights in E4M3 codes: x [x_rows, Kd] with
+    x_scales float32 [x_rows, ceil(Kd / 128)], w [E, Nc, Kd] with w_scales float32
+    [E, ceil(Nc / 128), ceil(Kd / 128)] -> out bf16 or float32 [rows, Nc] ([E*cap,
+    Nc] for the masked layout).  With row_src (the layout's), x holds token rows.
+    Rows that hold no token are not written."""
+    x_rows = _rows2d(x, "x")[0]
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise EPError("w must be a tensor [E, Nc, Kd]")
+    E, Nc, Kd = w.shape
+    if layout == EP_LAYOUT_MASKED:
+        rows = E * cap
+    else:
+        rows = x_rows if row_src is None else row_src.numel()
+    if out is None:
+        out = _empty((rows, Nc), out_dtype, x)
+    elif out.numel() != rows * Nc:
+        raise EPError(f"out must hold {rows} x {Nc} elements")
+    dt = _float_type(out, "out")
+    _check("ep_expert_matmul_fp8", lib().ep_expert_matmul_fp8(
+        _codes(x, "x", (x_rows, Kd)),
+        _dev(x_scales, torch.float32, "x_scales", (x_rows, scale_blocks(Kd))), x_rows,
+        _codes(w, "w"),
+        _dev(w_scales, torch.float32, "w_scales", (E, scale_blocks(Nc), scale_blocks(Kd))), E, Nc,
+        Kd, _dev(expert_offsets, torch.int32, "expert_offsets", (E + 1,)), layout, cap, rows,
+        _opt(row_src, torch.int32, "row_src"), 0 if row_src is None else row_src.numel(), dt,
+        _dev(out, out.dtype, "out"), _opt(status, torch.int32, "status", (1,)), _stream(stream)))
+    return out
+
+
+Norm = namedtuple("Norm", "y residual q scales rstd")
+
+
+def alloc_norm(rows, cols, dtype, device, y=True, residual=False, codes=False, rstd=False) -> Norm:
+    """Outputs of ep_rms_norm, None for those that are not wanted."""
+    def z(on, shape, t):
+        return torch.empty(shape, dtype=t, device=device) if on else None
+    return Norm(z(y, (rows, cols), dtype), z(residual, (rows, cols), dtype),
+                z(codes, (rows, cols), torch.uint8),
+                z(codes, (rows, scale_blocks(cols)), torch.float32), z(rstd, (rows,), torch.float32))
+
+
+def ep_rms_norm(x, weight, residual=None, eps=1e-6, out: Norm | None = None, stream=None) -> Norm:
+    """Root-mean-square norm of x (+ residual), rows bf16 or float32 [rows, cols],
+    weight bf16 or float32 [cols].  Writes the outputs that `out` holds
+    (alloc_norm): y, residual (the sum, in the rows' type), q and scales (the E4M3
+    codes of y), rstd float32 [rows].  Without `out`: y, rstd and, with a residual,
+    the sum."""
+    rows, cols = _rows2d(x, "x")
+    dt, wt = _float_type(x, "x"), _float_type(weight, "weight")
+    if out is None:
+        out = alloc_norm(rows, cols, x.dtype, x.device, residual=residual is not None, rstd=True)
+    shape = (rows, cols)
+    _check("ep_rms_norm", lib().ep_rms_norm(
+        _dev(x, x.dtype, "x"), dt, _opt(residual, x.dtype, "residual", shape),
+        _dev(weight, weight.dtype, "weight", (cols,)), wt, rows, cols, eps,
+        _opt(out.residual, x.dtype, "out.residual", shape), _opt(out.y, x.dtype, "out.y", shape),
+        None if out.q is None else _codes(out.q, "out.q", shape),
+        _opt(out.scales, torch.float32, "out.scales", (rows, scale_blocks(cols))),
+        _opt(out.rstd, torch.float32, "out.rstd", (rows,)), _stream(stream)))
+    return out
+
+
+def ep_rms_norm_backward_workspace_size(rows, cols) -> int:
+    return int(lib().ep_rms_norm_backward_workspace_size(rows, cols))
+
+
+def ep_rms_norm_backward(d_y, z, weight, rstd, d_residual=None, d_x=None, d_weight=None,
+                         weight_grad=True, workspace=None, stream=None):
+    """Gradients of ep_rms_norm's y: z (its residual output, or x where it had no
+    residual) and rstd are what the forward call kept.  Returns (d_x of the rows'
+    type: the gradient of x and of the residual, with d_residual added; d_weight
+    float32 [cols], None with weight_grad=False)."""
+    rows, cols = _rows2d(z, "z")
+    dt, wt = _float_type(z, "z"), _float_type(weight, "weight")
+    shape = (rows, cols)
+    if d_x is None:
+        d_x = torch.empty_like(z)
+    if not weight_grad:
+        d_weight = workspace = None
+    else:
+        if d_weight is None:
+            d_weight = _empty((cols,), torch.float32, z)
+        if workspace is None:
+            workspace = _empty((ep_rms_norm_backward_workspace_size(rows, cols),), torch.uint8, z)
+            if stream is not None and workspace.is_cuda:
+                workspace.record_stream(stream)
+    _check("ep_rms_norm_backward", lib().ep_rms_norm_backward(
+        _dev(d_y, z.dtype, "d_y", shape), dt, _dev(z, z.dtype, "z"),
+        _dev(weight, weight.dtype, "weight", (cols,)), wt,
+        _dev(rstd, torch.float32, "rstd", (rows,)), _opt(d_residual, z.dtype, "d_residual", shape),
+        rows, cols, _dev(d_x, z.dtype, "d_x", shape),
+        _opt(d_weight, torch.float32, "d_weight", (cols,)),
+        _opt(workspace, torch.uint8, "workspace"),
+        0 if workspace is None else workspace.numel(), _stream(stream)))
+    return d_x, d_weight
+
 
 
 def ep_selftest_wait_timeout(stream=None):

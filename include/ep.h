@@ -473,6 +473,138 @@ ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_r
                              ep_dtype_t out_dtype, void* out, int32_t* status, void* stream);
 
 /*
+ * ep_quantize_blocks -- rows to E4M3 codes with one scale for every 128 columns,
+ * the form that ep_dispatch writes (EP_DTYPE_FP8_E4M3_B128) and
+ * ep_expert_matmul_fp8 reads; an addition of this library.
+ *   v      = x (EP_ACT_NONE), or silu(x[:cols]) * x[cols:] (EP_ACT_SWIGLU, x
+ *            rows of 2*cols: the experts' first product, gate half first), in
+ *            float32.
+ *   scale  = max|v| / 448 over a block of 128 columns (a row's last block may be
+ *            shorter); 1 where that quotient is 0.  code = E4M3(v / scale),
+ *            rounded to nearest even; quotients by IEEE division, so that
+ *            EP_ACT_NONE of bf16 rows gives ep_dispatch's codes.  A NaN takes no
+ *            part in the maximum and is a NaN as a code; a block with an infinity
+ *            gets the scale infinity and stands for NaN throughout.
+ *   x      [rows, cols or 2*cols] float32 or bf16, 16-byte aligned.
+ *   expert_offsets, E, layout, cap   as for ep_quantize_rows: rows that hold no
+ *            token are neither read nor written.
+ *   q      uint8 [rows, cols], 16-byte aligned; scales float32 [rows,
+ *            ceil(cols / 128)].
+ *   x_q, x_scales   NULL, or (EP_ACT_SWIGLU) the codes of x itself, uint8 [rows,
+ *            2*cols] and float32 [rows, ceil(2*cols / 128)]: the activation's
+ *            checkpoint, as EP_ACT_NONE of x would write it.
+ * cols is a multiple of 16; rows times the blocks of a row of x is below 2^31.
+ */
+ep_status_t ep_quantize_blocks(const void* x, ep_dtype_t x_dtype, ep_act_t act, int32_t rows,
+                               int32_t cols, const int32_t* expert_offsets, int32_t E,
+                               ep_layout_t layout, int32_t cap, uint8_t* q, float* scales,
+                               uint8_t* x_q, float* x_scales, void* stream);
+
+/*
+ * ep_dequantize_blocks -- the values that such codes stand for: out = code * scale
+ * in float32, rounded to out's type.  Arguments as above; rows that hold no token
+ * are neither read nor written.
+ *   out    [rows, cols] float32 or bf16 (out_dtype), 16-byte aligned.
+ */
+ep_status_t ep_dequantize_blocks(const uint8_t* q, const float* scales, int32_t rows, int32_t cols,
+                                 const int32_t* expert_offsets, int32_t E, ep_layout_t layout,
+                                 int32_t cap, ep_dtype_t out_dtype, void* out, void* stream);
+
+/*
+ * ep_swiglu_backward -- gradient of silu(g) * u with respect to x = (g, u), from
+ * x itself or from its 8-bit checkpoint:
+ *   d_g = d_out * u * s * (1 + g * (1 - s)),  d_u = d_out * g * s,
+ *   s = 1 / (1 + exp(-g)), in float32, rounded once to the rows' type.
+ *   d_out  [rows, cols] float32 or bf16 (dtype).
+ *   x      x_scales NULL: rows [rows, 2*cols] of the same type.  Else: uint8
+ *          codes [rows, 2*cols] with x_scales float32 [rows, ceil(2*cols / 128)]
+ *          (ep_quantize_blocks's x_q and x_scales).
+ *   expert_offsets, E, layout, cap   as above.
+ *   d_x    [rows, 2*cols] of the same type; may be x where x holds rows, and
+ *          overlaps no input otherwise.
+ * d_out, x and d_x are 16-byte aligned; cols is a multiple of 16.
+ */
+ep_status_t ep_swiglu_backward(const void* d_out, ep_dtype_t dtype, const void* x,
+                               const float* x_scales, int32_t rows, int32_t cols,
+                               const int32_t* expert_offsets, int32_t E, ep_layout_t layout,
+                               int32_t cap, void* d_x, void* stream);
+
+/*
+ * ep_expert_matmul_fp8 -- every expert's product of its rows with its own weights,
+ * in E4M3 codes with a scale for every 128 columns of a row and for every 128 x
+ * 128 block of a weight; an addition of this library, which reads what
+ * ep_dispatch (EP_DTYPE_FP8_E4M3_B128), ep_quantize_blocks and ep_rms_norm write.
+ *   out[r, n] = sum_b x_scales[s, b] * w_scales[e, n / 128, b] *
+ *               sum_{k in block b} x[s, k] * w[e, n, k]
+ * A block's sum is held in the float32 accumulators of the tensor cores; its
+ * product with the two scales and the sum over the blocks are float32, and the
+ * output is rounded once to its type.  A NaN code makes every output of its row
+ * (or channel) NaN.
+ *   x       uint8 [x_rows, Kd] with x_scales float32 [x_rows, ceil(Kd / 128)].
+ *   w       uint8 [E, Nc, Kd] with w_scales float32 [E, ceil(Nc / 128),
+ *           ceil(Kd / 128)].
+ *   Rows, layouts, row_src, out, status and limits are ep_expert_matmul's: rows
+ *   that hold no token are not written, a row_src outside [0, x_rows) gives a
+ *   row of zeros.
+ */
+ep_status_t ep_expert_matmul_fp8(const uint8_t* x, const float* x_scales, int32_t x_rows,
+                                 const uint8_t* w, const float* w_scales, int32_t E, int32_t Nc,
+                                 int32_t Kd, const int32_t* expert_offsets, ep_layout_t layout,
+                                 int32_t cap, int32_t rows, const int32_t* row_src, int32_t n_src,
+                                 ep_dtype_t out_dtype, void* out, int32_t* status, void* stream);
+
+/*
+ * ep_rms_norm -- root-mean-square norm of rows, with the residual's addition
+ * before it and the experts' codes behind it; an addition of this library.
+ *   z      = x + residual, rounded to the rows' type (x without a residual).
+ *   r      = 1 / sqrt(mean(z^2) + eps)
+ *   y      = z * r * weight, in float32 from the rounded z.
+ *   x, residual (or NULL)   [rows, cols] float32 or bf16 (dtype).
+ *   weight [cols] float32 or bf16 (weight_dtype).
+ *   Outputs, each NULL where it is not wanted (one at least is):
+ *   residual_out  z, of the rows' type.
+ *   y             of the rows' type.
+ *   q, scales     E4M3 codes uint8 [rows, cols] of the float32 y and their scales
+ *                 float32 [rows, ceil(cols / 128)], as ep_quantize_blocks makes
+ *                 them (both or neither).
+ *   rstd          r, float32 [rows], for ep_rms_norm_backward.
+ * An output of the rows' type may be x or residual itself; nothing else overlaps.
+ * The sum of squares is float32: rows whose mean square passes its range (values
+ * from some 1e19 on) have r = 0.  eps is above 0 and finite.  Rows, weight and q
+ * are 16-byte aligned; cols is a multiple of 16, at most 16384.
+ */
+ep_status_t ep_rms_norm(const void* x, ep_dtype_t dtype, const void* residual, const void* weight,
+                        ep_dtype_t weight_dtype, int32_t rows, int32_t cols, float eps,
+                        void* residual_out, void* y, uint8_t* q, float* scales, float* rstd,
+                        void* stream);
+
+/* Bytes of device workspace ep_rms_norm_backward needs where d_weight is wanted
+ * (a multiple of 256).  Depends on the current device's number of SMs. */
+size_t ep_rms_norm_backward_workspace_size(int32_t rows, int32_t cols);
+
+/*
+ * ep_rms_norm_backward -- gradients of y = z * r * weight; with n = z * r and
+ * g = d_y * weight, in float32:
+ *   d_x      = r * (g - n * mean(g * n)) + d_residual, rounded once to the rows'
+ *              type: the gradient of x and of the residual alike.
+ *   d_weight = sum over the rows of d_y * n, in float32 and in a fixed order for
+ *              these sizes on this device (NULL: not wanted).
+ *   d_y, z, d_residual (or NULL: no gradient comes along the residual), d_x
+ *              [rows, cols] float32 or bf16 (dtype), 16-byte aligned; z is
+ *              ep_rms_norm's residual_out (x where it had no residual).
+ *   rstd       float32 [rows], the forward call's.
+ *   d_weight   float32 [cols]; rows == 0 gives zeros.
+ *   workspace  where d_weight is wanted: ep_rms_norm_backward_workspace_size
+ *              bytes, 16-byte aligned, no initialisation needed.
+ * d_x may be d_y, z or d_residual itself; nothing else overlaps.  Sizes as for
+ * ep_rms_norm.
+ */
+ep_status_t ep_rms_norm_backward(const void* d_y, ep_dtype_t dtype, const void* z,
+                                 const void* weight, ep_dtype_t weight_dtype, const float* rstd,
+                                 const void* d_residual, int32_t rows, int32_t cols, void* d_x,
+                                 float* d_weight, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * ep_host_pipeline_* -- no counterpart in the source pages: the path for
  * callers whose inputs and results live in host memory.  Each step copies the
  * step's logits, rank offsets, tokens x and expert outputs y in, runs
