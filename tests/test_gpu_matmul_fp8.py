@@ -108,6 +108,27 @@ def test_exact_sums_masked(counts, Nc, Kd, cap, gather):
                         layout=MASKED))
 
 
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,Nc,Kd,cap", [
+    ([300, 1, 0, 129] * 12, 1000, 272, 0),  # tiles for every SM, of an expert's rows in even parts
+    ([257] * 30, 1544, 112, 0),             # one block of K a tile
+    ([128, 200, 40, 260] * 20, 520, 656, 256),
+    ([100] * 40, 1023, 144, 0),             # rows of out that start anywhere
+])
+def test_exact_sums_of_many_tiles(counts, Nc, Kd, cap, gather):
+    check_exact(problem(counts, Nc, Kd, Nc + cap + 1, True, x_rows=500 if gather else None, cap=cap,
+                        layout=MASKED if cap else CONTIG))
+    if not gather:
+        check_near(problem(counts, Nc, Kd, Nc + cap + 2, False, cap=cap, layout=MASKED if cap else CONTIG), BF)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+def test_exact_sums_of_many_units_of_one_block(gather):
+    """Several units a CTA, each over before the stages of the next are handed on."""
+    check_exact(problem([5, 0, 9, 1] * 50, 2100, 128, 15, True, x_rows=31 if gather else None))
+    check_exact(problem([3] * 100, 2100, 208, 16, True, x_rows=31 if gather else None))
+
+
 @pytest.mark.parametrize("out", [BF, F32])
 @pytest.mark.parametrize("counts,Nc,Kd", [([2, 0, 1], 130, 272), ([300, 40], 392, 1168),
                                           ([20] * 9, 257, 784), ([1], 64, 7168), ([70, 700], 264, 2064)])
@@ -126,6 +147,17 @@ def test_rows_that_read_nothing_are_zeros():
     p = problem([3, 2], 40, 64, 4, True, x_rows=5)
     p["x"], p["xs"] = p["x"][:0], p["xs"][:0]
     assert (run(p) == 0).all()
+
+
+def test_scales_that_start_on_four_bytes():
+    p = problem([70, 140], 136, 1024, 14, True)
+    for name in ("xs", "ws"):
+        t = p[name]
+        p[name] = torch.cat([torch.zeros(1), t.flatten()]).cuda()[1:].view(t.shape)
+    got = run(p).double().cpu().numpy()
+    p["xs"], p["ws"] = p["xs"].cpu(), p["ws"].cpu()
+    want, _, _ = want_of(p)
+    np.testing.assert_array_equal(got, want)
 
 
 def test_fewer_sources_than_rows():
