@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(BlockQuantArg
     for (int j = 0; j < kVec; ++j) v[j] = u[j] = 0.0f;
     if (on) {
         const T* row = static_cast<const T*>(a.x) + r * (SWIGLU ? 2 * (size_t)a.cols : (size_t)a.cols) + p.col;
-        load16<true>(row, v);
-        if constexpr (SWIGLU) load16<true>(row + a.cols, u);
+        load16<true>(row, v, a.wide);
+        if constexpr (SWIGLU) load16<true>(row + a.cols, u, a.wide);
     }
     float scale;
     if constexpr (KEEP) {
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_blocks_kernel(BlockRestor
     const uint4 q = __ldcs(reinterpret_cast<const uint4*>(a.q + r * a.cols + p.col));
     float v[kVec];
     decode16(q, __ldg(a.scales + r * blocks + p.col / kScaleBlock), v);
-    store16(static_cast<T*>(a.out) + r * a.cols + p.col, v);
+    store16(static_cast<T*>(a.out) + r * a.cols + p.col, v, a.wide);
 }
 
 template <typename T, bool CODES>
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluGradArg
     if (p.row >= (uint32_t)a.rows || !holds_token(a.tokens, p.row)) return;
     const size_t r = p.row, wide = 2 * (size_t)a.cols;
     float g[kVec], u[kVec], d[kVec];
-    load16<true>(static_cast<const T*>(a.d_out) + r * a.cols + p.col, d);
+    load16<true>(static_cast<const T*>(a.d_out) + r * a.cols + p.col, d, a.wide);
     if constexpr (CODES) {
         const uint8_t* q = static_cast<const uint8_t*>(a.x) + r * wide + p.col;
         const float* s = a.x_scales + r * scale_blocks(2 * a.cols);
@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluGradArg
         decode16(uq, __ldg(s + (a.cols + p.col) / kScaleBlock), u);
     } else {
         const T* x = static_cast<const T*>(a.x) + r * wide + p.col;
-        load16<true>(x, g);
-        load16<true>(x + a.cols, u);
+        load16<true>(x, g, a.wide);
+        load16<true>(x + a.cols, u, a.wide);
     }
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluGradArg
         u[j] = up;
     }
     T* out = static_cast<T*>(a.d_x) + r * wide + p.col;
-    store16(out, g);
-    store16(out + a.cols, u);
+    store16(out, g, a.wide);
+    store16(out + a.cols, u, a.wide);
 }
 
 template <typename Args>
@@ -168,20 +168,26 @@ cudaError_t quantize_t(const BlockQuantArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_quantize_blocks(const BlockQuantArgs& a, cudaStream_t s) {
-    if (a.rows == 0) return cudaSuccess;
+cudaError_t launch_quantize_blocks(const BlockQuantArgs& args, cudaStream_t s) {
+    if (args.rows == 0) return cudaSuccess;
+    BlockQuantArgs a = args;
+    a.wide = aligned32(a.x);
     return a.bf16 ? quantize_t<__nv_bfloat16>(a, s) : quantize_t<float>(a, s);
 }
 
-cudaError_t launch_dequantize_blocks(const BlockRestoreArgs& a, cudaStream_t s) {
-    if (a.rows == 0) return cudaSuccess;
+cudaError_t launch_dequantize_blocks(const BlockRestoreArgs& args, cudaStream_t s) {
+    if (args.rows == 0) return cudaSuccess;
+    BlockRestoreArgs a = args;
+    a.wide = aligned32(a.out);
     const uint64_t pieces = a.cols / kVec;
     return a.bf16 ? run(dequantize_blocks_kernel<__nv_bfloat16>, a, pieces, s)
                   : run(dequantize_blocks_kernel<float>, a, pieces, s);
 }
 
-cudaError_t launch_swiglu_backward(const SwigluGradArgs& a, cudaStream_t s) {
-    if (a.rows == 0) return cudaSuccess;
+cudaError_t launch_swiglu_backward(const SwigluGradArgs& args, cudaStream_t s) {
+    if (args.rows == 0) return cudaSuccess;
+    SwigluGradArgs a = args;
+    a.wide = aligned32(a.d_out, a.d_x, a.x_scales == nullptr ? a.x : nullptr);
     const uint64_t pieces = a.cols / kVec;
     if (a.x_scales != nullptr)
         return a.bf16 ? run(swiglu_backward_kernel<__nv_bfloat16, true>, a, pieces, s)

@@ -244,6 +244,7 @@ struct BlockQuantArgs {
     uint8_t* x_q;               // or nullptr: codes of x itself (SwiGLU)
     float* x_scales;
     int rows, cols, swiglu, bf16;
+    int wide;                   // set by the launcher: rows start on 32 bytes
 };
 cudaError_t launch_quantize_blocks(const BlockQuantArgs& a, cudaStream_t s);
 
@@ -253,6 +254,7 @@ struct BlockRestoreArgs {
     TokenRows tokens;
     void* out;
     int rows, cols, bf16;
+    int wide;                   // as in BlockQuantArgs
 };
 cudaError_t launch_dequantize_blocks(const BlockRestoreArgs& a, cudaStream_t s);
 
@@ -263,6 +265,7 @@ struct SwigluGradArgs {
     TokenRows tokens;
     void* d_x;
     int rows, cols, bf16;
+    int wide;                   // as in BlockQuantArgs
 };
 cudaError_t launch_swiglu_backward(const SwigluGradArgs& a, cudaStream_t s);
 
@@ -284,6 +287,7 @@ struct NormArgs {
     float* rstd;
     float eps;
     int rows, cols, bf16, weight_bf16;
+    int wide;                   // as in BlockQuantArgs (weight too)
 };
 cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
 
@@ -297,6 +301,7 @@ struct NormGradArgs {
     float* d_weight;            // or nullptr
     float* partial;             // [blocks, cols], where d_weight is given
     int rows, cols, bf16, weight_bf16;
+    int wide;                   // as in NormArgs
 };
 // Blocks of the kernel that sums the weight's gradient, each with a partial sum.
 int norm_grad_blocks(int rows, int cols);

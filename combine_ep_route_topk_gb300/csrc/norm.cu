@@ -21,28 +21,29 @@ namespace {
 
 using namespace rows;
 
-// Sum over the row's threads: whole warps, nt of them (NT at most), one warp
-// without shared memory.  s_part: NT / 32 floats that nothing else uses until the
-// block's next barrier but one.
+// Sum over the row's threads: NT of them where that is a warp or a part of one
+// (a power of two), else nt <= NT in whole warps, whose partial sums meet in
+// s_part (NT / 32 floats that nothing else uses until the block's next barrier but
+// one); barrier `bar` counts nt threads.
 template <int NT>
-__device__ __forceinline__ float row_sum(float v, int nt, float* s_part) {
+__device__ __forceinline__ float row_sum(float v, int nt, int tid, int bar, float* s_part) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    for (int off = (NT < 32 ? NT : 32) / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
     if constexpr (NT > 32) {
-        if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = 0.0f;
+        if ((tid & 31) == 0) s_part[tid >> 5] = v;
+        asm volatile("barrier.sync %0, %1;" ::"r"(bar), "r"(nt) : "memory");
+        const int w = tid & (NT / 32 - 1);  // each NT / 32 lanes join all the warps' sums
+        v = w * 32 < nt ? s_part[w] : 0.0f;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w)
-            if (w * 32 < nt) v += s_part[w];
+        for (int off = NT / 64; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
     }
     return v;
 }
 
 template <bool STREAM>
 __device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)[kVec]) {
-    if (a.weight_bf16) load16<STREAM>(static_cast<const __nv_bfloat16*>(a.weight) + c, w);
-    else load16<STREAM>(static_cast<const float*>(a.weight) + c, w);
+    if (a.weight_bf16) load16<STREAM>(static_cast<const __nv_bfloat16*>(a.weight) + c, w, a.wide);
+    else load16<STREAM>(static_cast<const float*>(a.weight) + c, w, a.wide);
 }
 
 __device__ __forceinline__ float rounded(float v, const __nv_bfloat16*) {
@@ -50,17 +51,17 @@ __device__ __forceinline__ float rounded(float v, const __nv_bfloat16*) {
 }
 __device__ __forceinline__ float rounded(float v, const float*) { return v; }
 
-// Up to NT threads a row, whole warps, HELD vectors of 16 each; ROWS rows a block
-// (more than 1: a warp each).
+// Up to NT threads a row, HELD vectors of 16 each: whole warps and a row a block
+// (ROWS = 1), or NT = 8, 16 or 32 threads and ROWS rows a block.
 template <typename T, int NT, int ROWS, int HELD>
 __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
-    static_assert(ROWS == 1 || NT == 32, "a warp per row");
-    __shared__ float s_part[NT / 32];
+    static_assert(ROWS == 1 || NT <= 32, "a warp or a part of one for each of several rows");
+    __shared__ float s_part[(NT + 31) / 32];
     pdl_prologue();
     const int nt = ROWS > 1 ? NT : (int)blockDim.x;
     const int tid = ROWS > 1 ? (int)threadIdx.x % NT : (int)threadIdx.x;
     const long long r = (long long)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / NT : 0);
-    if (r >= a.rows) return;  // a whole warp, or none of the block
+    const int cols = r < a.rows ? a.cols : 0;  // past the last row, lanes only take part in sums
     const size_t at = (size_t)r * a.cols;
     const T* x = static_cast<const T*>(a.x) + at;
     const T* res = a.residual != nullptr ? static_cast<const T*>(a.residual) + at : nullptr;
@@ -71,11 +72,11 @@ __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
         const int c = (i * nt + tid) * kVec;
 #pragma unroll
         for (int j = 0; j < kVec; ++j) z[i][j] = 0.0f;
-        if (c < a.cols) {
-            load16<true>(x + c, z[i]);
+        if (c < cols) {
+            load16<true>(x + c, z[i], a.wide);
             if (res != nullptr) {
                 float t[kVec];
-                load16<true>(res + c, t);
+                load16<true>(res + c, t, a.wide);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) z[i][j] = rounded(z[i][j] + t[j], x);
             }
@@ -88,28 +89,28 @@ __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             const int c = (i * nt + tid) * kVec;
-            if (c < a.cols) store16(to + c, z[i]);
+            if (c < cols) store16(to + c, z[i], a.wide);
         }
     }
-    sum = row_sum<NT>(sum, nt, s_part);
+    sum = row_sum<NT>(sum, nt, tid, 0, s_part);
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)a.cols) + a.eps));
-    if (tid == 0 && a.rstd != nullptr) a.rstd[r] = rstd;
+    if (tid == 0 && cols > 0 && a.rstd != nullptr) a.rstd[r] = rstd;
     if (a.y == nullptr && a.q == nullptr) return;
     const int blocks = scale_blocks(a.cols);
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
         const int c = (i * nt + tid) * kVec;
-        if (c < a.cols) {
+        if (c < cols) {
             float w[kVec];
             load_weight<false>(a, c, w);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) z[i][j] = z[i][j] * rstd * w[j];
-            if (a.y != nullptr) store16(static_cast<T*>(a.y) + at + c, z[i]);
+            if (a.y != nullptr) store16(static_cast<T*>(a.y) + at + c, z[i], a.wide);
         }
         if (a.q != nullptr) {  // every lane takes part in the blocks' maxima
             float scale;
             const uint4 codes = encode16(z[i], scale);
-            if (c < a.cols) {
+            if (c < cols) {
                 *reinterpret_cast<uint4*>(a.q + at + c) = codes;
                 if (c % kScaleBlock == 0) a.scales[(size_t)r * blocks + c / kScaleBlock] = scale;
             }
@@ -127,6 +128,8 @@ cudaError_t norm_shape(const NormArgs& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
+    if (a.cols <= 128) return norm_shape<T, 8, 32, 1>(a, s);
+    if (a.cols <= 256) return norm_shape<T, 16, 16, 1>(a, s);
     if (a.cols <= 512) return norm_shape<T, 32, 8, 1>(a, s);
     if (a.cols <= 1024) return norm_shape<T, 32, 4, 2>(a, s);
     if (a.cols <= 4096) return norm_shape<T, 256, 1, 1>(a, s);
@@ -136,114 +139,139 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
 
 // ---- gradient --------------------------------------------------------------------
 
-constexpr int kGradVec = 8;
-constexpr int kGradWarps = 8;  // warps of a block whose warps take a row each
+constexpr int kGradThreads = 512;  // of a block, one block an SM
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[kGradVec]) {
-    unpack8(__ldcs(reinterpret_cast<const uint4*>(p)), v);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[kGradVec]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[kGradVec]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[kGradVec]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store16f(float* p, const float (&v)[kVec]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
-template <typename T, int NT, int ROWS, int HELD>
-__global__ void __launch_bounds__(NT * ROWS) rms_norm_backward_kernel(NormGradArgs a) {
-    static_assert(ROWS == 1 || NT == 32, "a warp per row");
-    __shared__ float s_part[2][NT / 32];
-    extern __shared__ float s_dw[];  // ROWS > 1: [ROWS][cols]
+// Sixteen columns as they lie in memory.
+template <typename T>
+struct Raw {
+    uint32_t r[kVec * sizeof(T) / 32][8];
+    __device__ __forceinline__ void load(const T* p, bool wide) {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h) load32<true>(p + h * (32 / sizeof(T)), r[h], wide);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[h][i] = 0;
+    }
+    __device__ __forceinline__ float at(int j) const {
+        if (sizeof(T) == 4) return __uint_as_float(r[j / 8][j % 8]);
+        return j % 2 ? hi_of(r[0][j / 2]) : lo_of(r[0][j / 2]);
+    }
+};
+
+// How the threads share the rows: nt threads a row, `groups` rows at a time in a block.
+struct GradShape {
+    int nt, groups, blocks;
+};
+int grad_held(int cols) { return cols <= kGradThreads * kVec ? 1 : 2; }
+GradShape grad_shape(int rows, int cols) {
+    GradShape g;
+    const int vectors = cols / kVec, held = grad_held(cols);
+    g.nt = ((vectors + held - 1) / held + 31) / 32 * 32;
+    g.groups = kGradThreads / g.nt;
+    if (g.nt > 32) g.groups = std::min(g.groups, 15);  // a barrier each, and one for the block
+    g.blocks = (int)std::min<long long>(sm_count(), ((long long)rows + g.groups - 1) / g.groups);
+    return g;
+}
+
+// A row's three arrays load together, and where the registers allow it (HELD = 1) while
+// the row before is worked on.
+template <typename T, int HELD>
+__global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_kernel(NormGradArgs a, GradShape g) {
+    extern __shared__ __align__(16) float s_dw[];  // [groups][cols], for more than one group
+    __shared__ float s_part[2][kGradThreads / 32];
+    constexpr bool kAhead = HELD == 1;
     pdl_prologue();
-    const int nt = ROWS > 1 ? NT : (int)blockDim.x;
-    const int tid = ROWS > 1 ? (int)threadIdx.x % NT : (int)threadIdx.x;
-    const int sub = ROWS > 1 ? (int)threadIdx.x / NT : 0;
-    float dw[HELD][kGradVec];
+    const int nt = g.nt, group = (int)threadIdx.x / nt, tid = (int)threadIdx.x % nt;
+    const bool has_res = a.d_residual != nullptr, wide = a.wide;
+    const int first = (int)blockIdx.x * g.groups + group, step = (int)gridDim.x * g.groups;
+    Raw<T> z[HELD], dy[HELD], res[HELD];
+    float rstd = 0.0f;
+    const auto load = [&](size_t r) {
+        rstd = __ldg(a.rstd + r);
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int c = (i * nt + tid) * kVec;
+            z[i].zero();
+            dy[i].zero();
+            res[i].zero();
+            if (c < a.cols) {
+                const size_t at = r * a.cols + c;
+                z[i].load(static_cast<const T*>(a.z) + at, wide);
+                dy[i].load(static_cast<const T*>(a.d_y) + at, wide);
+                if (has_res) res[i].load(static_cast<const T*>(a.d_residual) + at, wide);
+            }
+        }
+    };
+    float dw[HELD][kVec];
 #pragma unroll
     for (int i = 0; i < HELD; ++i)
 #pragma unroll
-        for (int j = 0; j < kGradVec; ++j) dw[i][j] = 0.0f;
+        for (int j = 0; j < kVec; ++j) dw[i][j] = 0.0f;
     int turn = 0;
-    for (long long r = (long long)blockIdx.x * ROWS + sub; r < a.rows; r += (long long)gridDim.x * ROWS) {
-        const size_t at = (size_t)r * a.cols;
-        const float rstd = __ldg(a.rstd + r);
-        float n[HELD][kGradVec], g[HELD][kGradVec];
+    if (kAhead && first < a.rows) load(first);
+    for (long long r = first; r < a.rows; r += step) {
+        if (!kAhead) load(r);
+        float n[HELD][kVec], gy[HELD][kVec];
+        Raw<T> d[HELD];
+        const float scale = rstd;
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
-            const int c = (i * nt + tid) * kGradVec;
-            if (c < a.cols) {
-                load8(static_cast<const T*>(a.z) + at + c, n[i]);
-                load8(static_cast<const T*>(a.d_y) + at + c, g[i]);
-            } else {
+            const int c = min((i * nt + tid) * kVec, a.cols - kVec);  // idle threads hold zeros
+            float w[kVec];
+            if (a.weight_bf16) load16<false>(static_cast<const __nv_bfloat16*>(a.weight) + c, w, wide);
+            else load16<false>(static_cast<const float*>(a.weight) + c, w, wide);
 #pragma unroll
-                for (int j = 0; j < kGradVec; ++j) n[i][j] = g[i][j] = 0.0f;
+            for (int j = 0; j < kVec; ++j) {
+                n[i][j] = z[i].at(j) * scale;
+                gy[i][j] = dy[i].at(j);
+                dw[i][j] = fmaf(gy[i][j], n[i][j], dw[i][j]);
+                gy[i][j] *= w[j];
+                sum = fmaf(gy[i][j], n[i][j], sum);
             }
+            d[i] = res[i];
         }
-#pragma unroll
-        for (int i = 0; i < HELD; ++i) {
-            const int c = (i * nt + tid) * kGradVec;
-            if (c < a.cols) {
-                float w[kGradVec];
-                if (a.weight_bf16) {
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.weight) + c)), w);
-                } else {
-                    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c);
-                    const float4 lo = __ldg(p), hi = __ldg(p + 1);
-                    w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
-                    w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
-                }
-#pragma unroll
-                for (int j = 0; j < kGradVec; ++j) {
-                    n[i][j] *= rstd;
-                    dw[i][j] = fmaf(g[i][j], n[i][j], dw[i][j]);
-                    g[i][j] *= w[j];
-                    sum = fmaf(g[i][j], n[i][j], sum);
-                }
-            }
-        }
+        if (kAhead && r + step < a.rows) load(r + step);
         // two buffers in turn: a warp may be one row ahead of another
-        sum = row_sum<NT>(sum, nt, s_part[turn]);
+        if (nt == 32) sum = row_sum<32>(sum, nt, tid, 0, nullptr);
+        else sum = row_sum<kGradThreads>(sum, nt, tid, group + 1, s_part[turn] + group * (nt >> 5));
         turn ^= 1;
         const float mean = __fdiv_rn(sum, (float)a.cols);
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
-            const int c = (i * nt + tid) * kGradVec;
-            if (c < a.cols) {
-                float d[kGradVec];
+            const int c = (i * nt + tid) * kVec;
 #pragma unroll
-                for (int j = 0; j < kGradVec; ++j) d[j] = 0.0f;
-                if (a.d_residual != nullptr) load8(static_cast<const T*>(a.d_residual) + at + c, d);
-#pragma unroll
-                for (int j = 0; j < kGradVec; ++j) d[j] = fmaf(rstd, fmaf(-n[i][j], mean, g[i][j]), d[j]);
-                store8(static_cast<T*>(a.d_x) + at + c, d);
-            }
+            for (int j = 0; j < kVec; ++j) n[i][j] = fmaf(scale, fmaf(-n[i][j], mean, gy[i][j]), d[i].at(j));
+            if (c < a.cols) store16(static_cast<T*>(a.d_x) + (size_t)r * a.cols + c, n[i], wide);
         }
     }
     if (a.d_weight == nullptr) return;
     float* to = a.partial + (size_t)blockIdx.x * a.cols;
-    if constexpr (ROWS > 1) {
+    if (g.groups > 1) {
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
-            const int c = (i * nt + tid) * kGradVec;
-            if (c < a.cols) store8(s_dw + (size_t)sub * a.cols + c, dw[i]);
+            const int c = (i * nt + tid) * kVec;
+            if (c < a.cols) store16f(s_dw + (size_t)group * a.cols + c, dw[i]);
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < a.cols; c += NT * ROWS) {
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
             float v = 0.0f;
-            for (int k = 0; k < ROWS; ++k) v += s_dw[(size_t)k * a.cols + c];
+            for (int k = 0; k < g.groups; ++k) v += s_dw[(size_t)k * a.cols + c];
             to[c] = v;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
-            const int c = (i * nt + tid) * kGradVec;
-            if (c < a.cols) store8(to + c, dw[i]);
+            const int c = (i * nt + tid) * kVec;
+            if (c < a.cols) store16f(to + c, dw[i]);
         }
     }
 }
@@ -265,46 +293,42 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(NormGradArgs a, int p
     if (lane == 0 && blockIdx.x * 32 + strand < (unsigned)a.cols) a.d_weight[blockIdx.x * 32 + strand] = v;
 }
 
-template <typename T, int NT, int ROWS, int HELD>
-cudaError_t grad_shape(const NormGradArgs& a, cudaStream_t s) {
-    const int vectors = (a.cols + kGradVec - 1) / kGradVec;
-    const int nt = ROWS > 1 ? NT : std::min(NT, ((vectors + HELD - 1) / HELD + 31) / 32 * 32);
-    const size_t smem = ROWS > 1 ? (size_t)ROWS * a.cols * sizeof(float) : 0;
-    return launch(rms_norm_backward_kernel<T, NT, ROWS, HELD>, dim3(norm_grad_blocks(a.rows, a.cols)),
-                  dim3(nt * ROWS), smem, s, a);
-}
-
 template <typename T>
-cudaError_t grad_t(const NormGradArgs& a, cudaStream_t s) {
-    if (a.cols <= 256) return grad_shape<T, 32, kGradWarps, 1>(a, s);
-    if (a.cols <= 512) return grad_shape<T, 32, kGradWarps, 2>(a, s);
-    if (a.cols <= 2048) return grad_shape<T, 256, 1, 1>(a, s);
-    if (a.cols <= 4096) return grad_shape<T, 256, 1, 2>(a, s);
-    if (a.cols <= 8192) return grad_shape<T, 512, 1, 2>(a, s);
-    return grad_shape<T, 512, 1, 4>(a, s);
+cudaError_t grad_t(const NormGradArgs& a, const GradShape& g, cudaStream_t s) {
+    // at most 512 threads of 16 columns: 32 KB
+    const size_t smem = g.groups > 1 ? (size_t)g.groups * a.cols * sizeof(float) : 0;
+    const dim3 grid(g.blocks), block(g.nt * g.groups);
+    return grad_held(a.cols) == 1 ? launch(rms_norm_backward_kernel<T, 1>, grid, block, smem, s, a, g)
+                                  : launch(rms_norm_backward_kernel<T, 2>, grid, block, smem, s, a, g);
 }
 
 }  // namespace
 
-cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
-    if (a.rows == 0) return cudaSuccess;
+cudaError_t launch_rms_norm(const NormArgs& args, cudaStream_t s) {
+    if (args.rows == 0) return cudaSuccess;
+    NormArgs a = args;
+    a.wide = aligned32(a.x, a.residual, a.residual_out, a.y) && aligned32(a.weight);
     const cudaError_t err = a.bf16 ? norm_t<__nv_bfloat16>(a, s) : norm_t<float>(a, s);
     note_launch();
     return err;
 }
 
+// The most blocks of any type and residual: a row a block.
 int norm_grad_blocks(int rows, int cols) {
-    const int per = cols <= 512 ? kGradWarps : 1;
-    return (int)std::min<long long>(2ll * sm_count(), ((long long)rows + per - 1) / per);
+    (void)cols;
+    return std::min(sm_count(), rows);
 }
 
-cudaError_t launch_rms_norm_backward(const NormGradArgs& a, cudaStream_t s) {
+cudaError_t launch_rms_norm_backward(const NormGradArgs& args, cudaStream_t s) {
+    NormGradArgs a = args;
+    a.wide = aligned32(a.d_y, a.z, a.d_residual, a.d_x) && aligned32(a.weight);
     if (a.rows == 0)
         return a.d_weight != nullptr ? cudaMemsetAsync(a.d_weight, 0, (size_t)a.cols * sizeof(float), s) : cudaSuccess;
-    cudaError_t err = a.bf16 ? grad_t<__nv_bfloat16>(a, s) : grad_t<float>(a, s);
+    const GradShape g = grad_shape(a.rows, a.cols);
+    cudaError_t err = a.bf16 ? grad_t<__nv_bfloat16>(a, g, s) : grad_t<float>(a, g, s);
     note_launch();
     if (err != cudaSuccess || a.d_weight == nullptr) return err;
-    err = launch(weight_grad_kernel, dim3((a.cols + 31) / 32), dim3(1024), 0, s, a, norm_grad_blocks(a.rows, a.cols));
+    err = launch(weight_grad_kernel, dim3((a.cols + 31) / 32), dim3(1024), 0, s, a, g.blocks);
     note_launch();
     return err;
 }

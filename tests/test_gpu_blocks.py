@@ -96,6 +96,23 @@ def test_codes_round_ties_to_even():
     assert got == [448.0, 1.0, 1.25, -1.0, 16.0, 20.0, 448.0, 0.0, 2.0 ** -8]
 
 
+def test_signs_of_zeros_and_quotients_at_borders():
+    """-0 keeps its sign; multiples of a scale that lie between two codes, with scales
+    whose reciprocals are not exact (amax = 448 m for odd m, and m / 7)."""
+    x = torch.zeros((64, 256))
+    x[:, ::3] = -0.0
+    mids = torch.from_numpy(ref.e4m3(np.arange(8, 0x7e, dtype=np.uint8)))
+    mids = ((mids[1:] + mids[:-1]) / 2).float()  # 117 values between two codes
+    for r in range(64):
+        x[r, :117] = mids * (r + 1 if r < 32 else (r - 31) / 7)
+        x[r, 127] = 448.0 * (r + 1 if r < 32 else (r - 31) / 7)
+    x[5, 128:] = -0.0
+    for dtype in (torch.float32, torch.bfloat16):
+        q, s = ep.ep_quantize_blocks(x.to(dtype).cuda())
+        want_q, want_s = ref.quantize32(x.to(dtype))
+        assert torch.equal(s.cpu(), want_s) and torch.equal(q.cpu(), want_q)
+
+
 def test_tiny_rows_and_zeros():
     x = torch.zeros((4, 256))
     x[0, 5] = 1e-44     # its quotient by 448 is 0
