@@ -288,6 +288,7 @@ struct NormArgs {
     float eps;
     int rows, cols, bf16, weight_bf16;
     int wide;                   // as in BlockQuantArgs (weight too)
+    int few;                    // set by the launcher: the weight is fetched ahead
 };
 cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
 

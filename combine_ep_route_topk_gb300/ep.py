@@ -486,6 +486,11 @@ def scale_blocks(cols) -> int:
     return -(-cols // SCALE_BLOCK)
 
 
+def _rows(rows, cols, dtype, device):
+    """torch.empty((rows, cols)) in half of its host time."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _codes(t, name, shape=None):
     """Device pointer of E4M3 codes: uint8, or torch's own type of them."""
     if isinstance(t, torch.Tensor) and t.dtype is torch.float8_e4m3fn:
@@ -519,9 +524,9 @@ def ep_quantize_blocks(x, act=EP_ACT_NONE, expert_offsets=None, layout=EP_LAYOUT
         raise EPError("x must have an even number of columns for SwiGLU")
     cols = wide // 2 if act == EP_ACT_SWIGLU else wide
     if q is None:
-        q = _empty((rows, cols), torch.uint8, x)
+        q = _rows(rows, cols, torch.uint8, x.device)
     if scales is None:
-        scales = _empty((rows, scale_blocks(cols)), torch.float32, x)
+        scales = _rows(rows, scale_blocks(cols), torch.float32, x.device)
     offs, E = _tokens(expert_offsets)
     _check("ep_quantize_blocks", lib().ep_quantize_blocks(
         _dev(x, x.dtype, "x"), dt, act, rows, cols, offs, E, layout, cap,
@@ -538,7 +543,7 @@ def ep_dequantize_blocks(q, scales, expert_offsets=None, layout=EP_LAYOUT_CONTIG
     values that they stand for, bf16 or float32 [rows, cols]."""
     rows, cols = _rows2d(q, "q")
     if out is None:
-        out = _empty((rows, cols), out_dtype, q)
+        out = _rows(rows, cols, out_dtype, q.device)
     dt = _float_type(out, "out")
     offs, E = _tokens(expert_offsets)
     _check("ep_dequantize_blocks", lib().ep_dequantize_blocks(
@@ -556,7 +561,7 @@ def ep_swiglu_backward(d_out, x, x_scales=None, expert_offsets=None, layout=EP_L
     rows, cols = _rows2d(d_out, "d_out")
     dt = _float_type(d_out, "d_out")
     if d_x is None:
-        d_x = _empty((rows, 2 * cols), d_out.dtype, d_out)
+        d_x = _rows(rows, 2 * cols, d_out.dtype, d_out.device)
     if x_scales is None:
         px = _dev(x, d_out.dtype, "x", (rows, 2 * cols))
     else:
@@ -586,7 +591,7 @@ def ep_expert_matmul_fp8(x, x_scales, w, w_scales, expert_offsets, layout=EP_LAY
     else:
         rows = x_rows if row_src is None else row_src.numel()
     if out is None:
-        out = _empty((rows, Nc), out_dtype, x)
+        out = _rows(rows, Nc, out_dtype, x.device)
     elif out.numel() != rows * Nc:
         raise EPError(f"out must hold {rows} x {Nc} elements")
     dt = _float_type(out, "out")
@@ -606,11 +611,12 @@ Norm = namedtuple("Norm", "y residual q scales rstd")
 
 def alloc_norm(rows, cols, dtype, device, y=True, residual=False, codes=False, rstd=False) -> Norm:
     """Outputs of ep_rms_norm, None for those that are not wanted."""
-    def z(on, shape, t):
-        return torch.empty(shape, dtype=t, device=device) if on else None
-    return Norm(z(y, (rows, cols), dtype), z(residual, (rows, cols), dtype),
-                z(codes, (rows, cols), torch.uint8),
-                z(codes, (rows, scale_blocks(cols)), torch.float32), z(rstd, (rows,), torch.float32))
+    return Norm(_rows(rows, cols, dtype, device) if y else None,
+                _rows(rows, cols, dtype, device) if residual else None,
+                _rows(rows, cols, torch.uint8, device) if codes else None,
+                _rows(rows, scale_blocks(cols), torch.float32, device) if codes else None,
+                torch.empty_strided((rows,), (1,), dtype=torch.float32, device=device)
+                if rstd else None)
 
 
 def ep_rms_norm(x, weight, residual=None, eps=1e-6, out: Norm | None = None, stream=None) -> Norm:

@@ -28,6 +28,16 @@ expert_layer
     seven calls serve prefill (contiguous) and decode (masked), without an
     allocation, so a step can be captured in a CUDA graph.
 
+expert_layer_fp8, expert_mlp_fp8, expert_mlp_fp8_backward
+    The same layer in E4M3 codes with a scale for every 128 columns (128 x 128 of
+    a weight).  Tokens come as bf16 rows or as the codes that ep_rms_norm wrote
+    behind the residual's addition.  Prefill from bf16 rows dispatches them as
+    codes; decode, and codes, are read in place through the layout's row_src.  The
+    experts' part alone runs on rows that lie expert-major, keeps the first
+    product's output as 8-bit codes where a backward pass follows, and has its
+    gradient to the rows: two products with the transposed weights around
+    SwiGLU's gradient from that checkpoint.
+
 HostPipeline
     Steps whose inputs and result live in pinned host memory: the binding of
     the library's native pipeline (ep_host_pipeline_*).  Copies in, kernels
@@ -335,6 +345,217 @@ def expert_layer(x, logits, rank_offsets, weights, buf, score=_ep.EP_SCORE_SIGMO
                          layout=buf.layout, cap=buf.cap, out=buf.down, status=buf.down_status)
     return _ep.ep_combine(buf.down, buf.idx, buf.wt, lay.pos, off, E, layout=buf.layout,
                           cap=buf.cap, out=buf.comb)
+
+
+@dataclass
+class ExpertWeightsFP8:
+    """Gated-linear experts in E4M3 codes (uint8): up [E, 2 I, H] (the gate half
+    first) and down [E, H, I], with a float32 scale for every 128 x 128 block of an
+    expert's matrix; and, for gradients, both transposed (the same codes)."""
+    up: torch.Tensor
+    up_scales: torch.Tensor
+    down: torch.Tensor
+    down_scales: torch.Tensor
+    up_t: torch.Tensor | None = None
+    up_t_scales: torch.Tensor | None = None
+    down_t: torch.Tensor | None = None
+    down_t_scales: torch.Tensor | None = None
+
+
+def quantize_expert_weights_fp8(up, down, gradients=False):
+    """bf16 or float32 weights up [E, 2 I, H] and down [E, H, I] on the GPU ->
+    ExpertWeightsFP8: each 128 x 128 block by its largest magnitude, as
+    ep_quantize_blocks does with 128 columns.  gradients=True also lays the
+    transposed weights out, which expert_mlp_fp8_backward reads."""
+    if up.dim() != 3 or down.shape != (up.shape[0], up.shape[2], up.shape[1] // 2):
+        raise ValueError(f"up {tuple(up.shape)} and down {tuple(down.shape)} are not "
+                         "[E, 2 I, H] and [E, H, I]")
+    B = _ep.SCALE_BLOCK
+
+    def one(w):
+        n, k = w.shape
+        nb, kb = _ep.scale_blocks(n), _ep.scale_blocks(k)
+        v = torch.nn.functional.pad(w.float(), (0, kb * B - k, 0, nb * B - n)).view(nb, B, kb, B)
+        top = v.abs().amax((1, 3))
+        # a tensor as divisor: by a number, torch multiplies with its reciprocal
+        scales = torch.where(top > 0, top / torch.full_like(top, 448.0), 1.0)
+        v = (v / scales[:, None, :, None]).clamp_(-448.0, 448.0).view(nb * B, kb * B)[:n, :k]
+        return v.to(torch.float8_e4m3fn).view(torch.uint8), scales
+
+    def every(ws):  # an expert at a time: the float32 form of one fits anywhere
+        codes, scales = zip(*(one(w) for w in ws))
+        return torch.stack(codes), torch.stack(scales)
+    out = ExpertWeightsFP8(*every(up), *every(down))
+    if gradients:
+        def turned(t):
+            return t.transpose(1, 2).contiguous()
+        out.up_t, out.up_t_scales = turned(out.up), turned(out.up_scales)
+        out.down_t, out.down_t_scales = turned(out.down), turned(out.down_scales)
+    return out
+
+
+@dataclass
+class MLPBuffersFP8:
+    """Everything that expert_mlp_fp8 writes for `rows` expert-major rows, and,
+    with keep=True, what its backward pass reads and writes."""
+    layout: int
+    cap: int
+    up: torch.Tensor            # [rows, 2 I] bf16
+    hq: torch.Tensor            # SwiGLU's codes [rows, I] and scales
+    hs: torch.Tensor
+    down: torch.Tensor          # [rows, H] bf16
+    up_status: torch.Tensor     # [1] each: 0 once its product completed, 1 if it gave up
+    down_status: torch.Tensor
+    upq: torch.Tensor | None = None   # the checkpoint of up: codes [rows, 2 I] and scales
+    ups: torch.Tensor | None = None
+    gq: torch.Tensor | None = None    # codes of a gradient [rows, max(H, 2 I)], flat, and scales
+    gs: torch.Tensor | None = None
+    d_h: torch.Tensor | None = None   # [rows, I] bf16
+    d_up: torch.Tensor | None = None  # [rows, 2 I] bf16
+    d_rows: torch.Tensor | None = None  # [rows, H] bf16
+    d_h_status: torch.Tensor | None = None
+    d_rows_status: torch.Tensor | None = None
+
+    def check(self):
+        """Waits for the last products; raises if one of them gave up (its rows are
+        then incomplete)."""
+        for name, status in (("first", self.up_status), ("second", self.down_status),
+                             ("second's gradient", self.d_h_status),
+                             ("first's gradient", self.d_rows_status)):
+            if status is not None and int(status) != 0:
+                raise _ep.EPError(f"expert_mlp_fp8: the {name} product gave up waiting")
+
+
+def make_mlp_buffers_fp8(rows, H, inner, layout=_ep.EP_LAYOUT_CONTIG, cap=0, keep=False,
+                         device="cuda"):
+    """Buffers for `rows` rows (E * cap for the masked layout)."""
+    def z(shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+    def codes(cols):
+        return z((rows, cols), torch.uint8), z((rows, _ep.scale_blocks(cols)), torch.float32)
+
+    def status():
+        return torch.zeros((1,), dtype=torch.int32, device=device)
+    b = MLPBuffersFP8(layout, cap, z((rows, 2 * inner)), *codes(inner), z((rows, H)), status(),
+                      status())
+    if keep:
+        widest = max(H, 2 * inner)
+        b.upq, b.ups = codes(2 * inner)
+        b.gq = z((rows * widest,), torch.uint8)
+        b.gs = z((rows * _ep.scale_blocks(widest),), torch.float32)
+        b.d_h, b.d_up, b.d_rows = z((rows, inner)), z((rows, 2 * inner)), z((rows, H))
+        b.d_h_status, b.d_rows_status = status(), status()
+    return b
+
+
+def expert_mlp_fp8(x, x_scales, expert_offsets, weights, buf, row_src=None):
+    """The experts on E4M3 rows x with x_scales (expert-major, or token rows read
+    through row_src) -> buf.down bf16 [rows, H], on the current stream.  Buffers made
+    with keep=True also get the checkpoint of the first product's output."""
+    kw = dict(layout=buf.layout, cap=buf.cap)
+    _ep.ep_expert_matmul_fp8(x, x_scales, weights.up, weights.up_scales, expert_offsets,
+                             row_src=row_src, out=buf.up, status=buf.up_status, **kw)
+    _ep.ep_quantize_blocks(buf.up, act=_ep.EP_ACT_SWIGLU, expert_offsets=expert_offsets, q=buf.hq,
+                           scales=buf.hs, x_q=buf.upq, x_scales=buf.ups, **kw)
+    return _ep.ep_expert_matmul_fp8(buf.hq, buf.hs, weights.down, weights.down_scales,
+                                    expert_offsets, out=buf.down, status=buf.down_status, **kw)
+
+
+def expert_mlp_fp8_backward(d_down, expert_offsets, weights, buf):
+    """Gradient of expert_mlp_fp8 to its rows: d_down bf16 [rows, H], the gradient of
+    buf.down's rows, expert-major -> buf.d_rows bf16 [rows, H] (of x's values; with
+    row_src, of the row that each position read).  The forward pass's buffers
+    (keep=True) are unchanged since; weights hold their transposed forms.  Both
+    gradients go into the products as E4M3 codes; the weights and the rounding to codes
+    count as constants."""
+    if buf.upq is None or weights.up_t is None:
+        raise ValueError("buffers made with keep=True and weights with gradients=True are needed")
+    rows, H = buf.down.shape
+    kw = dict(layout=buf.layout, cap=buf.cap)
+
+    def coded(g):
+        cols = g.shape[1]
+        return _ep.ep_quantize_blocks(
+            g, expert_offsets=expert_offsets, q=buf.gq[:rows * cols].view(rows, cols),
+            scales=buf.gs[:rows * _ep.scale_blocks(cols)].view(rows, -1), **kw)
+    _ep.ep_expert_matmul_fp8(*coded(d_down), weights.down_t, weights.down_t_scales, expert_offsets,
+                             out=buf.d_h, status=buf.d_h_status, **kw)
+    _ep.ep_swiglu_backward(buf.d_h, buf.upq, buf.ups, expert_offsets=expert_offsets, d_x=buf.d_up,
+                           **kw)
+    return _ep.ep_expert_matmul_fp8(*coded(buf.d_up), weights.up_t, weights.up_t_scales,
+                                    expert_offsets, out=buf.d_rows, status=buf.d_rows_status, **kw)
+
+
+@dataclass
+class LayerBuffersFP8:
+    """Everything that expert_layer_fp8 writes for N tokens."""
+    idx: torch.Tensor
+    picks: torch.Tensor         # idx before expert_map
+    wt: torch.Tensor
+    lay: _ep.Layout
+    ws: torch.Tensor
+    xq: torch.Tensor            # the tokens' codes: [N, H], or dispatched [rows, H]
+    xs: torch.Tensor
+    mlp: MLPBuffersFP8
+    comb: torch.Tensor          # [N, H] bf16
+
+    def check(self):
+        """Waits for the last layer's products; raises if one of them gave up."""
+        self.mlp.check()
+
+
+def make_layer_buffers_fp8(N, E, K, H, inner, R, cap=0, keep=False, device="cuda"):
+    """Buffers for N tokens over experts of inner width `inner`; cap > 0: the masked
+    layout with that capacity per expert; keep: for a backward pass of the experts."""
+    layout = _ep.EP_LAYOUT_MASKED if cap > 0 else _ep.EP_LAYOUT_CONTIG
+    rows = _ep.dispatch_rows(N, K, E, layout, cap)
+
+    def z(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=device)
+    held = rows if _dispatches(layout, H) else N
+    return LayerBuffersFP8(
+        z((N, K), torch.int32), z((N, K), torch.int32), z((N, K), torch.float32),
+        _ep.alloc_layout(N, E, K, R, cap, device),
+        z(_ep.ep_dispatch_layout_workspace_size(N, E, K, R), torch.uint8),
+        z((held, H), torch.uint8), z((held, _ep.scale_blocks(H)), torch.float32),
+        make_mlp_buffers_fp8(rows, H, inner, layout, cap, keep, device),
+        z((N, H), torch.bfloat16))
+
+
+def _dispatches(layout, H):
+    """Whether bf16 tokens are dispatched as codes: the contiguous layout's many rows an
+    expert are read faster where they lie together (1024 rows an expert: 0.81 against
+    1.64 ms); ep_dispatch's scales need whole blocks."""
+    return layout == _ep.EP_LAYOUT_CONTIG and H % _ep.SCALE_BLOCK == 0
+
+
+def expert_layer_fp8(x, logits, rank_offsets, weights, buf, score=_ep.EP_SCORE_SIGMOID, bias=None,
+                     groups=1, topk_groups=None, group_top=2, renorm=True, scale=1.0,
+                     expert_map=None):
+    """x bf16 [N, H], or (codes uint8 [N, H], scales) as ep_rms_norm and
+    ep_quantize_blocks write them; logits [N, E] -> buf.comb bf16 [N, H], on the
+    current stream.  The gate's arguments are ep_gate_topk's.  buf.check() tells, once
+    the step is done, that both products completed."""
+    E = logits.shape[1]
+    K = buf.idx.shape[1]
+    lay, off, mlp = buf.lay, buf.lay.expert_offsets, buf.mlp
+    _ep.ep_gate_topk(logits, K, score, bias=bias, groups=groups, topk_groups=topk_groups,
+                     group_top=group_top, renorm=renorm, scale=scale, expert_map=expert_map,
+                     topk_idx=buf.idx, topk_w=buf.wt, picks=buf.picks)
+    _ep.ep_dispatch_layout(buf.idx, rank_offsets, E, mlp.cap, out=lay, workspace=buf.ws)
+    row_src = lay.row_src
+    if isinstance(x, (tuple, list)):
+        xq, xs = x
+    elif _dispatches(mlp.layout, x.shape[1]):
+        xq, xs, row_src = buf.xq, buf.xs, None
+        _ep.ep_dispatch(x, buf.idx, lay.pos, off, E, mlp.layout, mlp.cap,
+                        _ep.EP_DTYPE_FP8_E4M3_B128, out=xq, out_scales=xs)
+    else:
+        xq, xs = _ep.ep_quantize_blocks(x, q=buf.xq, scales=buf.xs)
+    expert_mlp_fp8(xq, xs, off, weights, mlp, row_src)
+    return _ep.ep_combine(mlp.down, buf.idx, buf.wt, lay.pos, off, E, layout=mlp.layout,
+                          cap=mlp.cap, out=buf.comb)
 
 
 def host_empty(shape, dtype):
