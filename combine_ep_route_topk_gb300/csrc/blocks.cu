@@ -33,8 +33,6 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 
 // Item i of a kernel's thread: row i / pieces, columns 16 (i % pieces) and on.
-// The pieces of a row are rounded up to whole blocks, so that 8 consecutive
-// threads hold a block.
 struct Place {
     uint32_t row;
     int col;
@@ -53,21 +51,25 @@ __device__ __forceinline__ Place place(uint64_t i, uint32_t pieces) {
 
 // KEEP: also the codes of x, whose blocks lie on the halves' (cols a multiple of 128).
 template <typename T, bool SWIGLU, bool KEEP>
-__global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(BlockQuantArgs a) {
+__global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(BlockQuantArgs a, Divisor per_row) {
     pdl_prologue();
-    const int blocks = scale_blocks(a.cols);
-    const Place p = place((uint64_t)blockIdx.x * kThreads + threadIdx.x, (uint32_t)blocks * kLanes);
+    const int blocks = (int)per_row.d;
+    // the block of 128 that this thread's 8 lanes hold, below 2^31 of them
+    const uint32_t block = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+    Place p;
+    p.row = per_row.divide(block);
+    p.col = (int)((block - p.row * (uint32_t)blocks) * kScaleBlock + threadIdx.x % kLanes * kVec);
     // the lanes of a block decide together; all lanes take part in the maxima
     const bool row_on = p.row < (uint32_t)a.rows && holds_token(a.tokens, p.row);
     const bool on = row_on && p.col < a.cols;
     const size_t r = p.row;
-    float v[kVec], u[kVec];
+    float v[kVec], u[kVec];  // the values' negatives, as encode16 takes them
 #pragma unroll
     for (int j = 0; j < kVec; ++j) v[j] = u[j] = 0.0f;
     if (on) {
         const T* row = static_cast<const T*>(a.x) + r * (SWIGLU ? 2 * (size_t)a.cols : (size_t)a.cols) + p.col;
-        load16<true>(row, v, a.wide);
-        if constexpr (SWIGLU) load16<true>(row + a.cols, u, a.wide);
+        load16<true, true>(row, v, a.wide);
+        if constexpr (SWIGLU) load16<true, true>(row + a.cols, u, a.wide);
     }
     float scale;
     if constexpr (KEEP) {
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(BlockQuantArg
     }
     if constexpr (SWIGLU) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = v[j] * fast_rcp(1.0f + fast_exp(-v[j])) * u[j];
+        for (int j = 0; j < kVec; ++j) v[j] = v[j] * fast_rcp(1.0f + fast_exp(v[j])) * -u[j];
     }
     const uint4 codes = encode16(v, scale);
     if (on) {
@@ -150,20 +152,26 @@ cudaError_t run(void (*kernel)(Args), const Args& a, uint64_t pieces, cudaStream
     return err;
 }
 
+cudaError_t run_quantize(void (*kernel)(BlockQuantArgs, Divisor), const BlockQuantArgs& a, cudaStream_t s) {
+    const uint64_t blocks = (uint64_t)scale_blocks(a.cols) * a.rows, per = kThreads / kLanes;
+    const cudaError_t err = launch(kernel, dim3((unsigned)((blocks + per - 1) / per)), dim3(kThreads), 0, s, a,
+                                   Divisor((uint32_t)scale_blocks(a.cols)));
+    note_launch();
+    return err;
+}
+
 template <typename T>
 cudaError_t quantize_t(const BlockQuantArgs& a, cudaStream_t s) {
-    const uint64_t pieces = (uint64_t)scale_blocks(a.cols) * kLanes;
-    if (!a.swiglu) return run(quantize_blocks_kernel<T, false, false>, a, pieces, s);
-    if (a.x_q == nullptr) return run(quantize_blocks_kernel<T, true, false>, a, pieces, s);
-    if (a.cols % kScaleBlock == 0) return run(quantize_blocks_kernel<T, true, true>, a, pieces, s);
+    if (!a.swiglu) return run_quantize(quantize_blocks_kernel<T, false, false>, a, s);
+    if (a.x_q == nullptr) return run_quantize(quantize_blocks_kernel<T, true, false>, a, s);
+    if (a.cols % kScaleBlock == 0) return run_quantize(quantize_blocks_kernel<T, true, true>, a, s);
     // a block of x straddles the halves: its codes in a pass of their own
     BlockQuantArgs kept = a;
     kept.cols = 2 * a.cols;
     kept.q = a.x_q;
     kept.scales = a.x_scales;
-    const cudaError_t err =
-        run(quantize_blocks_kernel<T, false, false>, kept, (uint64_t)scale_blocks(kept.cols) * kLanes, s);
-    return err != cudaSuccess ? err : run(quantize_blocks_kernel<T, true, false>, a, pieces, s);
+    const cudaError_t err = run_quantize(quantize_blocks_kernel<T, false, false>, kept, s);
+    return err != cudaSuccess ? err : run_quantize(quantize_blocks_kernel<T, true, false>, a, s);
 }
 
 }  // namespace

@@ -116,6 +116,8 @@ __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
             if (a.y != nullptr) store16(static_cast<T*>(a.y) + at + c, z[i], a.wide);
         }
         if (a.q != nullptr) {  // every lane takes part in the blocks' maxima
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) z[i][j] = -z[i][j];
             float scale;
             const uint4 codes = encode16(z[i], scale);
             if (c < cols) {

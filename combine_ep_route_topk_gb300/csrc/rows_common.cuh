@@ -62,27 +62,28 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool wi
     }
 }
 
-// 16 columns, once (streamed: nothing reads them again) or kept in cache.  wide: rows
-// start on 32 bytes.
-template <bool STREAM>
+// 16 columns, once (streamed: nothing reads them again) or kept in cache; wide: rows
+// start on 32 bytes; NEG: their negatives.
+template <bool STREAM, bool NEG = false>
 __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[kVec], bool wide) {
     uint32_t r[8];
     load32<STREAM>(p, r, wide);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        if (NEG) r[i] ^= 0x80008000u;
         v[2 * i] = lo_of(r[i]);
         v[2 * i + 1] = hi_of(r[i]);
     }
 }
-template <bool STREAM>
+template <bool STREAM, bool NEG = false>
 __device__ __forceinline__ void load16(const float* p, float (&v)[kVec], bool wide) {
     uint32_t r[8], t[8];
     load32<STREAM>(p, r, wide);
     load32<STREAM>(p + 8, t, wide);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        v[i] = __uint_as_float(r[i]);
-        v[8 + i] = __uint_as_float(t[i]);
+        v[i] = __uint_as_float(r[i] ^ (NEG ? 0x80000000u : 0u));
+        v[8 + i] = __uint_as_float(t[i] ^ (NEG ? 0x80000000u : 0u));
     }
 }
 
@@ -131,39 +132,80 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float m;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
 // Codes of a block's values as ep_dispatch makes them, by the 8 lanes that hold
 // them (all lanes of the warp call it; lanes past the row's end hold zeros):
 // scale = max|v| / 448 (1 where that is 0), code = E4M3(v / scale), both quotients
 // rounded as IEEE divisions are.  A NaN takes no part in the maximum and stays NaN
 // as a code; a block with an infinity gets the scale infinity, so that its values
-// are NaN.  The quotients are products with the rounded reciprocal, corrected once
+// are NaN.  The quotients are products with the reciprocal, corrected once
 // by their remainder (Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000 processor", 1990), which is exact here: v has a remainder that
-// a float32 holds, or a quotient far below the smallest code.  3 instructions a
-// value instead of a division's; 32768 x 7168 bf16 rows QUANT_US us instead of 158.
-// The remainder is taken as q scale - v so that -0 keeps its sign.
-__device__ __forceinline__ uint4 encode16(const float (&v)[kVec], float& scale) {
-    float top = 0.0f;
+// a float32 holds, or a quotient far below the smallest code.  (The hardware's
+// reciprocal is off by 2^-23 of itself, which leaves 2^-22 of a last place: a quotient
+// that is a float32, like the borders between codes, comes out as itself.)  Given are the values'
+// negatives, nv: the remainder q scale - v, taken from the quotient, keeps the sign of
+// -0, and two values an instruction have no modifier for a sign.  32768 x 7168 bf16
+// rows 119 us, with divisions 158.
+__device__ __forceinline__ uint4 encode16(const float (&nv)[kVec], float& scale) {
+    float top = max_abs3(nv[0], nv[1], nv[2]);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) top = fmaxf(top, fabsf(v[j]));
+    for (int j = 3; j < kVec - 1; j += 2) top = max_abs3(top, nv[j], nv[j + 1]);
+    top = fmaxf(top, fabsf(nv[kVec - 1]));
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-    scale = __fdiv_rn(top, 448.0f);
-    if (scale == 0.0f) scale = 1.0f;
     uint32_t p[8];
     if (top >= 0x1p-100f && top <= 0x1.fffffep127f) {
-        const float inv = __frcp_rn(scale);
+        constexpr float kInv448 = 1.0f / 448.0f;
+        scale = top * kInv448;
+        scale = fmaf(fmaf(-scale, 448.0f, top), kInv448, scale);
+        float ninv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ninv) : "f"(-scale));
+        uint64_t ninv2, scale2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(ninv2) : "f"(ninv));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(scale2) : "f"(scale));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float a = v[2 * j] * inv, b = v[2 * j + 1] * inv;
-            p[j] = e4m3x2(fmaf(-fmaf(a, scale, -v[2 * j]), inv, a), fmaf(-fmaf(b, scale, -v[2 * j + 1]), inv, b));
+            float x, y;
+            asm("{\n.reg .b64 v, q, r;\n"
+                "mov.b64 v, {%2, %3};\n"
+                "mul.rn.f32x2 q, v, %4;\n"
+                "fma.rn.f32x2 r, q, %5, v;\n"
+                "fma.rn.f32x2 q, r, %4, q;\n"
+                "mov.b64 {%0, %1}, q;\n}\n"
+                : "=f"(x), "=f"(y) : "f"(nv[2 * j]), "f"(nv[2 * j + 1]), "l"(ninv2), "l"(scale2));
+            p[j] = e4m3x2(x, y);
         }
     } else {
+        scale = top == top ? __fdiv_rn(top, 448.0f) : 0.0f;  // 0 for nothing but NaN
+        if (scale == 0.0f) scale = 1.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = e4m3x2(__fdiv_rn(v[2 * j], scale), __fdiv_rn(v[2 * j + 1], scale));
+        for (int j = 0; j < 8; ++j) p[j] = e4m3x2(__fdiv_rn(-nv[2 * j], scale), __fdiv_rn(-nv[2 * j + 1], scale));
     }
-    return make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
+    return make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                      __byte_perm(p[4], p[5], 0x5410), __byte_perm(p[6], p[7], 0x5410));
 }
+
+// n / d for n below 2^31 by one product (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994), made on the host.
+struct Divisor {
+    uint32_t d, m, shift;
+    Divisor() = default;
+    explicit Divisor(uint32_t by) : d(by), m(0), shift(0) {
+        if (by > 1) {
+            uint32_t l = 1;
+            while ((1ull << l) < by) ++l;
+            m = (uint32_t)((1ull << (31 + l)) / by + 1);
+            shift = l - 1;
+        }
+    }
+    __device__ __forceinline__ uint32_t divide(uint32_t n) const { return d == 1 ? n : __umulhi(n, m) >> shift; }
+};
 
 // Whether row r holds a token.
 __device__ __forceinline__ bool holds_token(const TokenRows& t, uint32_t r) {
