@@ -14,7 +14,7 @@
 // multiply-add.
 //   2 TMA warps weights in [BN x 128 bytes] boxes, rows of x in boxes of 32 or, with
 //               row_src, 4 a copy; 128-byte swizzle
-//   MMA thread  issues the MMAs
+//   MMA warp    issues the MMAs
 //   unit warp   the list of tiles, their rows and their scales, ahead of the others
 //   8 warps     TMEM -> scales -> registers; at a tile's end -> rows of out
 // Rows that a tile lacks are neither copied nor stored: what lies in their place in
@@ -23,14 +23,17 @@
 // frees its TMEM.
 //
 // What bounds it: with few rows per expert the weights' bytes (32 experts of 4096 x
-// 7168, 64 rows each: 154 us = 6.3 TB/s).  With many (1024 rows each: 0.80 ms = 2.4
-// PFLOP/s) the way of the sums: a step of 128 x 256 x 128 takes 1000 cycles, of
-// which the MMAs take 512; without the reads of TMEM and the multiply-adds the same
-// steps take 830, and one accumulator for all of K (no scales) 770, which is what
-// shared memory needs to be written and read (96 KB at 128 bytes a cycle).  Halving
-// that by pairs of CTAs (cta_group::2) changed nothing: 0.84 against 0.89 ms.  Nor did
-// 16 summing warps (0.88), accumulators of 128 or 160 channels (1.03, 1.19), taking
-// the accumulator in two halves (0.90) or spinning on the barriers (1.05).
+// 7168, 64 rows each: 154 us = 6.3 TB/s).  With many (1024 rows each: 0.77 ms = 2.5
+// PFLOP/s; 0.88 in a long loop at the 1.72 GHz that the power limit leaves) the summing
+// warps: a step of 128 x 256 x 128 takes 900 cycles, of which the MMAs take 512 and a
+// warp's 128 loads and multiply-adds 430 beside the other warp of its scheduler, the rest
+// being its waits, arrivals and scales.  Without loads and multiply-adds the same steps
+// take 830, and one accumulator for all of K (no scales) 770, which is what shared memory
+// needs to be written and read (96 KB at 128 bytes a cycle).  Pairs of CTAs
+// (cta_group::2), which halve that, gained nothing: 0.89 ms when this took 0.84.  Nor did
+// 16 summing warps (1.03 when this took 0.77), accumulators of 128 or 160 channels (1.03,
+// 1.19), taking the accumulator in two halves (0.90), two values a multiply-add (0.94)
+// or spinning on the barriers (1.05).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -60,14 +63,15 @@ struct Shape {
     static constexpr int kStages = 192 * 1024 / kStageBytes;
     static constexpr int kAcc = (int)kTmemCols / BN;      // accumulators
     static constexpr int kCols = BN / 2;                  // channels of a summing thread
+    static_assert(kStages >= kAcc, "no turn of a stage is missed");
     static_assert(kCols <= kScaleBlock && BN <= 256, "one scale a thread; a TMA box");
 };
 
 constexpr int kMaxStages = 6, kMaxAcc = 4, kUnitSlots = 4;
 constexpr int kScaleGroup = 4, kScaleSlots = 6;  // blocks whose scales come together, groups under way
 struct Shared {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t acc_full[kMaxAcc], acc_empty[kMaxAcc];
+    uint64_t full[kMaxStages], done[kMaxStages];  // a stage has landed; its MMAs are over
+    uint64_t acc_empty[kMaxAcc];
     uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
     uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
     uint64_t drained;
@@ -83,11 +87,19 @@ struct Shared {
 template <class S>
 constexpr int kSmemBytes = 1024 + S::kStages * S::kStageBytes + (int)sizeof(Shared);
 
+// By a whole warp, one lane of which issues: with the choice inside, the operands stay
+// in uniform registers (four of these and the commit take 156 cycles, 240 in a branch).
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+        "{\n.reg .pred p, one;\nelect.sync _|one, 0xffffffff;\nsetp.ne.u32 p, %4, 0;\n"
+        "@one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u) : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+    asm volatile(
+        "{\n.reg .pred one;\nelect.sync _|one, 0xffffffff;\n"
+        "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
+        ::"r"(smem_u32(bar)) : "memory");
 }
 
 // 32 columns of this warp's 32 lanes, without the wait; then the wait, which the
@@ -126,6 +138,28 @@ __device__ __forceinline__ void fetch4(uint32_t dst, const float* src, bool on) 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
 }
 
+// A place in a ring of N and the parity of its turn.
+template <int N>
+struct Ring {
+    uint32_t i = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Whether the phase with this parity is over; does not wait.
+__device__ __forceinline__ bool test_now(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return done != 0;
+}
 // A warp's wait.
 template <class Shared>
 __device__ __forceinline__ bool wait_warp(Shared* sh, uint64_t* bar, uint32_t parity) {
@@ -194,12 +228,9 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
         sh->abort = 0;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh->full[i], 2);
-            mbar_init(&sh->empty[i], 1);
+            mbar_init(&sh->done[i], 1);
         }
-        for (int i = 0; i < kAcc; ++i) {
-            mbar_init(&sh->acc_full[i], 1);
-            mbar_init(&sh->acc_empty[i], kSumWarps);
-        }
+        for (int i = 0; i < kAcc; ++i) mbar_init(&sh->acc_empty[i], kSumWarps);
         for (int i = 0; i < kUnitSlots; ++i) {
             mbar_init(&sh->unit_full[i], 1);
             mbar_init(&sh->unit_empty[i], kSumWarps + 2);  // all that look rows up
@@ -249,7 +280,7 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
                 const uint32_t bytes = (last - first) * (gather ? 4 : 32) * kBK + (weights ? S::kBBytes : 0);
                 for (int kb = 0; kb < kblocks; ++kb, ++c) {
                     const uint32_t s = c % kStages;
-                    ok = mbar_wait_warp(sh, &sh->empty[s], (c / kStages & 1) ^ 1);
+                    ok = mbar_wait_warp(sh, &sh->done[s], (c / kStages & 1) ^ 1);
                     if (!ok) break;
                     if (elect_one()) {
                         uint8_t* stage = s_stage + s * S::kStageBytes;
@@ -271,38 +302,39 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
             }
             // the last MMAs' arrivals on each stage land before the CTA ends
             for (uint32_t i = c < kStages ? 0 : c - kStages; ok && i < c; ++i)
-                ok = mbar_wait_warp(sh, &sh->empty[i % kStages], i / kStages & 1);
+                ok = mbar_wait_warp(sh, &sh->done[i % kStages], i / kStages & 1);
             if (!ok && lane == 0) drain_copies<kStages>(sh->full, c);
         } else if (warp == kMmaWarp) {
             // ---- MMA: one elected thread ----
-            if (elect_one()) {
-                const uint64_t desc0 = operand_desc(smem_u32(s_stage));
-                // float32 accumulators, E4M3 operands, both K-major
-                constexpr uint32_t idesc = 1u << 4 | (uint32_t)(S::BN >> 3) << 17 | (uint32_t)(S::TN >> 4) << 24;
-                const uint64_t total = (uint64_t)units * kblocks;
-                uint32_t c = 0;
-                bool ok = true;
-                for (uint64_t i = 0; i < total; ++i, ++c) {
-                    const uint32_t acc = c % kAcc, s = c % kStages;
-                    ok = mbar_wait(sh, &sh->full[s], c / kStages & 1);
-                    if (ok) ok = mbar_wait(sh, &sh->acc_empty[acc], (c / kAcc & 1) ^ 1);
+            const uint64_t desc0 = operand_desc(smem_u32(s_stage));
+            // float32 accumulators, E4M3 operands, both K-major
+            constexpr uint32_t idesc = 1u << 4 | (uint32_t)(S::BN >> 3) << 17 | (uint32_t)(S::TN >> 4) << 24;
+            Ring<kStages> st;
+            Ring<kAcc> acc;
+            bool ok = true, any = false;
+            for (uint32_t u = 0; ok && u < units; ++u) {
+#pragma unroll 1
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    ok = wait_warp(sh, &sh->full[st.i], st.phase) && wait_warp(sh, &sh->acc_empty[acc.i], acc.phase ^ 1);
                     if (!ok) break;
                     tmem_fence_after();
-                    const uint64_t da = desc0 + (uint64_t)(s * (S::kStageBytes >> 4)), db = da + (S::kABytes >> 4);
+                    const uint64_t da = desc0 + (uint64_t)(st.i * (S::kStageBytes >> 4)), db = da + (S::kABytes >> 4);
+                    const uint32_t d = tmem + acc.i * S::BN;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f8(tmem + acc * S::BN, da + k * 2, db + k * 2, idesc, k > 0);
-                    mma_commit<1>(&sh->acc_full[acc]);
-                    mma_commit<1>(&sh->empty[s]);
-                }
-                if (!ok && c > 0) {  // the MMAs in flight end before their operands' memory is given up
-                    mma_commit<1>(&sh->drained);
-                    const long long start = clock64();
-                    while (!mbar_try(smem_u32(&sh->drained), 0))
-                        if (clock64() - start > kWaitCycles) break;
+                    for (int k = 0; k < 4; ++k) mma_f8(d, da + k * 2, db + k * 2, idesc, k > 0);
+                    commit_elected(&sh->done[st.i]);
+                    any = true;
+                    st.next();
+                    acc.next();
                 }
             }
-            __syncwarp();
+            if (!ok && any) {  // the MMAs in flight end before their operands' memory is given up
+                commit_elected(&sh->drained);
+                const long long start = clock64();
+                while (!mbar_try(smem_u32(&sh->drained), 0))
+                    if (clock64() - start > kWaitCycles) break;
+                __syncwarp();
+            }
         } else {
             // ---- units, their rows and their scales, a few ahead ----
             Steps<S> steps(a, blockIdx.x, gridDim.x);
@@ -364,6 +396,8 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
         const bool vectors = (size_t)a.Nc * size % 16 == 0;
         const int row = quarter * 32 + lane;
         uint32_t c = 0, g = 0;  // blocks and groups of scales so far
+        Ring<kStages> st;
+        bool ready = false, soon = false;  // the next block is there already
         bool ok = true;
         for (uint32_t u = 0; ok && u < units; ++u) {
             const uint32_t slot = u % kUnitSlots;
@@ -394,7 +428,7 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
                 for (int j = 0; j < kScaleGroup; ++j) {
                     if (kb + j >= kblocks) break;
                     const uint32_t b = c % kAcc;
-                    ok = wait_warp(sh, &sh->acc_full[b], c / kAcc & 1);
+                    if (!ready) ok = wait_warp(sh, &sh->done[st.i], st.phase);
                     if (!ok) break;
                     tmem_fence_after();
                     if (busy) {
@@ -408,13 +442,18 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
                             } else {  // all of it is in registers: the next block may come
                                 tmem_fence_before();
                                 if (lane == 0) mbar_arrive(&sh->acc_empty[b]);
+                                st.next();
+                                soon = test_now(&sh->done[st.i], st.phase);  // answered behind the last sums
                             }
                             add_scaled32(acc + i * 32, v[i & 1], s[j]);
                         }
-                    } else if (lane == 0) {
-                        mbar_arrive(&sh->acc_empty[b]);
+                    } else {
+                        if (lane == 0) mbar_arrive(&sh->acc_empty[b]);
+                        st.next();
+                        soon = false;
                     }
                     ++c;
+                    ready = __all_sync(kFull, soon);
                     if (!ok) break;
                 }
             }
@@ -519,11 +558,11 @@ cudaError_t launch_shape(const MatmulArgs& a, cudaStream_t s) {
 cudaError_t launch_expert_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {
     if (a.rows == 0)
         return a.status != nullptr ? cudaMemsetAsync(a.status, 0, sizeof(int32_t), s) : cudaSuccess;
-    // Wide tiles take half the steps at 1000 cycles instead of 620; narrow ones have twice
+    // Wide tiles take half the steps at 900 cycles instead of 620; narrow ones have twice
     // the tiles and more weights in flight.  Us with 256 channels and with 128, 32 experts of
-    // 4096 x 7168: 64 rows each 160, 154; 128 rows 188, 207; 1024 rows 805, 1040; one
+    // 4096 x 7168: 64 rows each 160, 154; 128 rows 188, 213; 1024 rows 772, 1085; one
     // expert of 4096 x 4096, 512 rows (64 wide tiles) 27, 20.  Rows fetched by 4 cost a
-    // step more: 32 rows each 164, 192.  A capacity counts half.
+    // step more: 32 rows each 164, 195.  A capacity counts half.
     const double mean = a.layout == 0 ? (double)a.rows / a.E : 0.5 * a.cap;
     const double tiles = a.E * std::ceil(mean / 128) * ((a.Nc + 255) / 256);
     const bool wide = tiles >= sm_count() && mean >= (a.row_src != nullptr ? 16 : 96);
