@@ -63,6 +63,7 @@ struct Shape {
     static constexpr int kStages = 192 * 1024 / kStageBytes;
     static constexpr int kAcc = (int)kTmemCols / BN;      // accumulators
     static constexpr int kCols = BN / 2;                  // channels of a summing thread
+    static constexpr bool kAnywhere = BN == 128;          // out's rows may start off 16 bytes
     static_assert(kStages >= kAcc, "no turn of a stage is missed");
     static_assert(kCols <= kScaleBlock && BN <= 256, "one scale a thread; a TMA box");
 };
@@ -79,6 +80,7 @@ struct Shared {
     alignas(16) int source[kUnitSlots][128];   // rows of x of a unit's rows, -1 for none
     alignas(16) float x_scales[kScaleSlots][128][kScaleGroup];  // of a row in the blocks of a group
     alignas(16) float w_scales[kScaleSlots][2][kScaleGroup];           // of the channels' two halves
+    float turn[kSumWarps][8][33];  // 8 channels of a summing warp's 32 rows on their way out
     uint32_t tmem;
     int abort;
     long long warp_sums[kTileGroups / 32];
@@ -188,25 +190,21 @@ __device__ __forceinline__ Unit unpack_unit(int4 q) {
     return t;
 }
 
-// Eight channels of a row of out; cols: how many there are from here.
-__device__ __forceinline__ void store8(const MatmulArgs& a, uint8_t* to, int cols, bool vectors, const float (&f)[8]) {
-    if (vectors) {
-        if (a.out_bf16) {
-            if (cols > 0)
-                *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                                           pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-        } else {
-            if (cols > 0) *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
-            if (cols > 4) *reinterpret_cast<float4*>(to + 16) = make_float4(f[4], f[5], f[6], f[7]);
-        }
-        return;
+// Whether each row of out starts on 16 bytes (out does).
+__host__ __device__ __forceinline__ bool rows_on_16(const MatmulArgs& a) {
+    return (size_t)a.Nc * (a.out_bf16 ? 2 : 4) % 16 == 0;
+}
+
+// Eight channels of a row of out that starts on 16 bytes; cols: how many there are from here.
+__device__ __forceinline__ void store8(const MatmulArgs& a, uint8_t* to, int cols, const float (&f)[8]) {
+    if (a.out_bf16) {
+        if (cols > 0)
+            *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                       pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    } else {
+        if (cols > 0) *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+        if (cols > 4) *reinterpret_cast<float4*>(to + 16) = make_float4(f[4], f[5], f[6], f[7]);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < cols) {
-            if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(to)[i] = __float2bfloat16_rn(f[i]);
-            else reinterpret_cast<float*>(to)[i] = f[i];
-        }
 }
 // 32 bytes that start on a boundary of 32: a whole sector of memory.
 __device__ __forceinline__ void store32(uint8_t* to, const uint32_t (&r)[8]) {
@@ -393,7 +391,7 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
         const int size = a.out_bf16 ? 2 : 4;
         // rows of out start on 32 bytes, or on 16
         const bool sectors = (size_t)a.Nc * size % 32 == 0 && reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
-        const bool vectors = (size_t)a.Nc * size % 16 == 0;
+        const bool vectors = rows_on_16(a);
         const int row = quarter * 32 + lane;
         uint32_t c = 0, g = 0;  // blocks and groups of scales so far
         Ring<kStages> st;
@@ -462,8 +460,33 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
             const bool none = sh->source[slot][row] < 0;  // a row of zeros, whatever lay in its place
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->unit_empty[slot]);
-            if (row >= t.rows || !busy) continue;
             const int ch0 = t.channel + half * kCols;
+            if constexpr (S::kAnywhere) {
+                if (!vectors) {
+                    // 8 channels at a time through shared memory, so that a store takes 8
+                    // neighbours of four rows (6 experts of 500 x 1008, 64 rows each: 14 us,
+                    // 22 by each thread's own row)
+                    const int rows = min(t.rows - quarter * 32, 32), c = lane & 7;
+                    uint8_t* to = static_cast<uint8_t*>(a.out) +
+                                  ((first_row(a, t.e, t.begin) + t.first + quarter * 32) * (size_t)a.Nc + ch0 + c) * size;
+#pragma unroll
+                    for (int j = 0; j < kCols; j += 8) {
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sh->turn[warp][i][lane] = none ? 0.0f : acc[j + i];
+                        __syncwarp();
+                        if (ch0 + j + c < a.Nc)
+                            for (int r = lane >> 3; r < rows; r += 4) {
+                                const float y = sh->turn[warp][c][r];
+                                uint8_t* at = to + ((size_t)r * a.Nc + j) * size;
+                                if (a.out_bf16) *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(y);
+                                else *reinterpret_cast<float*>(at) = y;
+                            }
+                    }
+                    continue;
+                }
+            }
+            if (row >= t.rows || !busy) continue;
             uint8_t* to = static_cast<uint8_t*>(a.out) +
                           ((first_row(a, t.e, t.begin) + t.first + row) * (size_t)a.Nc + ch0) * size;
             const int cols = a.Nc - ch0;
@@ -493,7 +516,7 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
                     float f[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] = none ? 0.0f : acc[j + i];
-                    store8(a, to + j * size, cols - j, vectors, f);
+                    store8(a, to + j * size, cols - j, f);
                 }
             }
         }
@@ -562,10 +585,13 @@ cudaError_t launch_expert_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {
     // the tiles and more weights in flight.  Us with 256 channels and with 128, 32 experts of
     // 4096 x 7168: 64 rows each 160, 154; 128 rows 188, 213; 1024 rows 772, 1085; one
     // expert of 4096 x 4096, 512 rows (64 wide tiles) 27, 20.  Rows fetched by 4 cost a
-    // step more: 32 rows each 164, 195.  A capacity counts half.
+    // step more: 32 rows each 164, 195.  A capacity counts half.  Rows of out off 16 bytes are
+    // narrow tiles' alone: the way through shared memory costs the wide ones registers that
+    // their steps need (prefill 0.86 ms instead of 0.77).  32 experts of 4100 x 7168, 1024 rows
+    // each: 1.23 ms, wide tiles with each thread's own stores 1.79.
     const double mean = a.layout == 0 ? (double)a.rows / a.E : 0.5 * a.cap;
     const double tiles = a.E * std::ceil(mean / 128) * ((a.Nc + 255) / 256);
-    const bool wide = tiles >= sm_count() && mean >= (a.row_src != nullptr ? 16 : 96);
+    const bool wide = tiles >= sm_count() && mean >= (a.row_src != nullptr ? 16 : 96) && rows_on_16(a);
     const cudaError_t err = wide ? launch_shape<Shape<256>>(a, s) : launch_shape<Shape<128>>(a, s);
     note_launch();
     return err;
