@@ -376,9 +376,10 @@ def quantize_expert_weights_fp8(up, down, gradients=False):
         n, k = w.shape
         nb, kb = _ep.scale_blocks(n), _ep.scale_blocks(k)
         v = torch.nn.functional.pad(w.float(), (0, kb * B - k, 0, nb * B - n)).view(nb, B, kb, B)
-        top = v.abs().amax((1, 3))
+        top = torch.where(v.isnan(), 0.0, v.abs()).amax((1, 3))
         # a tensor as divisor: by a number, torch multiplies with its reciprocal
-        scales = torch.where(top > 0, top / torch.full_like(top, 448.0), 1.0)
+        scales = top / torch.full_like(top, 448.0)
+        scales = torch.where(scales > 0, scales, 1.0)  # 0 for zeros and the smallest values
         v = (v / scales[:, None, :, None]).clamp_(-448.0, 448.0).view(nb * B, kb * B)[:n, :k]
         return v.to(torch.float8_e4m3fn).view(torch.uint8), scales
 
@@ -525,7 +526,7 @@ def make_layer_buffers_fp8(N, E, K, H, inner, R, cap=0, keep=False, device="cuda
 
 def _dispatches(layout, H):
     """Whether bf16 tokens are dispatched as codes: the contiguous layout's many rows an
-    expert are read faster where they lie together (1024 rows an expert: 0.81 against
+    expert are read faster where they lie together (1024 rows an expert: 0.77 against
     1.64 ms); ep_dispatch's scales need whole blocks."""
     return layout == _ep.EP_LAYOUT_CONTIG and H % _ep.SCALE_BLOCK == 0
 
