@@ -721,7 +721,7 @@ ep_status_t ep_rms_norm(const void* x, ep_dtype_t dtype, const void* residual, c
 
 size_t ep_rms_norm_backward_workspace_size(int32_t rows, int32_t cols) {
     if (check_norm(rows, cols) != EP_OK) return 256;
-    return ((size_t)norm_grad_blocks(rows, cols) * cols * sizeof(float) + 511) / 256 * 256;
+    return ((size_t)norm_grad_blocks(rows) * cols * sizeof(float) + 511) / 256 * 256;
 }
 
 ep_status_t ep_rms_norm_backward(const void* d_y, ep_dtype_t dtype, const void* z,

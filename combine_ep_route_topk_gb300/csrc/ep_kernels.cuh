@@ -305,7 +305,7 @@ struct NormGradArgs {
     int wide;                   // as in NormArgs
 };
 // Blocks of the kernel that sums the weight's gradient, each with a partial sum.
-int norm_grad_blocks(int rows, int cols);
+int norm_grad_blocks(int rows);
 cudaError_t launch_rms_norm_backward(const NormGradArgs& a, cudaStream_t s);
 
 }  // namespace ep

@@ -40,10 +40,10 @@ __device__ __forceinline__ float row_sum(float v, int nt, int tid, int bar, floa
     return v;
 }
 
-template <bool STREAM>
-__device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)[kVec]) {
-    if (a.weight_bf16) load16<STREAM>(static_cast<const __nv_bfloat16*>(a.weight) + c, w, a.wide);
-    else load16<STREAM>(static_cast<const float*>(a.weight) + c, w, a.wide);
+template <typename Args>
+__device__ __forceinline__ void load_weight(const Args& a, int c, float (&w)[kVec]) {
+    if (a.weight_bf16) load16<false>(static_cast<const __nv_bfloat16*>(a.weight) + c, w, a.wide);
+    else load16<false>(static_cast<const float*>(a.weight) + c, w, a.wide);
 }
 
 __device__ __forceinline__ float rounded(float v, const __nv_bfloat16*) {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
         const int c = (i * nt + tid) * kVec;
         if (c < cols) {
             float w[kVec];
-            load_weight<false>(a, c, w);
+            load_weight(a, c, w);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) z[i][j] = z[i][j] * rstd * w[j];
             if (a.y != nullptr) store16(static_cast<T*>(a.y) + at + c, z[i], a.wide);
@@ -240,10 +240,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_kernel(Norm
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
-            const int c = min((i * nt + tid) * kVec, a.cols - kVec);  // idle threads hold zeros
+            const int c = (i * nt + tid) * kVec;
+            if (c >= a.cols) {  // idle threads add nothing
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) n[i][j] = gy[i][j] = 0.0f;
+                continue;
+            }
             float w[kVec];
-            if (a.weight_bf16) load16<false>(static_cast<const __nv_bfloat16*>(a.weight) + c, w, wide);
-            else load16<false>(static_cast<const float*>(a.weight) + c, w, wide);
+            load_weight(a, c, w);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 n[i][j] = z[i].at(j) * scale;
@@ -252,8 +256,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_kernel(Norm
                 gy[i][j] *= w[j];
                 sum = fmaf(gy[i][j], n[i][j], sum);
             }
-            d[i] = res[i];
         }
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) d[i] = res[i];
         if (kAhead) load(r + step);
         // two buffers in turn: a warp may be one row ahead of another
         if (nt == 8) sum = row_sum<8>(sum, nt, tid, 0, nullptr);
@@ -334,10 +339,7 @@ cudaError_t launch_rms_norm(const NormArgs& args, cudaStream_t s) {
 }
 
 // The most blocks of any type and residual: a row a block.
-int norm_grad_blocks(int rows, int cols) {
-    (void)cols;
-    return std::min(sm_count(), rows);
-}
+int norm_grad_blocks(int rows) { return std::min(sm_count(), rows); }
 
 cudaError_t launch_rms_norm_backward(const NormGradArgs& args, cudaStream_t s) {
     NormGradArgs a = args;
