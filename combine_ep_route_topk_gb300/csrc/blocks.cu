@@ -6,8 +6,12 @@
 //   scale  = max|v| / 448 over 128 columns (1 for zeros), code = E4M3(v / scale)
 //   d_g    = d u s (1 + g (1 - s)),  d_u = d g s,  s = 1 / (1 + exp(-g))
 //
-// All three pass once over their rows and are bound by those bytes.  A thread
-// takes 16 columns: 8 threads share a block's maximum in registers.
+// All three pass once over their rows.  A thread takes 16 columns, in accesses of
+// 32 bytes: 8 threads share a block's maximum in registers.  Bound by those bytes,
+// and where the codes are made nearly as much by instructions (186 a thread's 16
+// columns, 56 to 67 % of the issue slots).  32768 rows of bf16: 7168 columns to codes
+// 117 us = 6.0 TB/s and back 102 us = 6.9; SwiGLU of 2 x 2048 57 us = 5.9, with the
+// checkpoint 92 = 5.1, its gradient from that 80 us = 6.7, from rows 92 = 7.3.
 #include <algorithm>
 
 #include "rows_common.cuh"

@@ -289,6 +289,7 @@ struct NormArgs {
     int rows, cols, bf16, weight_bf16;
     int wide;                   // as in BlockQuantArgs (weight too)
     int few;                    // set by the launcher: the weight is fetched ahead
+    float inv_cols;             // set by the launcher: 1 / cols
 };
 cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
 
@@ -303,6 +304,7 @@ struct NormGradArgs {
     float* partial;             // [blocks, cols], where d_weight is given
     int rows, cols, bf16, weight_bf16;
     int wide;                   // as in NormArgs
+    float inv_cols;             // as in NormArgs
 };
 // Blocks of the kernel that sums the weight's gradient, each with a partial sum.
 int norm_grad_blocks(int rows);

@@ -6,12 +6,19 @@
 //   with n = z r and g = d_y w:
 //   d_x = r (g - n mean(g n)) + d_residual,  d_w = sum over the rows of d_y n
 //
-// One pass: a block (a warp for short rows) holds its row in registers, joins the
-// sum in shared memory and writes every output, so the bytes moved are the rows
-// read and written.  Sums are float32, over at most 64 terms a thread and then a
-// tree.  In the gradient a block takes rows blockIdx.x, + gridDim.x, ... with the
-// same columns in a thread throughout, which sums d_w of its columns in
-// registers; the blocks' sums are joined by a second kernel in a fixed order.
+// One pass: a block (a warp or a part of one for short rows) holds its row in
+// registers, joins the sum in shared memory and writes every output, so the bytes
+// moved are the rows read and written.  Sums are float32, over at most 32 terms a
+// thread and then a tree.  In the gradient a block of 512 threads on each SM shares
+// them among as many rows as they hold, takes rows in turn with the same columns in
+// a thread throughout, loads the next row while it works on one, and sums d_w of
+// its columns in registers; the blocks' sums are joined by a second kernel in a
+// fixed order.
+//
+// Bound by those bytes, but where codes alone are written by instructions.  32768 x
+// 7168 bf16: y, codes and the residual 344 us = 6.1 TB/s, y alone 143 = 6.6, codes
+// alone 152 = 4.7 (73 % of the issue slots); the gradient with the residual's 313 us =
+// 6.0 TB/s.  16384 x 7168 float32: 285 and 284 us = 7.0 and 6.6 TB/s.
 #include <algorithm>
 
 #include "rows_common.cuh"
@@ -44,6 +51,16 @@ template <typename Args>
 __device__ __forceinline__ void load_weight(const Args& a, int c, float (&w)[kVec]) {
     if (a.weight_bf16) load16<false>(static_cast<const __nv_bfloat16*>(a.weight) + c, w, a.wide);
     else load16<false>(static_cast<const float*>(a.weight) + c, w, a.wide);
+}
+
+// 1 / sqrt(sum / cols + eps): the hardware's root (2^-22) and a Newton step, which leave
+// 2^-23; every thread of a row computes it, and a root and two quotients in full took a
+// quarter of the kernel's instructions (codes alone, 32768 x 7168: 184 us,
+// 174 so).
+__device__ __forceinline__ float rstd_of(float sum, const NormArgs& a) {
+    const float v = fmaf(sum, a.inv_cols, a.eps), y = rsqrtf(v);
+    const float r = fmaf(0.5f * y, fmaf(-v * y, y, 1.0f), y);
+    return y == 0.0f ? 0.0f : r;  // v infinite
 }
 
 __device__ __forceinline__ float rounded(float v, const __nv_bfloat16*) {
@@ -101,7 +118,7 @@ __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
         }
     }
     sum = row_sum<NT>(sum, nt, tid, 0, s_part);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)a.cols) + a.eps));
+    const float rstd = rstd_of(sum, a);
     if (tid == 0 && cols > 0 && a.rstd != nullptr) a.rstd[r] = rstd;
     if (a.y == nullptr && a.q == nullptr) return;
     const int blocks = scale_blocks(a.cols);
@@ -128,6 +145,128 @@ __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
     }
 }
 
+// bf16 rows without a residual, of up to 512 vectors, a thread's vector each: blocks stay
+// and take rows blockIdx.x, + gridDim.x, ..., the weight in registers, the next row on its
+// way to shared memory (two rows ahead: 150 us where one takes 143).  A warp fetches its own
+// 1 KB of a row in 16-byte pieces, so that only its own lanes wait for them.  Where codes
+// are wanted, bound by its 300 instructions a vector.
+constexpr int kAheadThreads = 512, kAheadRows = 2;
+
+__device__ __forceinline__ uint32_t piece_place(uint32_t c) { return c ^ (c >> 3 & 1); }  // in a warp's 64, without bank conflicts
+
+__device__ __forceinline__ void fetch_piece(uint32_t to, const __nv_bfloat16* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void take_piece(uint32_t from, uint32_t* r) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(from) : "memory");
+}
+
+// Two values an instruction: a pair by a pair, or by twice the same.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t square2(uint64_t a, uint64_t sum) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %1, %2;" : "=l"(r) : "l"(a), "l"(sum));
+    return r;
+}
+__device__ __forceinline__ void apart(uint64_t a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a)); }
+
+__global__ void __launch_bounds__(kAheadThreads, 2) rms_norm_ahead_kernel(NormArgs a) {
+    extern __shared__ __align__(16) uint4 s_rows[];  // [kAheadRows][warps][64]
+    __shared__ float s_part[2][kAheadThreads / 32];
+    pdl_prologue();
+    const int nt = (int)blockDim.x, tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c = tid * kVec, pieces = a.cols / 8, blocks = scale_blocks(a.cols);
+    const bool on = c < a.cols;
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x);
+    const int slot_pieces = nt * 2;
+    const uint32_t first = (uint32_t)__cvta_generic_to_shared(s_rows + warp * 64), slot_bytes = slot_pieces * 16;
+    // this lane's two pieces of a row, or none; what is never fetched stays 0
+    const int p0 = warp * 64 + lane, p1 = p0 + 32;
+    const uint32_t to0 = first + piece_place(lane) * 16, to1 = first + piece_place(32 + lane) * 16;
+    for (int i = tid; i < kAheadRows * slot_pieces; i += nt) s_rows[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    const auto fetch = [&](long long r, uint32_t slot) {
+        if (r < a.rows) {
+            const __nv_bfloat16* row = x + (size_t)r * a.cols;
+            if (p0 < pieces) fetch_piece(to0 + slot, row + p0 * 8);
+            if (p1 < pieces) fetch_piece(to1 + slot, row + p1 * 8);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < kAheadRows - 1; ++i) fetch(blockIdx.x + (long long)i * gridDim.x, i * slot_bytes);
+    uint64_t w[kVec / 2];
+    {
+        float f[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) f[j] = 0.0f;
+        if (on) load_weight(a, c, f);
+#pragma unroll
+        for (int j = 0; j < kVec / 2; ++j) w[j] = pair(f[2 * j], f[2 * j + 1]);
+    }
+    const uint32_t own0 = first + piece_place(2 * lane) * 16, own1 = first + piece_place(2 * lane + 1) * 16;
+    uint32_t slot = 0, next = (kAheadRows - 1) * slot_bytes;  // what next held was read before the last barrier
+    int turn = 0;
+    for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        fetch(r + (kAheadRows - 1ll) * gridDim.x, next);
+        next = slot;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAheadRows - 1) : "memory");
+        __syncwarp();
+        const size_t at = (size_t)r * a.cols + c;
+        uint32_t p[8];
+        take_piece(own0 + slot, p);
+        take_piece(own1 + slot, p + 4);
+        slot = slot == (kAheadRows - 1) * slot_bytes ? 0 : slot + slot_bytes;
+        if (on && a.residual_out != nullptr) store32(static_cast<__nv_bfloat16*>(a.residual_out) + at, p, a.wide);
+        uint64_t z[8], sums = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            z[j] = pair(lo_of(p[j]), hi_of(p[j]));
+            sums = square2(z[j], sums);
+        }
+        float sum, odd;
+        apart(sums, sum, odd);
+        sum = row_sum<kAheadThreads>(sum + odd, nt, tid, 0, s_part[turn]);
+        turn ^= 1;
+        const float rstd = rstd_of(sum, a);
+        if (tid == 0 && a.rstd != nullptr) a.rstd[r] = rstd;
+        // the negatives, as encode16 takes them
+        const uint64_t by = pair(-rstd, -rstd);
+        float nv[kVec];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) apart(mul2(mul2(z[j], by), w[j]), nv[2 * j], nv[2 * j + 1]);
+        if (on && a.y != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = pack2(nv[2 * j], nv[2 * j + 1]) ^ 0x80008000u;
+            store32(static_cast<__nv_bfloat16*>(a.y) + at, p, a.wide);
+        }
+        if (a.q != nullptr) {  // every lane takes part in the blocks' maxima
+            float scale;
+            const uint4 codes = encode16(nv, scale);
+            if (on) {
+                *reinterpret_cast<uint4*>(a.q + at) = codes;
+                if (c % kScaleBlock == 0) a.scales[(size_t)r * blocks + c / kScaleBlock] = scale;
+            }
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+cudaError_t norm_ahead(const NormArgs& a, cudaStream_t s) {
+    const int nt = (a.cols / kVec + 31) / 32 * 32;
+    const size_t smem = (size_t)kAheadRows * nt * 32;  // 32 KB at most
+    const long long blocks = std::min<long long>(a.rows, (long long)sm_count() * (2 * kAheadThreads / nt));
+    return launch(rms_norm_ahead_kernel, dim3((unsigned)blocks), dim3(nt), smem, s, a);
+}
+
 template <typename T, int NT, int ROWS, int HELD>
 cudaError_t norm_shape(const NormArgs& a, cudaStream_t s) {
     const int vectors = (a.cols + kVec - 1) / kVec;
@@ -138,6 +277,10 @@ cudaError_t norm_shape(const NormArgs& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
+    // Us, one row a block / blocks that stay, 32768 rows: y of 7168 176 / 143, of 8192
+    // 190 / 160, of 2048 43 / 43; codes of 7168 182 / 160; one row 8.2 / 6.1.  With a residual the
+    // former have as many bytes under way by themselves: y and codes of 4096 174 / 195.
+    if (a.bf16 && a.residual == nullptr && a.cols > 1024 && a.cols <= kAheadThreads * kVec) return norm_ahead(a, s);
     if (a.cols <= 128) return norm_shape<T, 8, 32, 1>(a, s);
     if (a.cols <= 256) return norm_shape<T, 16, 16, 1>(a, s);
     if (a.cols <= 512) return norm_shape<T, 32, 8, 1>(a, s);
@@ -266,7 +409,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_kernel(Norm
         else if (nt == 32) sum = row_sum<32>(sum, nt, tid, 0, nullptr);
         else sum = row_sum<kGradThreads>(sum, nt, tid, group + 1, s_part[turn] + group * (nt >> 5));
         turn ^= 1;
-        const float mean = __fdiv_rn(sum, (float)a.cols);
+        const float mean = sum * a.inv_cols;
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             const int c = (i * nt + tid) * kVec;
@@ -332,6 +475,7 @@ cudaError_t launch_rms_norm(const NormArgs& args, cudaStream_t s) {
     a.wide = aligned32(a.x, a.residual, a.residual_out, a.y) && aligned32(a.weight);
     // One row of 7168: 8.2 us instead of 10.2.  Many rows find the weight in L1 and only
     // pay: 65536 rows of 512 would take 168 us instead of 47.
+    a.inv_cols = 1.0f / (float)a.cols;
     a.few = a.rows <= sm_count() && (a.y != nullptr || a.q != nullptr);
     const cudaError_t err = a.bf16 ? norm_t<__nv_bfloat16>(a, s) : norm_t<float>(a, s);
     note_launch();
@@ -344,6 +488,7 @@ int norm_grad_blocks(int rows) { return std::min(sm_count(), rows); }
 cudaError_t launch_rms_norm_backward(const NormGradArgs& args, cudaStream_t s) {
     NormGradArgs a = args;
     a.wide = aligned32(a.d_y, a.z, a.d_residual, a.d_x) && aligned32(a.weight);
+    a.inv_cols = 1.0f / (float)a.cols;
     if (a.rows == 0)
         return a.d_weight != nullptr ? cudaMemsetAsync(a.d_weight, 0, (size_t)a.cols * sizeof(float), s) : cudaSuccess;
     const GradShape g = grad_shape(a.rows, a.cols);

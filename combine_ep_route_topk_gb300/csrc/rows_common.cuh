@@ -160,6 +160,9 @@ __device__ __forceinline__ uint4 encode16(const float (&nv)[kVec], float& scale)
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
     uint32_t p[8];
+    // zeros, of padded rows or of lanes past the row's end: scale 1 by the same way (the other,
+    // with its divisions, made a norm of 65536 x 1040 rows take 170 us instead of 104)
+    if (top == 0.0f) top = 448.0f;
     if (top >= 0x1p-100f && top <= 0x1.fffffep127f) {
         constexpr float kInv448 = 1.0f / 448.0f;
         scale = top * kInv448;
@@ -182,7 +185,7 @@ __device__ __forceinline__ uint4 encode16(const float (&nv)[kVec], float& scale)
             p[j] = e4m3x2(x, y);
         }
     } else {
-        scale = top == top ? __fdiv_rn(top, 448.0f) : 0.0f;  // 0 for nothing but NaN
+        scale = top == top ? __fdiv_rn(top, 448.0f) : 0.0f;  // nothing but NaN: 1 as for zeros
         if (scale == 0.0f) scale = 1.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[j] = e4m3x2(__fdiv_rn(-nv[2 * j], scale), __fdiv_rn(-nv[2 * j + 1], scale));
