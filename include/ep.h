@@ -41,8 +41,9 @@
  *     EP_ERR_UNSUPPORTED) and launches nothing.  A failed launch returns
  *     EP_ERR_CUDA.  No kernel traps or asserts.  Besides the stream-order wait
  *     of programmatic launch (below), the only waits are the bounded grid
- *     barriers inside ep_route_layout and ep_expert_matmul's bounded waits for
- *     its own copies and products (its status tells if one ran out).
+ *     barriers inside ep_route_layout and the bounded waits of ep_expert_matmul
+ *     and ep_expert_matmul_fp8 for their own copies and products (their status
+ *     tells if one ran out).
  *   - Device-side data that break a precondition (an expert id outside
  *     [0,E), rank_offsets that are not a non-decreasing 0..N sequence, pos
  *     values that do not come from ep_dispatch_layout) never cause an access
@@ -478,7 +479,8 @@ ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_r
  * ep_expert_matmul_fp8 reads; an addition of this library.
  *   v      = x (EP_ACT_NONE), or silu(x[:cols]) * x[cols:] (EP_ACT_SWIGLU, x
  *            rows of 2*cols: the experts' first product, gate half first), in
- *            float32.
+ *            float32; exp and 1 / x are the hardware's (some 2^-22 off, results
+ *            below some 1e-35 may be 0).
  *   scale  = max|v| / 448 over a block of 128 columns (a row's last block may be
  *            shorter); 1 where that quotient is 0.  code = E4M3(v / scale),
  *            rounded to nearest even; quotients by IEEE division, so that
@@ -514,7 +516,8 @@ ep_status_t ep_dequantize_blocks(const uint8_t* q, const float* scales, int32_t 
  * ep_swiglu_backward -- gradient of silu(g) * u with respect to x = (g, u), from
  * x itself or from its 8-bit checkpoint:
  *   d_g = d_out * u * s * (1 + g * (1 - s)),  d_u = d_out * g * s,
- *   s = 1 / (1 + exp(-g)), in float32, rounded once to the rows' type.
+ *   s = 1 / (1 + exp(-g)), in float32 with ep_quantize_blocks's exp and 1 / x,
+ *   rounded once to the rows' type.
  *   d_out  [rows, cols] float32 or bf16 (dtype).
  *   x      x_scales NULL: rows [rows, 2*cols] of the same type.  Else: uint8
  *          codes [rows, 2*cols] with x_scales float32 [rows, ceil(2*cols / 128)]
