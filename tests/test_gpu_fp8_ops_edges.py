@@ -213,3 +213,21 @@ def test_block_codes_in_a_graph_with_other_rows():
         for e, n in enumerate(counts):
             held[e * 24:e * 24 + min(n, 24)] = True
         assert ((dx == 7.0).all(1).cpu() == ~held).all() and ((v == 7.0).all(1).cpu() == ~held).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (37, 48), (19, 144), (9, 1440), (5, 2896), (3, 6096),
+                                       (3, 6160), (3, 8176), (3, 8208)])
+def test_checkpoint_whose_blocks_straddle_the_halves(rows, cols, dtype):
+    """One call writes what two calls write."""
+    x = rows_of(rows, 2 * cols, dtype, cols).cuda()
+    x[0, 5], x[-1, cols + 7] = float("nan"), float("inf")
+    xq = torch.full((rows + 1, 2 * cols), 9, dtype=torch.uint8, device="cuda")
+    xs = torch.full((rows + 1, ep.scale_blocks(2 * cols)), 7.0, device="cuda")
+    q, s = ep.ep_quantize_blocks(x, act=ep.EP_ACT_SWIGLU, x_q=xq[:rows], x_scales=xs[:rows])
+    for a, b in zip((q, s), ep.ep_quantize_blocks(x, act=ep.EP_ACT_SWIGLU)):
+        assert torch.equal(a, b)
+    wq, wsc = ep.ep_quantize_blocks(x)
+    same = (xq[:rows] == wq) | (((xq[:rows] & 127) == 127) & ((wq & 127) == 127))  # NaN of any sign
+    assert same.all() and torch.equal(xs[:rows], wsc)
+    assert (xq[rows] == 9).all() and (xs[rows] == 7.0).all()
