@@ -20,6 +20,7 @@
 // alone 152 = 4.7 (73 % of the issue slots); the gradient with the residual's 313 us =
 // 6.0 TB/s.  16384 x 7168 float32: 285 and 284 us = 7.0 and 6.6 TB/s.
 #include <algorithm>
+#include <atomic>
 
 #include "rows_common.cuh"
 
@@ -334,6 +335,34 @@ GradShape grad_shape(int rows, int cols) {
     return g;
 }
 
+// The block's partial sums of d_w: of one group from its registers, of more joined in s_dw.
+template <int HELD>
+__device__ __forceinline__ void join_groups(const NormGradArgs& a, const GradShape& g, const float (&dw)[HELD][kVec],
+                                            float* s_dw, int group, int tid) {
+    const int nt = g.nt;
+    if (a.d_weight == nullptr) return;
+    float* to = a.partial + (size_t)blockIdx.x * a.cols;
+    if (g.groups > 1) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int c = (i * nt + tid) * kVec;
+            if (c < a.cols) store16f(s_dw + (size_t)group * a.cols + c, dw[i]);
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            float v = 0.0f;
+            for (int k = 0; k < g.groups; ++k) v += s_dw[(size_t)k * a.cols + c];
+            to[c] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int c = (i * nt + tid) * kVec;
+            if (c < a.cols) store16f(to + c, dw[i]);
+        }
+    }
+}
+
 // A row's three arrays load together, and where the registers allow it (HELD = 1) while
 // the row before is worked on.
 template <typename T, int HELD>
@@ -418,27 +447,97 @@ __global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_kernel(Norm
             if (r < a.rows && c < a.cols) store16(static_cast<T*>(a.d_x) + (size_t)r * a.cols + c, n[i], wide);
         }
     }
-    if (a.d_weight == nullptr) return;
-    float* to = a.partial + (size_t)blockIdx.x * a.cols;
-    if (g.groups > 1) {
-#pragma unroll
-        for (int i = 0; i < HELD; ++i) {
-            const int c = (i * nt + tid) * kVec;
-            if (c < a.cols) store16f(s_dw + (size_t)group * a.cols + c, dw[i]);
+    join_groups<HELD>(a, g, dw, s_dw, group, tid);
+}
+
+// bf16 rows of whole warps: the next two rows of a group are on their way to shared memory,
+// as in rms_norm_ahead_kernel (32768 x 7168 with the residual's gradient 283 us, with one row
+// ahead in registers 313; their registers are the limit there).
+constexpr int kGradRows = 3;
+
+__global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_ahead_kernel(NormGradArgs a, GradShape g) {
+    extern __shared__ __align__(16) uint4 s_grad[];  // [kGradRows][z, d_y, d_residual][warps][64]
+    __shared__ float s_part[2][kGradThreads / 32];
+    pdl_prologue();
+    const int nt = g.nt, group = (int)threadIdx.x / nt, tid = (int)threadIdx.x % nt, lane = tid & 31, warp = tid >> 5;
+    const int c = tid * kVec, pieces = a.cols / 8;
+    const bool on = c < a.cols, has_res = a.d_residual != nullptr;
+    const uint32_t array_bytes = blockDim.x * 32, slot_bytes = (has_res ? 3 : 2) * array_bytes;
+    const uint32_t first = (uint32_t)__cvta_generic_to_shared(s_grad) + threadIdx.x / 32 * 1024;
+    const int p0 = warp * 64 + lane, p1 = p0 + 32;
+    const uint32_t to0 = first + piece_place(lane) * 16, to1 = first + piece_place(32 + lane) * 16;
+    const auto fetch_row = [&](const void* rows, size_t at, uint32_t to) {
+        const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(rows) + at;
+        if (p0 < pieces) fetch_piece(to0 + to, row + p0 * 8);
+        if (p1 < pieces) fetch_piece(to1 + to, row + p1 * 8);
+    };
+    const auto fetch = [&](long long r, uint32_t slot) {
+        if (r < a.rows) {
+            const size_t at = (size_t)r * a.cols;
+            fetch_row(a.z, at, slot);
+            fetch_row(a.d_y, at, slot + array_bytes);
+            if (has_res) fetch_row(a.d_residual, at, slot + 2 * array_bytes);
         }
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            float v = 0.0f;
-            for (int k = 0; k < g.groups; ++k) v += s_dw[(size_t)k * a.cols + c];
-            to[c] = v;
-        }
-    } else {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const long long step = (long long)gridDim.x * g.groups;
+    long long r = (long long)blockIdx.x * g.groups + group;
+    for (int i = 0; i < kGradRows - 1; ++i) fetch(r + i * step, i * slot_bytes);
+    float w[kVec], dw[1][kVec];
 #pragma unroll
-        for (int i = 0; i < HELD; ++i) {
-            const int c = (i * nt + tid) * kVec;
-            if (c < a.cols) store16f(to + c, dw[i]);
+    for (int j = 0; j < kVec; ++j) w[j] = dw[0][j] = 0.0f;
+    if (on) load_weight(a, c, w);
+    float next_scale = r < a.rows ? __ldg(a.rstd + r) : 0.0f;
+    const uint32_t own0 = first + piece_place(2 * lane) * 16, own1 = first + piece_place(2 * lane + 1) * 16;
+    uint32_t slot = 0, next = (kGradRows - 1) * slot_bytes;
+    int turn = 0;
+    for (; r < a.rows; r += step) {
+        __syncwarp();  // what lies in next has been read
+        fetch(r + (kGradRows - 1) * step, next);
+        next = slot;
+        const float scale = next_scale;
+        if (r + step < a.rows) next_scale = __ldg(a.rstd + r + step);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kGradRows - 1) : "memory");
+        __syncwarp();
+        uint32_t z[8], d[8], res[8];
+        take_piece(own0 + slot, z);
+        take_piece(own1 + slot, z + 4);
+        take_piece(own0 + slot + array_bytes, d);
+        take_piece(own1 + slot + array_bytes, d + 4);
+        if (has_res) {
+            take_piece(own0 + slot + 2 * array_bytes, res);
+            take_piece(own1 + slot + 2 * array_bytes, res + 4);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) res[j] = 0;
+        }
+        slot = slot == (kGradRows - 1) * slot_bytes ? 0 : slot + slot_bytes;
+        float n[kVec], gy[kVec], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            n[j] = gy[j] = 0.0f;
+            if (on) {
+                n[j] = (j % 2 ? hi_of(z[j / 2]) : lo_of(z[j / 2])) * scale;
+                gy[j] = j % 2 ? hi_of(d[j / 2]) : lo_of(d[j / 2]);
+            }
+            dw[0][j] = fmaf(gy[j], n[j], dw[0][j]);
+            gy[j] *= w[j];
+            sum = fmaf(gy[j], n[j], sum);
+        }
+        if (nt == 32) sum = row_sum<32>(sum, nt, tid, 0, nullptr);
+        else sum = row_sum<kGradThreads>(sum, nt, tid, group + 1, s_part[turn] + group * (nt >> 5));
+        turn ^= 1;
+        const float mean = sum * a.inv_cols;
+        if (on) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                n[j] = fmaf(scale, fmaf(-n[j], mean, gy[j]), j % 2 ? hi_of(res[j / 2]) : lo_of(res[j / 2]));
+            store16(static_cast<__nv_bfloat16*>(a.d_x) + (size_t)r * a.cols + c, n, a.wide);
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();  // the rows' memory takes the groups' sums
+    join_groups<1>(a, g, dw, reinterpret_cast<float*>(s_grad), group, tid);
 }
 
 // Sum of the blocks' partial sums: 32 columns a block, 32 strands of partial sums
@@ -458,11 +557,30 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(NormGradArgs a, int p
     if (lane == 0 && blockIdx.x * 32 + strand < (unsigned)a.cols) a.d_weight[blockIdx.x * 32 + strand] = v;
 }
 
+// More than 48 KB of dynamic shared memory, allowed once for each device.
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<bool> (&done)[64]) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess || (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed))) return err;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+    return err;
+}
+
 template <typename T>
 cudaError_t grad_t(const NormGradArgs& a, const GradShape& g, cudaStream_t s) {
+    const dim3 grid(g.blocks), block(g.nt * g.groups);
+    if (sizeof(T) == 2 && g.nt >= 32 && grad_held(a.cols) == 1) {
+        static std::atomic<bool> done[64];
+        const int row_bytes = 32 * kGradRows;  // of a thread, of each array
+        const cudaError_t err = allow_smem(reinterpret_cast<const void*>(rms_norm_backward_ahead_kernel),
+                                           3 * row_bytes * kGradThreads, done);
+        if (err != cudaSuccess) return err;
+        return launch(rms_norm_backward_ahead_kernel, grid, block,
+                      (size_t)(a.d_residual != nullptr ? 3 : 2) * row_bytes * block.x, s, a, g);
+    }
     // at most 512 threads of 16 columns: 32 KB
     const size_t smem = g.groups > 1 ? (size_t)g.groups * a.cols * sizeof(float) : 0;
-    const dim3 grid(g.blocks), block(g.nt * g.groups);
     return grad_held(a.cols) == 1 ? launch(rms_norm_backward_kernel<T, 1>, grid, block, smem, s, a, g)
                                   : launch(rms_norm_backward_kernel<T, 2>, grid, block, smem, s, a, g);
 }
