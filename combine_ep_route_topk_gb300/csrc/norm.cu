@@ -11,14 +11,14 @@
 // moved are the rows read and written.  Sums are float32, over at most 32 terms a
 // thread and then a tree.  In the gradient a block of 512 threads on each SM shares
 // them among as many rows as they hold, takes rows in turn with the same columns in
-// a thread throughout, loads the next row while it works on one, and sums d_w of
-// its columns in registers; the blocks' sums are joined by a second kernel in a
-// fixed order.
+// a thread throughout, has the next rows on their way to shared memory (registers
+// for the shortest and longest rows) and sums d_w of its columns in registers; the
+// blocks' sums are joined by a second kernel in a fixed order.
 //
 // Bound by those bytes, but where codes alone are written by instructions.  32768 x
 // 7168 bf16: y, codes and the residual 344 us = 6.1 TB/s, y alone 143 = 6.6, codes
-// alone 152 = 4.7 (73 % of the issue slots); the gradient with the residual's 313 us =
-// 6.0 TB/s.  16384 x 7168 float32: 285 and 284 us = 7.0 and 6.6 TB/s.
+// alone 152 = 4.7 (73 % of the issue slots); the gradient with the residual's 284 us =
+// 6.6 TB/s.  16384 x 7168 float32: 285 and 262 us = 7.0 and 7.2 TB/s.
 #include <algorithm>
 #include <atomic>
 
@@ -153,14 +153,26 @@ __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
 // are wanted, bound by its 300 instructions a vector.
 constexpr int kAheadThreads = 512, kAheadRows = 2;
 
-__device__ __forceinline__ uint32_t piece_place(uint32_t c) { return c ^ (c >> 3 & 1); }  // in a warp's 64, without bank conflicts
-
-__device__ __forceinline__ void fetch_piece(uint32_t to, const __nv_bfloat16* from) {
+// Where piece c of a warp's lies, so that lanes that read their vectors' i-th pieces meet
+// no bank conflicts.
+template <typename T>
+__device__ __forceinline__ uint32_t piece_place(uint32_t c) {
+    return c ^ (c >> 3 & (sizeof(T) == 2 ? 1 : 3));
+}
+__device__ __forceinline__ void fetch_piece(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void take_piece(uint32_t from, uint32_t* r) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(from) : "memory");
 }
+// A lane's vector as it lies in memory, and its values.
+template <typename T>
+__device__ __forceinline__ void take_vector(const uint32_t (&own)[sizeof(T)], uint32_t slot, uint32_t (&r)[4 * sizeof(T)]) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) take_piece(own[i] + slot, r + 4 * i);
+}
+__device__ __forceinline__ float value_of(const uint32_t (&r)[8], int j) { return j % 2 ? hi_of(r[j / 2]) : lo_of(r[j / 2]); }
+__device__ __forceinline__ float value_of(const uint32_t (&r)[16], int j) { return __uint_as_float(r[j]); }
 
 // Two values an instruction: a pair by a pair, or by twice the same.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -192,7 +204,7 @@ __global__ void __launch_bounds__(kAheadThreads, 2) rms_norm_ahead_kernel(NormAr
     const uint32_t first = (uint32_t)__cvta_generic_to_shared(s_rows + warp * 64), slot_bytes = slot_pieces * 16;
     // this lane's two pieces of a row, or none; what is never fetched stays 0
     const int p0 = warp * 64 + lane, p1 = p0 + 32;
-    const uint32_t to0 = first + piece_place(lane) * 16, to1 = first + piece_place(32 + lane) * 16;
+    const uint32_t to0 = first + piece_place<__nv_bfloat16>(lane) * 16, to1 = first + piece_place<__nv_bfloat16>(32 + lane) * 16;
     for (int i = tid; i < kAheadRows * slot_pieces; i += nt) s_rows[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const auto fetch = [&](long long r, uint32_t slot) {
@@ -213,7 +225,7 @@ __global__ void __launch_bounds__(kAheadThreads, 2) rms_norm_ahead_kernel(NormAr
 #pragma unroll
         for (int j = 0; j < kVec / 2; ++j) w[j] = pair(f[2 * j], f[2 * j + 1]);
     }
-    const uint32_t own0 = first + piece_place(2 * lane) * 16, own1 = first + piece_place(2 * lane + 1) * 16;
+    const uint32_t own0 = first + piece_place<__nv_bfloat16>(2 * lane) * 16, own1 = first + piece_place<__nv_bfloat16>(2 * lane + 1) * 16;
     uint32_t slot = 0, next = (kAheadRows - 1) * slot_bytes;  // what next held was read before the last barrier
     int turn = 0;
     for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -363,8 +375,8 @@ __device__ __forceinline__ void join_groups(const NormGradArgs& a, const GradSha
     }
 }
 
-// A row's three arrays load together, and where the registers allow it (HELD = 1) while
-// the row before is worked on.
+// Rows of a part of a warp (HELD = 1) or of more than 512 vectors (2): a row's three arrays
+// load together, and with HELD = 1 while the row before is worked on.
 template <typename T, int HELD>
 __global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_kernel(NormGradArgs a, GradShape g) {
     extern __shared__ __align__(16) float s_dw[];  // [groups][cols], for more than one group
@@ -450,26 +462,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_kernel(Norm
     join_groups<HELD>(a, g, dw, s_dw, group, tid);
 }
 
-// bf16 rows of whole warps: the next two rows of a group are on their way to shared memory,
-// as in rms_norm_ahead_kernel (32768 x 7168 with the residual's gradient 283 us, with one row
-// ahead in registers 313; their registers are the limit there).
-constexpr int kGradRows = 3;
-
+// Rows of whole warps, a thread's vector each: the next rows of a group (ROWS - 1 of them)
+// are on their way to shared memory, as in rms_norm_ahead_kernel.  32768 x 7168 bf16 with the
+// residual's gradient 283 us, with one row ahead in registers 313; 5003 x 2880 float32 31 us
+// instead of 37.  Registers allow one block an SM (two of 64 a thread, the weight read twice
+// from what is left of L1: 469).
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_ahead_kernel(NormGradArgs a, GradShape g) {
-    extern __shared__ __align__(16) uint4 s_grad[];  // [kGradRows][z, d_y, d_residual][warps][64]
+    constexpr int kPieces = sizeof(T);  // of 16 bytes in a vector
+    constexpr bool kEarly = sizeof(T) == 2;
+    extern __shared__ __align__(16) uint4 s_grad[];  // [ROWS][z, d_y, d_residual][warps][32 kPieces]
     __shared__ float s_part[2][kGradThreads / 32];
     pdl_prologue();
     const int nt = g.nt, group = (int)threadIdx.x / nt, tid = (int)threadIdx.x % nt, lane = tid & 31, warp = tid >> 5;
-    const int c = tid * kVec, pieces = a.cols / 8;
+    const int c = tid * kVec, pieces = a.cols / kVec * kPieces;
     const bool on = c < a.cols, has_res = a.d_residual != nullptr;
-    const uint32_t array_bytes = blockDim.x * 32, slot_bytes = (has_res ? 3 : 2) * array_bytes;
-    const uint32_t first = (uint32_t)__cvta_generic_to_shared(s_grad) + threadIdx.x / 32 * 1024;
-    const int p0 = warp * 64 + lane, p1 = p0 + 32;
-    const uint32_t to0 = first + piece_place(lane) * 16, to1 = first + piece_place(32 + lane) * 16;
-    const auto fetch_row = [&](const void* rows, size_t at, uint32_t to) {
-        const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(rows) + at;
-        if (p0 < pieces) fetch_piece(to0 + to, row + p0 * 8);
-        if (p1 < pieces) fetch_piece(to1 + to, row + p1 * 8);
+    const uint32_t array_bytes = blockDim.x * 16 * kPieces, slot_bytes = (has_res ? 3 : 2) * array_bytes;
+    const uint32_t first = (uint32_t)__cvta_generic_to_shared(s_grad) + threadIdx.x / 32 * (512 * kPieces);
+    uint32_t to[kPieces], own[kPieces];  // the pieces that this lane fetches, and those of its vector
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        to[i] = first + piece_place<T>(32 * i + lane) * 16;
+        own[i] = first + piece_place<T>(kPieces * lane + i) * 16;
+    }
+    const auto fetch_row = [&](const void* rows, size_t at, uint32_t slot) {
+        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const T*>(rows) + at);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = (warp * kPieces + i) * 32 + lane;
+            if (p < pieces) fetch_piece(to[i] + slot, row + p);
+        }
     };
     const auto fetch = [&](long long r, uint32_t slot) {
         if (r < a.rows) {
@@ -482,44 +504,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_ahead_kerne
     };
     const long long step = (long long)gridDim.x * g.groups;
     long long r = (long long)blockIdx.x * g.groups + group;
-    for (int i = 0; i < kGradRows - 1; ++i) fetch(r + i * step, i * slot_bytes);
+    for (int i = 0; i < ROWS - 1; ++i) fetch(r + i * step, i * slot_bytes);
     float w[kVec], dw[1][kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) w[j] = dw[0][j] = 0.0f;
     if (on) load_weight(a, c, w);
     float next_scale = r < a.rows ? __ldg(a.rstd + r) : 0.0f;
-    const uint32_t own0 = first + piece_place(2 * lane) * 16, own1 = first + piece_place(2 * lane + 1) * 16;
-    uint32_t slot = 0, next = (kGradRows - 1) * slot_bytes;
+    uint32_t slot = 0, next = (ROWS - 1) * slot_bytes;
     int turn = 0;
     for (; r < a.rows; r += step) {
         __syncwarp();  // what lies in next has been read
-        fetch(r + (kGradRows - 1) * step, next);
+        fetch(r + (ROWS - 1) * step, next);
         next = slot;
         const float scale = next_scale;
         if (r + step < a.rows) next_scale = __ldg(a.rstd + r + step);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kGradRows - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(ROWS - 1) : "memory");
         __syncwarp();
-        uint32_t z[8], d[8], res[8];
-        take_piece(own0 + slot, z);
-        take_piece(own1 + slot, z + 4);
-        take_piece(own0 + slot + array_bytes, d);
-        take_piece(own1 + slot + array_bytes, d + 4);
-        if (has_res) {
-            take_piece(own0 + slot + 2 * array_bytes, res);
-            take_piece(own1 + slot + 2 * array_bytes, res + 4);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) res[j] = 0;
-        }
-        slot = slot == (kGradRows - 1) * slot_bytes ? 0 : slot + slot_bytes;
+        uint32_t z[4 * kPieces], d[4 * kPieces], res[4 * kPieces];
+        take_vector<T>(own, slot, z);
+        take_vector<T>(own, slot + array_bytes, d);
+        // float32 has no registers for these before the sum
+        if (kEarly && has_res) take_vector<T>(own, slot + 2 * array_bytes, res);
         float n[kVec], gy[kVec], sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            n[j] = gy[j] = 0.0f;
-            if (on) {
-                n[j] = (j % 2 ? hi_of(z[j / 2]) : lo_of(z[j / 2])) * scale;
-                gy[j] = j % 2 ? hi_of(d[j / 2]) : lo_of(d[j / 2]);
-            }
+            n[j] = on ? value_of(z, j) * scale : 0.0f;
+            gy[j] = on ? value_of(d, j) : 0.0f;
             dw[0][j] = fmaf(gy[j], n[j], dw[0][j]);
             gy[j] *= w[j];
             sum = fmaf(gy[j], n[j], sum);
@@ -529,11 +539,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) rms_norm_backward_ahead_kerne
         turn ^= 1;
         const float mean = sum * a.inv_cols;
         if (on) {
+            if (!kEarly && has_res) take_vector<T>(own, slot + 2 * array_bytes, res);
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                n[j] = fmaf(scale, fmaf(-n[j], mean, gy[j]), j % 2 ? hi_of(res[j / 2]) : lo_of(res[j / 2]));
-            store16(static_cast<__nv_bfloat16*>(a.d_x) + (size_t)r * a.cols + c, n, a.wide);
+                n[j] = fmaf(scale, fmaf(-n[j], mean, gy[j]), has_res ? value_of(res, j) : 0.0f);
+            store16(static_cast<T*>(a.d_x) + (size_t)r * a.cols + c, n, a.wide);
         }
+        slot = slot == (ROWS - 1) * slot_bytes ? 0 : slot + slot_bytes;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();  // the rows' memory takes the groups' sums
@@ -567,18 +579,28 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<bool> (&done)[
     return err;
 }
 
+template <typename T, int ROWS>
+cudaError_t grad_ahead(const NormGradArgs& a, const GradShape& g, cudaStream_t s) {
+    static std::atomic<bool> done[64];
+    constexpr int kBytes = ROWS * 16 * (int)sizeof(T);  // of a thread, of each array
+    const int threads = g.nt * g.groups, arrays = a.d_residual != nullptr ? 3 : 2;
+    const cudaError_t err = allow_smem(reinterpret_cast<const void*>(rms_norm_backward_ahead_kernel<T, ROWS>),
+                                       (sizeof(T) == 4 && ROWS == 3 ? 2 : 3) * kBytes * kGradThreads, done);
+    if (err != cudaSuccess) return err;
+    return launch(rms_norm_backward_ahead_kernel<T, ROWS>, dim3(g.blocks), dim3(threads), (size_t)arrays * kBytes * threads,
+                  s, a, g);
+}
+
 template <typename T>
 cudaError_t grad_t(const NormGradArgs& a, const GradShape& g, cudaStream_t s) {
-    const dim3 grid(g.blocks), block(g.nt * g.groups);
-    if (sizeof(T) == 2 && g.nt >= 32 && grad_held(a.cols) == 1) {
-        static std::atomic<bool> done[64];
-        const int row_bytes = 32 * kGradRows;  // of a thread, of each array
-        const cudaError_t err = allow_smem(reinterpret_cast<const void*>(rms_norm_backward_ahead_kernel),
-                                           3 * row_bytes * kGradThreads, done);
-        if (err != cudaSuccess) return err;
-        return launch(rms_norm_backward_ahead_kernel, grid, block,
-                      (size_t)(a.d_residual != nullptr ? 3 : 2) * row_bytes * block.x, s, a, g);
+    // whole warps a row, a vector a thread: through shared memory, three rows of a group where
+    // they fit (float32 with a residual's gradient: two, 196 KB)
+    if (g.nt >= 32 && grad_held(a.cols) == 1) {
+        if constexpr (sizeof(T) == 4)
+            if (a.d_residual != nullptr) return grad_ahead<T, 2>(a, g, s);
+        return grad_ahead<T, 3>(a, g, s);
     }
+    const dim3 grid(g.blocks), block(g.nt * g.groups);
     // at most 512 threads of 16 columns: 32 KB
     const size_t smem = g.groups > 1 ? (size_t)g.groups * a.cols * sizeof(float) : 0;
     return grad_held(a.cols) == 1 ? launch(rms_norm_backward_kernel<T, 1>, grid, block, smem, s, a, g)
