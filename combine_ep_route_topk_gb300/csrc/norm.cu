@@ -16,8 +16,8 @@
 // blocks' sums are joined by a second kernel in a fixed order.
 //
 // Bound by those bytes, but where codes alone are written by instructions.  32768 x
-// 7168 bf16: y, codes and the residual 344 us = 6.1 TB/s, y alone 143 = 6.6, codes
-// alone 152 = 4.7 (73 % of the issue slots); the gradient with the residual's 284 us =
+// 7168 bf16: y, codes and the residual 311 us = 6.8 TB/s, y alone 141 = 6.7, codes
+// alone 152 = 4.7 (70 % of the issue slots); the gradient with the residual's 284 us =
 // 6.6 TB/s.  16384 x 7168 float32: 285 and 262 us = 7.0 and 7.2 TB/s.
 #include <algorithm>
 #include <atomic>
@@ -64,15 +64,63 @@ __device__ __forceinline__ float rstd_of(float sum, const NormArgs& a) {
     return y == 0.0f ? 0.0f : r;  // v infinite
 }
 
-__device__ __forceinline__ float rounded(float v, const __nv_bfloat16*) {
-    return __bfloat162float(__float2bfloat16_rn(v));
+// Sixteen columns as they lie in memory.
+template <typename T>
+struct Raw {
+    uint32_t r[kVec * sizeof(T) / 32][8];
+    __device__ __forceinline__ void load(const T* p, bool wide) {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h) load32<true>(p + h * (32 / sizeof(T)), r[h], wide);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[h][i] = 0;
+    }
+    // The sums with t's, rounded to the type.
+    __device__ __forceinline__ void add(const Raw& t) {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r[h][i] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(r[h][i]) + __uint_as_float(t.r[h][i]))
+                                         : pack2(lo_of(r[h][i]) + lo_of(t.r[h][i]), hi_of(r[h][i]) + hi_of(t.r[h][i]));
+    }
+    __device__ __forceinline__ void store(T* p, bool wide) const {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h) store32(p + h * (32 / sizeof(T)), r[h], wide);
+    }
+    __device__ __forceinline__ float at(int j) const {
+        if (sizeof(T) == 4) return __uint_as_float(r[j / 8][j % 8]);
+        return j % 2 ? hi_of(r[0][j / 2]) : lo_of(r[0][j / 2]);
+    }
+};
+
+// Stores the negatives of what v holds.
+__device__ __forceinline__ void store_negated(__nv_bfloat16* p, const float (&v)[kVec], bool wide) {
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = pack2(v[2 * i], v[2 * i + 1]) ^ 0x80008000u;
+    store32(p, r, wide);
 }
-__device__ __forceinline__ float rounded(float v, const float*) { return v; }
+__device__ __forceinline__ void store_negated(float* p, const float (&v)[kVec], bool wide) {
+    float n[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) n[i] = -v[i];
+    store16(p, n, wide);
+}
+
+// Blocks an SM that the registers are to allow.  Rows held as they lie in memory (bf16: half
+// of the registers) and these bounds: 32768 x 7168 bf16 with the residual, y and codes 311 us,
+// held as float32 with 4 blocks of 62 registers 344; 8192 x 16384 174 and 291 (one block).
+template <typename T, int NT, int HELD>
+constexpr int kMinBlocks = NT == 512 ? 2 : NT == 256 && (HELD == 1 || sizeof(T) == 2) ? 5 : 1;
 
 // Up to NT threads a row, HELD vectors of 16 each: whole warps and a row a block
 // (ROWS = 1), or NT = 8, 16 or 32 threads and ROWS rows a block.
 template <typename T, int NT, int ROWS, int HELD>
-__global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(NT * ROWS, kMinBlocks<T, NT, HELD>) rms_norm_kernel(NormArgs a) {
     static_assert(ROWS == 1 || NT <= 32, "a warp or a part of one for each of several rows");
     __shared__ float s_part[(NT + 31) / 32];
     pdl_prologue();
@@ -91,31 +139,29 @@ __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
                 asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const char*>(a.weight) + (size_t)c * (a.weight_bf16 ? 2 : 4)));
         }
     }
-    float z[HELD][kVec];
+    Raw<T> z[HELD];
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
         const int c = (i * nt + tid) * kVec;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) z[i][j] = 0.0f;
+        z[i].zero();
         if (c < cols) {
-            load16<true>(x + c, z[i], a.wide);
+            z[i].load(x + c, a.wide);
             if (res != nullptr) {
-                float t[kVec];
-                load16<true>(res + c, t, a.wide);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) z[i][j] = rounded(z[i][j] + t[j], x);
+                Raw<T> t;
+                t.load(res + c, a.wide);
+                z[i].add(t);
             }
         }
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) sum = fmaf(z[i][j], z[i][j], sum);
+        for (int j = 0; j < kVec; ++j) sum = fmaf(z[i].at(j), z[i].at(j), sum);
     }
     if (a.residual_out != nullptr) {
         T* to = static_cast<T*>(a.residual_out) + at;
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             const int c = (i * nt + tid) * kVec;
-            if (c < cols) store16(to + c, z[i], a.wide);
+            if (c < cols) z[i].store(to + c, a.wide);
         }
     }
     sum = row_sum<NT>(sum, nt, tid, 0, s_part);
@@ -126,18 +172,19 @@ __global__ void __launch_bounds__(NT * ROWS) rms_norm_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
         const int c = (i * nt + tid) * kVec;
+        float nv[kVec];  // the negatives, as encode16 takes them
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) nv[j] = 0.0f;
         if (c < cols) {
             float w[kVec];
             load_weight(a, c, w);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) z[i][j] = z[i][j] * rstd * w[j];
-            if (a.y != nullptr) store16(static_cast<T*>(a.y) + at + c, z[i], a.wide);
+            for (int j = 0; j < kVec; ++j) nv[j] = z[i].at(j) * -rstd * w[j];
+            if (a.y != nullptr) store_negated(static_cast<T*>(a.y) + at + c, nv, a.wide);
         }
         if (a.q != nullptr) {  // every lane takes part in the blocks' maxima
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) z[i][j] = -z[i][j];
             float scale;
-            const uint4 codes = encode16(z[i], scale);
+            const uint4 codes = encode16(nv, scale);
             if (c < cols) {
                 *reinterpret_cast<uint4*>(a.q + at + c) = codes;
                 if (c % kScaleBlock == 0) a.scales[(size_t)r * blocks + c / kScaleBlock] = scale;
@@ -256,11 +303,7 @@ __global__ void __launch_bounds__(kAheadThreads, 2) rms_norm_ahead_kernel(NormAr
         float nv[kVec];
 #pragma unroll
         for (int j = 0; j < 8; ++j) apart(mul2(mul2(z[j], by), w[j]), nv[2 * j], nv[2 * j + 1]);
-        if (on && a.y != nullptr) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = pack2(nv[2 * j], nv[2 * j + 1]) ^ 0x80008000u;
-            store32(static_cast<__nv_bfloat16*>(a.y) + at, p, a.wide);
-        }
+        if (on && a.y != nullptr) store_negated(static_cast<__nv_bfloat16*>(a.y) + at, nv, a.wide);
         if (a.q != nullptr) {  // every lane takes part in the blocks' maxima
             float scale;
             const uint4 codes = encode16(nv, scale);
@@ -290,9 +333,10 @@ cudaError_t norm_shape(const NormArgs& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
-    // Us, one row a block / blocks that stay, 32768 rows: y of 7168 176 / 143, of 8192
-    // 190 / 160, of 2048 43 / 43; codes of 7168 182 / 160; one row 8.2 / 6.1.  With a residual the
-    // former have as many bytes under way by themselves: y and codes of 4096 174 / 195.
+    // Us, one row a block / blocks that stay, 32768 rows: y of 7168 160 / 141, of 4096 86 / 82,
+    // of 2048 43 / 41; codes of 7168 168 / 152, of 2048 47 / 47; both of 7168 203 / 184, of 2048
+    // 53 / 55; one row 8.2 / 6.1.  With a residual the former are at the copy rate by
+    // themselves (311, the latter 342).
     if (a.bf16 && a.residual == nullptr && a.cols > 1024 && a.cols <= kAheadThreads * kVec) return norm_ahead(a, s);
     if (a.cols <= 128) return norm_shape<T, 8, 32, 1>(a, s);
     if (a.cols <= 256) return norm_shape<T, 16, 16, 1>(a, s);
@@ -311,26 +355,6 @@ __device__ __forceinline__ void store16f(float* p, const float (&v)[kVec]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
-
-// Sixteen columns as they lie in memory.
-template <typename T>
-struct Raw {
-    uint32_t r[kVec * sizeof(T) / 32][8];
-    __device__ __forceinline__ void load(const T* p, bool wide) {
-#pragma unroll
-        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h) load32<true>(p + h * (32 / sizeof(T)), r[h], wide);
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[h][i] = 0;
-    }
-    __device__ __forceinline__ float at(int j) const {
-        if (sizeof(T) == 4) return __uint_as_float(r[j / 8][j % 8]);
-        return j % 2 ? hi_of(r[0][j / 2]) : lo_of(r[0][j / 2]);
-    }
-};
 
 // How the threads share the rows: nt threads a row, `groups` rows at a time in a block.
 struct GradShape {
