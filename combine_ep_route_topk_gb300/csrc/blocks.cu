@@ -10,8 +10,8 @@
 // 32 bytes: 8 threads share a block's maximum in registers.  Bound by those bytes,
 // and where the codes are made nearly as much by instructions (186 a thread's 16
 // columns, 56 to 67 % of the issue slots).  32768 rows of bf16: 7168 columns to codes
-// 117 us = 6.0 TB/s and back 102 us = 6.9; SwiGLU of 2 x 2048 57 us = 5.9, with the
-// checkpoint 92 = 5.1, its gradient from that 80 us = 6.7, from rows 92 = 7.3.
+// 117 us = 6.0 TB/s and back 102 us = 6.9; SwiGLU of 2 x 2048 53 us = 6.3, with the
+// checkpoint 90 = 5.2, its gradient from that 80 us = 6.7, from rows 92 = 7.3.
 #include <algorithm>
 
 #include "rows_common.cuh"
@@ -53,9 +53,11 @@ __device__ __forceinline__ Place place(uint64_t i, uint32_t pieces) {
     return p;
 }
 
-// KEEP: also the codes of x, whose blocks lie on the halves' (cols a multiple of 128).
+// KEEP: also the codes of x, whose blocks lie on the halves' (cols a multiple of 128).  x
+// stays as it lies in memory, so that registers allow 6, 5 or 4 blocks an SM (as float32,
+// and 4 blocks with the checkpoint, 94 us where this takes 90; 57 and 53 without it).
 template <typename T, bool SWIGLU, bool KEEP>
-__global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(BlockQuantArgs a, Divisor per_row) {
+__global__ void __launch_bounds__(kThreads, !KEEP ? 6 : sizeof(T) == 2 ? 5 : 4) quantize_blocks_kernel(BlockQuantArgs a, Divisor per_row) {
     pdl_prologue();
     const int blocks = (int)per_row.d;
     // the block of 128 that this thread's 8 lanes hold, below 2^31 of them
@@ -67,15 +69,16 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(BlockQuantArg
     const bool row_on = p.row < (uint32_t)a.rows && holds_token(a.tokens, p.row);
     const bool on = row_on && p.col < a.cols;
     const size_t r = p.row;
-    float v[kVec], u[kVec];  // the values' negatives, as encode16 takes them
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) v[j] = u[j] = 0.0f;
+    const T* row = static_cast<const T*>(a.x) + r * (SWIGLU ? 2 * (size_t)a.cols : (size_t)a.cols) + p.col;
+    Raw<T> g, u;
+    g.zero();
+    u.zero();
     if (on) {
-        const T* row = static_cast<const T*>(a.x) + r * (SWIGLU ? 2 * (size_t)a.cols : (size_t)a.cols) + p.col;
-        load16<true, true>(row, v, a.wide);
-        if constexpr (SWIGLU) load16<true, true>(row + a.cols, u, a.wide);
+        g.load(row, a.wide);
+        if constexpr (SWIGLU) u.load(row + a.cols, a.wide);
     }
-    float scale;
+    float v[kVec], scale;  // the values' negatives, as encode16 takes them
+    g.negatives(v);
     if constexpr (KEEP) {
         const uint4 g_codes = encode16(v, scale);
         const size_t wide = 2 * (size_t)a.cols;
@@ -83,15 +86,18 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(BlockQuantArg
             *reinterpret_cast<uint4*>(a.x_q + r * wide + p.col) = g_codes;
             if (p.col % kScaleBlock == 0) a.x_scales[r * 2 * blocks + p.col / kScaleBlock] = scale;
         }
-        const uint4 u_codes = encode16(u, scale);
+        float w[kVec];
+        u.negatives(w);
+        const uint4 u_codes = encode16(w, scale);
         if (on) {
             *reinterpret_cast<uint4*>(a.x_q + r * wide + a.cols + p.col) = u_codes;
             if (p.col % kScaleBlock == 0) a.x_scales[r * 2 * blocks + blocks + p.col / kScaleBlock] = scale;
         }
     }
     if constexpr (SWIGLU) {
+        if constexpr (KEEP) g.negatives(v);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = v[j] * fast_rcp(1.0f + fast_exp(v[j])) * -u[j];
+        for (int j = 0; j < kVec; ++j) v[j] = v[j] * fast_rcp(1.0f + fast_exp(v[j])) * u.at(j);
     }
     const uint4 codes = encode16(v, scale);
     if (on) {

@@ -64,39 +64,6 @@ __device__ __forceinline__ float rstd_of(float sum, const NormArgs& a) {
     return y == 0.0f ? 0.0f : r;  // v infinite
 }
 
-// Sixteen columns as they lie in memory.
-template <typename T>
-struct Raw {
-    uint32_t r[kVec * sizeof(T) / 32][8];
-    __device__ __forceinline__ void load(const T* p, bool wide) {
-#pragma unroll
-        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h) load32<true>(p + h * (32 / sizeof(T)), r[h], wide);
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[h][i] = 0;
-    }
-    // The sums with t's, rounded to the type.
-    __device__ __forceinline__ void add(const Raw& t) {
-#pragma unroll
-        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                r[h][i] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(r[h][i]) + __uint_as_float(t.r[h][i]))
-                                         : pack2(lo_of(r[h][i]) + lo_of(t.r[h][i]), hi_of(r[h][i]) + hi_of(t.r[h][i]));
-    }
-    __device__ __forceinline__ void store(T* p, bool wide) const {
-#pragma unroll
-        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h) store32(p + h * (32 / sizeof(T)), r[h], wide);
-    }
-    __device__ __forceinline__ float at(int j) const {
-        if (sizeof(T) == 4) return __uint_as_float(r[j / 8][j % 8]);
-        return j % 2 ? hi_of(r[0][j / 2]) : lo_of(r[0][j / 2]);
-    }
-};
-
 // Stores the negatives of what v holds.
 __device__ __forceinline__ void store_negated(__nv_bfloat16* p, const float (&v)[kVec], bool wide) {
     uint32_t r[8];

@@ -20,11 +20,6 @@ constexpr int kLanes = kScaleBlock / kVec;
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ void unpack8(const uint4& q, float* v) {
-    v[0] = lo_of(q.x); v[1] = hi_of(q.x); v[2] = lo_of(q.y); v[3] = hi_of(q.y);
-    v[4] = lo_of(q.z); v[5] = hi_of(q.z); v[6] = lo_of(q.w); v[7] = hi_of(q.w);
-}
-
 // 32 bytes that start on a boundary of 32, in one access (whole sectors of memory: two
 // of 16 bytes by each thread, 32 apart, ask for every sector twice).
 template <bool STREAM>
@@ -63,27 +58,26 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool wi
 }
 
 // 16 columns, once (streamed: nothing reads them again) or kept in cache; wide: rows
-// start on 32 bytes; NEG: their negatives.
-template <bool STREAM, bool NEG = false>
+// start on 32 bytes.
+template <bool STREAM>
 __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[kVec], bool wide) {
     uint32_t r[8];
     load32<STREAM>(p, r, wide);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (NEG) r[i] ^= 0x80008000u;
         v[2 * i] = lo_of(r[i]);
         v[2 * i + 1] = hi_of(r[i]);
     }
 }
-template <bool STREAM, bool NEG = false>
+template <bool STREAM>
 __device__ __forceinline__ void load16(const float* p, float (&v)[kVec], bool wide) {
     uint32_t r[8], t[8];
     load32<STREAM>(p, r, wide);
     load32<STREAM>(p + 8, t, wide);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        v[i] = __uint_as_float(r[i] ^ (NEG ? 0x80000000u : 0u));
-        v[8 + i] = __uint_as_float(t[i] ^ (NEG ? 0x80000000u : 0u));
+        v[i] = __uint_as_float(r[i]);
+        v[8 + i] = __uint_as_float(t[i]);
     }
 }
 
@@ -106,6 +100,53 @@ __device__ __forceinline__ void store16(float* p, const float (&v)[kVec], bool w
         store32(p + h, r, wide);
     }
 }
+
+// Sixteen columns as they lie in memory.
+template <typename T>
+struct Raw {
+    uint32_t r[kVec * sizeof(T) / 32][8];
+    __device__ __forceinline__ void load(const T* p, bool wide) {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h) load32<true>(p + h * (32 / sizeof(T)), r[h], wide);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[h][i] = 0;
+    }
+    // What they hold, negated (encode16 takes that).
+    __device__ __forceinline__ void negatives(float (&v)[kVec]) const {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (sizeof(T) == 4) {
+                    v[h * 8 + i] = __uint_as_float(r[h][i] ^ 0x80000000u);
+                } else {
+                    v[2 * i] = lo_of(r[0][i] ^ 0x8000u);
+                    v[2 * i + 1] = hi_of(r[0][i] ^ 0x80000000u);
+                }
+            }
+    }
+    // The sums with t's, rounded to the type.
+    __device__ __forceinline__ void add(const Raw& t) {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r[h][i] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(r[h][i]) + __uint_as_float(t.r[h][i]))
+                                         : pack2(lo_of(r[h][i]) + lo_of(t.r[h][i]), hi_of(r[h][i]) + hi_of(t.r[h][i]));
+    }
+    __device__ __forceinline__ void store(T* p, bool wide) const {
+#pragma unroll
+        for (int h = 0; h < (int)(kVec * sizeof(T) / 32); ++h) store32(p + h * (32 / sizeof(T)), r[h], wide);
+    }
+    __device__ __forceinline__ float at(int j) const {
+        if (sizeof(T) == 4) return __uint_as_float(r[j / 8][j % 8]);
+        return j % 2 ? hi_of(r[0][j / 2]) : lo_of(r[0][j / 2]);
+    }
+};
 
 inline bool aligned32(const void* a, const void* b = nullptr, const void* c = nullptr, const void* d = nullptr) {
     return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c) |
@@ -151,7 +192,7 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 // that is a float32, like the borders between codes, comes out as itself.)  Given are the values'
 // negatives, nv: the remainder q scale - v, taken from the quotient, keeps the sign of
 // -0, and two values an instruction have no modifier for a sign.  32768 x 7168 bf16
-// rows 119 us, with divisions 158.
+// rows 117 us, with divisions 158.
 __device__ __forceinline__ uint4 encode16(const float (&nv)[kVec], float& scale) {
     float top = max_abs3(nv[0], nv[1], nv[2]);
 #pragma unroll
