@@ -477,9 +477,10 @@ def expert_mlp_fp8_backward(d_down, expert_offsets, weights, buf):
 
     def coded(g):
         cols = g.shape[1]
+        blocks = _ep.scale_blocks(cols)
         return _ep.ep_quantize_blocks(
             g, expert_offsets=expert_offsets, q=buf.gq[:rows * cols].view(rows, cols),
-            scales=buf.gs[:rows * _ep.scale_blocks(cols)].view(rows, -1), **kw)
+            scales=buf.gs[:rows * blocks].view(rows, blocks), **kw)
     _ep.ep_expert_matmul_fp8(*coded(d_down), weights.down_t, weights.down_t_scales, expert_offsets,
                              out=buf.d_h, status=buf.d_h_status, **kw)
     _ep.ep_swiglu_backward(buf.d_h, buf.upq, buf.ups, expert_offsets=expert_offsets, d_x=buf.d_up,
