@@ -536,12 +536,14 @@ def expert_layer_fp8(x, logits, rank_offsets, weights, buf, score=_ep.EP_SCORE_S
                      groups=1, topk_groups=None, group_top=2, renorm=True, scale=1.0,
                      expert_map=None):
     """x bf16 [N, H], or (codes uint8 [N, H], scales) as ep_rms_norm and
-    ep_quantize_blocks write them; logits [N, E] -> buf.comb bf16 [N, H], on the
-    current stream.  The gate's arguments are ep_gate_topk's.  buf.check() tells, once
-    the step is done, that both products completed."""
-    E = logits.shape[1]
+    ep_quantize_blocks write them (N rows at least); logits [N, E] -> buf.comb bf16
+    [N, H], on the current stream.  The gate's arguments are ep_gate_topk's.
+    buf.check() tells, once the step is done, that both products completed."""
+    N, E = logits.shape
     K = buf.idx.shape[1]
     lay, off, mlp = buf.lay, buf.lay.expert_offsets, buf.mlp
+    if isinstance(x, (tuple, list)) and x[0].shape[0] < N:
+        raise _ep.EPError(f"expert_layer_fp8: {x[0].shape[0]} rows of codes for {N} tokens")
     _ep.ep_gate_topk(logits, K, score, bias=bias, groups=groups, topk_groups=topk_groups,
                      group_top=group_top, renorm=renorm, scale=scale, expert_map=expert_map,
                      topk_idx=buf.idx, topk_w=buf.wt, picks=buf.picks)

@@ -55,3 +55,21 @@ def test_experts_forward_and_backward_of_any_number_of_rows(calls, rows):
         ("gradient", (rows, INNER), (rows, 2 * INNER), (rows, 2 * INNER)),
         ("codes", (rows, 2 * INNER), (rows, 3)),
         ("product", (rows, 2 * INNER), (rows, 3), (rows, H))]
+
+
+@pytest.mark.parametrize("cap", [0, 8])
+def test_layer_refuses_codes_of_fewer_rows_than_tokens(calls, cap):
+    """A token without its row would count as zeros; rows behind the last token are none's."""
+    N = 5
+    buf = pl.make_layer_buffers_fp8(N, E, K, H, INNER, 1, cap, device="cpu")
+    logits, ro = torch.zeros((N, E)), torch.tensor([0, N])
+
+    def layer(rows):
+        x = torch.zeros((rows, H), dtype=torch.uint8), torch.zeros((rows, 2))
+        return pl.expert_layer_fp8(x, logits, ro, WEIGHTS, buf)
+    for rows in (0, N - 1):
+        with pytest.raises(ep.EPError, match=f"{rows} rows of codes for {N} tokens"):
+            layer(rows)
+    assert calls == []  # refused before anything is launched
+    for rows in (N, N + 3):
+        assert layer(rows) is buf.comb
