@@ -451,6 +451,15 @@ def ep_quantize_rows(x, act=EP_ACT_NONE, expert_offsets=None, layout=EP_LAYOUT_C
     return q, scales
 
 
+def _sources(row_src, expert_offsets):
+    """(pointer, length) of row_src.  An empty tensor has no memory, and a null pointer would
+    say that there is no row_src: it gets an address that is never read."""
+    if row_src is None:
+        return None, 0
+    n = row_src.numel()
+    return _dev(row_src, torch.int32, "row_src") or expert_offsets.data_ptr(), n
+
+
 def ep_expert_matmul(x, x_scales, w, w_scales, expert_offsets, layout=EP_LAYOUT_CONTIG, cap=0,
                      row_src=None, out=None, out_dtype=torch.bfloat16, status=None, stream=None):
     """Every expert's rows times its weights: x int8 [x_rows, Kd], x_scales
@@ -474,7 +483,7 @@ def ep_expert_matmul(x, x_scales, w, w_scales, expert_offsets, layout=EP_LAYOUT_
         _dev(x_scales, torch.float32, "x_scales", (x_rows,)), x_rows, _dev(w, torch.int8, "w"),
         _dev(w_scales, torch.float32, "w_scales", (E, Nc)), E, Nc, Kd,
         _dev(expert_offsets, torch.int32, "expert_offsets", (E + 1,)), layout, cap, rows,
-        _opt(row_src, torch.int32, "row_src"), 0 if row_src is None else row_src.numel(), dt,
+        *_sources(row_src, expert_offsets), dt,
         _dev(out, out.dtype, "out"), _opt(status, torch.int32, "status", (1,)), _stream(stream)))
     return out
 
@@ -601,7 +610,7 @@ def ep_expert_matmul_fp8(x, x_scales, w, w_scales, expert_offsets, layout=EP_LAY
         _codes(w, "w"),
         _dev(w_scales, torch.float32, "w_scales", (E, scale_blocks(Nc), scale_blocks(Kd))), E, Nc,
         Kd, _dev(expert_offsets, torch.int32, "expert_offsets", (E + 1,)), layout, cap, rows,
-        _opt(row_src, torch.int32, "row_src"), 0 if row_src is None else row_src.numel(), dt,
+        *_sources(row_src, expert_offsets), dt,
         _dev(out, out.dtype, "out"), _opt(status, torch.int32, "status", (1,)), _stream(stream)))
     return out
 

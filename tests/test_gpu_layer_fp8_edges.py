@@ -44,3 +44,38 @@ def test_layer_without_tokens(cap, coded):
     d = torch.zeros_like(buf.mlp.down)
     pl.expert_mlp_fp8_backward(d, buf.lay.expert_offsets, w, buf.mlp)
     buf.check()
+
+
+@pytest.mark.parametrize("product", ["fp8", "int8"])
+def test_an_empty_row_src_reads_nothing(product):
+    """Not even where x has as many rows as the output."""
+    E, cap, Nc, Kd = 2, 3, 48, 64
+    g = torch.Generator().manual_seed(2)
+    x = torch.randint(1, 9, (E * cap, Kd), generator=g)
+    w = torch.randint(1, 9, (E, Nc, Kd), generator=g)
+    offs = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    src = torch.empty((0,), dtype=torch.int32, device="cuda")
+    kw = dict(layout=ep.EP_LAYOUT_MASKED, cap=cap, row_src=src)
+    out = torch.full((E * cap, Nc), -7.0, device="cuda")
+    if product == "fp8":
+        x, w = (t.float().to(torch.float8_e4m3fn).cuda() for t in (x, w))
+        ep.ep_expert_matmul_fp8(x, torch.ones((E * cap, 1), device="cuda"), w,
+                                torch.ones((E, 1, 1), device="cuda"), offs, out=out, **kw)
+    else:
+        x, w = (t.to(torch.int8).cuda() for t in (x, w))
+        ep.ep_expert_matmul(x, torch.ones(E * cap, device="cuda"), w,
+                            torch.ones((E, Nc), device="cuda"), offs, out=out, **kw)
+    held = torch.tensor([True, True, False] * E)
+    assert (out.cpu()[held] == 0).all() and (out.cpu()[~held] == -7.0).all()
+
+
+@pytest.mark.parametrize("cap", [0, 4])
+def test_integer_layer_without_tokens(cap):
+    E, K, H, inner = 4, 2, 256, 128
+    up = torch.ones((E, 2 * inner, H), dtype=BF, device="cuda")
+    w = pl.quantize_expert_weights(up, torch.ones((E, H, inner), dtype=BF, device="cuda"))
+    buf = pl.make_layer_buffers(0, E, K, H, inner, 1, cap)
+    ro = torch.zeros(2, dtype=torch.int32, device="cuda")
+    x = torch.zeros((0, H), dtype=BF, device="cuda")
+    assert pl.expert_layer(x, torch.zeros((0, E), device="cuda"), ro, w, buf).shape == (0, H)
+    buf.check()
