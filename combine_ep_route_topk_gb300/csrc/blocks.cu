@@ -23,13 +23,17 @@ using namespace rows;
 
 constexpr int kThreads = 256;
 
-// 2^(x log2 e) and 1 / x by the hardware's instructions: each off by about 2^-22,
-// relative, against the 2^-4 of a code's rounding and the 2^-8 of a bf16's.
-__device__ __forceinline__ float fast_exp(float x) {
+// exp of a row's value.  Float32 rows: CUDA's own, within two last places.  bf16 rows: the
+// hardware's 2^(x log2 e), off by some 2^-22 and, for the product's rounding, |x| 2^-23,
+// relative, far below the 2^-8 of the value that it is taken of and of a bf16's rounding.
+template <typename T>
+__device__ __forceinline__ float exp_of(float x) {
+    if constexpr (sizeof(T) == 4) return expf(x);
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
     return e;
 }
+// 1 / x by the hardware's instruction, within a last place (0 below 2^-126).
 __device__ __forceinline__ float fast_rcp(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, !KEEP ? 6 : sizeof(T) == 2 ? 5 : 4) 
     if constexpr (SWIGLU) {
         if constexpr (KEEP) g.negatives(v);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = v[j] * fast_rcp(1.0f + fast_exp(v[j])) * u.at(j);
+        for (int j = 0; j < kVec; ++j) v[j] = v[j] * fast_rcp(1.0f + exp_of<T>(v[j])) * u.at(j);
     }
     const uint4 codes = encode16(v, scale);
     if (on) {
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluGradArg
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
         // s and 1 - s from exp(-|g|), so that neither cancels or overflows
-        const float e = fast_exp(-fabsf(g[j])), big = fast_rcp(1.0f + e), small = e * big;
+        const float e = exp_of<T>(-fabsf(g[j])), big = fast_rcp(1.0f + e), small = e * big;
         const float s = g[j] >= 0.0f ? big : small, rest = g[j] >= 0.0f ? small : big;
         const float slope = s * fmaf(g[j], rest, 1.0f);
         const float up = d[j] * g[j] * s;

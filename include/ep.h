@@ -479,8 +479,9 @@ ep_status_t ep_expert_matmul(const int8_t* x, const float* x_scales, int32_t x_r
  * ep_expert_matmul_fp8 reads; an addition of this library.
  *   v      = x (EP_ACT_NONE), or silu(x[:cols]) * x[cols:] (EP_ACT_SWIGLU, x
  *            rows of 2*cols: the experts' first product, gate half first), in
- *            float32; exp and 1 / x are the hardware's (some 2^-22 off, results
- *            below some 1e-35 may be 0).
+ *            float32: within 2^-20 of its value; of bf16 rows, whose exp is
+ *            the hardware's instruction, 2^-20 + |gate| 2^-23.  A sigmoid below
+ *            2^-126 (a gate below -87) may count as 0.
  *   scale  = max|v| / 448 over a block of 128 columns (a row's last block may be
  *            shorter); 1 where that quotient is 0.  code = E4M3(v / scale),
  *            rounded to nearest even; quotients by IEEE division, so that
@@ -516,7 +517,8 @@ ep_status_t ep_dequantize_blocks(const uint8_t* q, const float* scales, int32_t 
  * ep_swiglu_backward -- gradient of silu(g) * u with respect to x = (g, u), from
  * x itself or from its 8-bit checkpoint:
  *   d_g = d_out * u * s * (1 + g * (1 - s)),  d_u = d_out * g * s,
- *   s = 1 / (1 + exp(-g)), in float32 with ep_quantize_blocks's exp and 1 / x,
+ *   s = 1 / (1 + exp(-g)), in float32 (within 2^-19 of the terms' magnitudes,
+ *   for bf16 rows 2^-19 + |g| 2^-23; a sigmoid below 2^-126 may count as 0),
  *   rounded once to the rows' type.
  *   d_out  [rows, cols] float32 or bf16 (dtype).
  *   x      x_scales NULL: rows [rows, 2*cols] of the same type.  Else: uint8
