@@ -259,7 +259,7 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
             // that lie together, in boxes of 32.  Rows anywhere (row_src) are fetched 4 a copy,
             // half of them by each warp.  Such copies take some 55 cycles each wherever they
             // are issued, 128 rows 0.93 us: 1024 rows an expert 1.64 ms, rows that lie
-            // together 0.81.  (16-byte copies by threads and the fence that orders them
+            // together 0.77.  (16-byte copies by threads and the fence that orders them
             // before the MMAs: 1.43 ms, but 0.85 us a step however few the rows, 57 us for
             // one token's 8 rows where this takes 45.) ----
             const bool gather = a.row_src != nullptr, weights = warp == kTmaWarp;
@@ -303,7 +303,7 @@ matmul_fp8_kernel(MatmulArgs a, const __grid_constant__ CUtensorMap w_map, const
                 ok = mbar_wait_warp(sh, &sh->done[i % kStages], i / kStages & 1);
             if (!ok && lane == 0) drain_copies<kStages>(sh->full, c);
         } else if (warp == kMmaWarp) {
-            // ---- MMA: one elected thread ----
+            // ---- MMA: the whole warp, an elected lane of which issues ----
             const uint64_t desc0 = operand_desc(smem_u32(s_stage));
             // float32 accumulators, E4M3 operands, both K-major
             constexpr uint32_t idesc = 1u << 4 | (uint32_t)(S::BN >> 3) << 17 | (uint32_t)(S::TN >> 4) << 24;
@@ -585,7 +585,12 @@ cudaError_t launch_expert_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {
     // the tiles and more weights in flight.  Us with 256 channels and with 128, 32 experts of
     // 4096 x 7168: 64 rows each 160, 154; 128 rows 188, 213; 1024 rows 772, 1085; one
     // expert of 4096 x 4096, 512 rows (64 wide tiles) 27, 20.  Rows fetched by 4 cost a
-    // step more: 32 rows each 164, 195.  A capacity counts half.  Rows of out off 16 bytes are
+    // step more: 32 rows each 164, 195.  A capacity counts half, as nothing here knows how
+    // many rows it holds.  Other sizes, with and without row_src: the rule's shape is within
+    // 8 % of the better one at 8 to 512 rows each of 32 experts of 7168 x 2048 and x 512 and of
+    // 128 of 2880 x 1440 (most at 96 rows of the last, wide 117 and narrow 111), and where a
+    // capacity of 64 to 1024 holds 1 to 64 rows (4096 x 7168, one row each: wide 171 and
+    // narrow 165).  Rows of out off 16 bytes are
     // narrow tiles' alone: the way through shared memory costs the wide ones registers that
     // their steps need (prefill 0.86 ms instead of 0.77).  32 experts of 4100 x 7168, 1024 rows
     // each: 1.23 ms, wide tiles with each thread's own stores 1.79.

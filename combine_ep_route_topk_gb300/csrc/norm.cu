@@ -18,7 +18,10 @@
 // Bound by those bytes, but where codes alone are written by instructions.  32768 x
 // 7168 bf16: y, codes and the residual 311 us = 6.8 TB/s, y alone 141 = 6.7, codes
 // alone 152 = 4.7 (70 % of the issue slots); the gradient with the residual's 284 us =
-// 6.6 TB/s.  16384 x 7168 float32: 285 and 262 us = 7.0 and 7.2 TB/s.
+// 6.6 TB/s.  16384 x 7168 float32: 285 and 262 us = 7.0 and 7.2 TB/s.  Gradients of rows
+// past 8192 columns hold two vectors a thread, of which 128 registers spill a part (88 bytes
+// a thread for bf16, 468 for float32): 8192 x 16384 with the residual's 195 us = 5.5 TB/s in
+// bf16, 557 = 3.9 in float32.
 #include <algorithm>
 #include <atomic>
 
